@@ -17,6 +17,8 @@ Calls (all asynchronous on the current stream):
   tree_prepare      token-tree layout: depths, positions, cache slots, ancestor masks
   block_attn_paged(tree_mask=...)  tree attention (block row sees its ancestors)
   tree_accept       lossless tree acceptance walk (stochastic or greedy)
+  block_table_update  block tables grown / shrunk from request lengths, slots of new tokens
+  token_sample      logits -> p (temperature, top-k, top-p, min-p) and tokens from given uniforms
 """
 from __future__ import annotations
 
@@ -39,7 +41,8 @@ EXPORTS = ("bdsa_status_string", "bdsa_version", "bdsa_prepare_block",
            "bdsa_block_attn_paged_append", "bdsa_spec_accept_workspace_bytes",
            "bdsa_spec_accept", "bdsa_spec_accept_noalloc", "bdsa_idlm_prepare",
            "bdsa_idlm_accept", "bdsa_kv_materialize_workspace_bytes", "bdsa_kv_materialize",
-           "bdsa_tree_prepare", "bdsa_block_attn_paged_tree", "bdsa_tree_accept")
+           "bdsa_tree_prepare", "bdsa_block_attn_paged_tree", "bdsa_tree_accept",
+           "bdsa_block_table_update", "bdsa_token_sample")
 
 _lib = None
 
@@ -101,6 +104,12 @@ def lib() -> ctypes.CDLL:
     L.bdsa_tree_accept.argtypes = [P, P, P, i64, i64, P, P, i32, i32, i32, P, P, P, P, P, i32,
                                    P, P]
     L.bdsa_tree_accept.restype = i32
+    L.bdsa_block_table_update.argtypes = [P, P, P, P, P, i32, i32, i32, i32, P, P, P, P, P, P, P,
+                                          i64, P, P]
+    L.bdsa_block_table_update.restype = i32
+    L.bdsa_token_sample.argtypes = [P, i32, i64, i64, P, P, P, P, P, i32, i32, i32, P, P, i64,
+                                    i64, i32, P, P]
+    L.bdsa_token_sample.restype = i32
     _lib = L
     return L
 
@@ -453,3 +462,118 @@ def tree_accept(block_ids, parent, p, u, seq_lens, *, p_strides=None, V: int | N
                                 _ptr(out["new_seq_lens"]), sms, _ptr(dev_status), _stream(dev))
     _check("bdsa_tree_accept", st)
     return out
+
+
+# ---------------------------------------------------------------------------
+def _arg(t, name: str, dtype, shape, device):
+    """A contiguous CUDA tensor of this dtype and shape on `device`, or None."""
+    if t is None:
+        return None
+    _dev(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _status_arg(t, device):
+    return None if t is None else _arg(t, "dev_status", torch.int32, (1,), device)
+
+
+TABLE_KEYS = ("owned", "free_state", "cu_tokens", "slot_map", "positions")
+
+
+def block_table_update(seq_lens, new_lens, owned, block_table, free_pages, free_state, *,
+                       page_size: int, total_tokens: int, shared=None, out=None,
+                       dev_status=None):
+    """bdsa_block_table_update.  seq_lens, new_lens, owned (and shared) int32 [bs];
+    block_table int32 [bs, max_pages] and the ring free_pages int32 [num_pages] are
+    updated in place; free_state int32 [2] = (head, count) of the ring.
+
+    total_tokens is the room for the new tokens (at least their number).  Returns
+    a dict of int32 tensors: owned [bs], free_state [2], cu_tokens [bs + 1],
+    slot_map and positions [total_tokens]; pass it back as `out` to reuse them
+    (owned and free_state must not be the inputs' memory).
+    """
+    _dev(block_table, "block_table", torch.int32)
+    dev = block_table.device
+    bs, max_pages = block_table.shape
+    i32 = torch.int32
+    if total_tokens < 0:
+        raise ValueError("total_tokens must be >= 0")
+    num_pages = _dev(free_pages, "free_pages", i32).numel()
+    ins = [_arg(t, n, i32, (bs,), dev) for t, n in
+           ((seq_lens, "seq_lens"), (new_lens, "new_lens"), (owned, "owned"), (shared, "shared"))]
+    if out is None:
+        pad = -total_tokens % 4  # slot_map and positions start on 16-byte boundaries
+        buf = torch.empty(2 * (total_tokens + pad) + 2 * bs + 3, dtype=i32, device=dev)
+        slot, _, pos, _, own, cu, state = buf.split([total_tokens, pad, total_tokens, pad, bs,
+                                                     bs + 1, 2])
+        out = dict(owned=own, free_state=state, cu_tokens=cu, slot_map=slot, positions=pos)
+    outs = [_arg(out[k], k, i32, n, dev) for k, n in
+            zip(TABLE_KEYS, ((bs,), (2,), (bs + 1,), (total_tokens,), (total_tokens,)))]
+    with torch.cuda.device(dev):
+        st = lib().bdsa_block_table_update(
+            *ins, block_table.data_ptr(), max_pages, num_pages, bs, int(page_size),
+            _arg(free_pages, "free_pages", i32, (num_pages,), dev),
+            _arg(free_state, "free_state", i32, (2,), dev), *outs, int(total_tokens),
+            _status_arg(dev_status, dev), _stream(dev))
+    _check("bdsa_block_table_update", st)
+    return out
+
+
+_LOGIT_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _rows(t, name: str):
+    """Strides (r, i) of a [bs, B, V] CUDA tensor whose last dimension is dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have shape [bs, B, V], got {tuple(t.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t.stride(0), t.stride(1)
+
+
+def token_sample(logits, u=None, *, temperature=None, top_k=None, top_p=None, min_p=None,
+                 want_probs: bool = False, probs=None, tokens=None, dev_status=None,
+                 sms: int = 0):
+    """bdsa_token_sample.  logits [bs, B, V] fp32, bf16 or fp16 (rows dense, any
+    strides between them); u fp32 [bs, B] uniforms in [0, 1); temperature, top_p,
+    min_p fp32 [bs] and top_k int32 [bs], each None for off.
+
+    Returns (tokens int32 [bs, B], or None without u; probs fp32 [bs, B, V], or
+    None unless want_probs or a tensor to fill is given).  probs is what the
+    acceptance calls take as p and q.
+    """
+    lsr, lsi = _rows(logits, "logits")
+    if logits.dtype not in _LOGIT_DTYPES:
+        raise TypeError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    bs, B, V = logits.shape
+    dev, f32, i32 = logits.device, torch.float32, torch.int32
+    if u is None and tokens is not None:
+        raise ValueError("tokens are drawn from u")
+    if u is not None and tokens is None:
+        tokens = torch.empty((bs, B), dtype=i32, device=dev)
+    if probs is None and want_probs:
+        probs = torch.empty((bs, B, V), dtype=f32, device=dev)
+    psr = psi = 0
+    if probs is not None:
+        psr, psi = _rows(probs, "probs")
+        if probs.dtype != f32 or tuple(probs.shape) != (bs, B, V) or probs.device != dev:
+            raise ValueError(f"probs must be float32 {(bs, B, V)} on {dev}")
+    if tokens is None and probs is None:
+        raise ValueError("nothing to do: neither u nor probs")
+    with torch.cuda.device(dev):
+        st = lib().bdsa_token_sample(
+            logits.data_ptr(), _LOGIT_DTYPES[logits.dtype], lsr, lsi,
+            _arg(u, "u", f32, (bs, B), dev), _arg(temperature, "temperature", f32, (bs,), dev),
+            _arg(top_k, "top_k", i32, (bs,), dev), _arg(top_p, "top_p", f32, (bs,), dev),
+            _arg(min_p, "min_p", f32, (bs,), dev), bs, B, V,
+            _arg(tokens, "tokens", i32, (bs, B), dev),
+            None if probs is None else probs.data_ptr(), psr, psi, sms,
+            _status_arg(dev_status, dev), _stream(dev))
+    _check("bdsa_token_sample", st)
+    return tokens, probs

@@ -31,6 +31,13 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
+// int32 ranges [a, a + n) and [b, b + n) share memory
+bool overlap(const int32_t *a, const int32_t *b, int64_t n) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    const uintptr_t len = static_cast<uintptr_t>(n) * sizeof(int32_t);
+    return a && b && x < y + len && y < x + len;
+}
+
 }  // namespace
 
 extern "C" {
@@ -412,6 +419,99 @@ int32_t bdsa_tree_accept(const int32_t *block_ids, const int32_t *parent, const 
     a.new_seq_lens = new_seq_lens;
     a.dev_status = dev_status;
     return bdsa::launch_tree_accept(a, static_cast<cudaStream_t>(stream));
+}
+
+int32_t bdsa_block_table_update(const int32_t *seq_lens, const int32_t *new_lens,
+                                const int32_t *owned, const int32_t *shared,
+                                int32_t *block_table, int32_t max_pages_per_req,
+                                int32_t num_pages, int32_t bs, int32_t page_size,
+                                int32_t *free_pages, const int32_t *free_state,
+                                int32_t *owned_out, int32_t *free_state_out, int32_t *cu_tokens,
+                                int32_t *slot_map, int32_t *positions, int64_t max_tokens,
+                                int32_t *dev_status, void *stream) {
+    if (bs < 0 || page_size < 1 || max_pages_per_req < 1 || num_pages < 1 || max_tokens < 0)
+        return BDSA_INVALID_ARG;
+    if (bs > BDSA_TABLE_MAX_REQUESTS || (int64_t)num_pages * page_size > INT32_MAX ||
+        max_tokens > INT32_MAX)
+        return BDSA_UNSUPPORTED;
+    if (!free_state || !free_state_out || !cu_tokens) return BDSA_INVALID_ARG;
+    if (bs > 0 && (!seq_lens || !new_lens || !owned || !block_table || !free_pages || !owned_out))
+        return BDSA_INVALID_ARG;
+    // the inputs are read while the outputs are written
+    if (overlap(owned, owned_out, bs) || overlap(free_state, free_state_out, 2) ||
+        overlap(seq_lens, owned_out, bs) || overlap(new_lens, owned_out, bs))
+        return BDSA_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(free_pages, 4) || !aligned(slot_map, 4) ||
+        !aligned(positions, 4))
+        return BDSA_MISALIGNED;
+    bdsa::TableArgs a;
+    a.seq_lens = seq_lens;
+    a.new_lens = new_lens;
+    a.owned = owned;
+    a.shared = shared;
+    a.block_table = block_table;
+    a.free_pages = free_pages;
+    a.free_state = free_state;
+    a.owned_out = owned_out;
+    a.free_state_out = free_state_out;
+    a.cu_tokens = cu_tokens;
+    a.slot_map = slot_map;
+    a.positions = positions;
+    a.max_tokens = (slot_map || positions) ? max_tokens : 0;
+    a.max_pages = max_pages_per_req;
+    a.num_pages = num_pages;
+    a.bs = bs;
+    a.page_size = page_size;
+    a.vec = aligned(slot_map, 16) && aligned(positions, 16);
+    a.dev_status = dev_status;
+    return bdsa::launch_block_table(a, bdsa::device_num_sms(0),
+                                    static_cast<cudaStream_t>(stream));
+}
+
+int32_t bdsa_token_sample(const void *logits, int32_t dtype, int64_t l_stride_r,
+                          int64_t l_stride_i, const float *u, const float *temperature,
+                          const int32_t *top_k, const float *top_p, const float *min_p,
+                          int32_t bs, int32_t B, int32_t V, int32_t *tokens, float *probs,
+                          int64_t p_stride_r, int64_t p_stride_i, int32_t num_sms,
+                          int32_t *dev_status, void *stream) {
+    if (bs < 0 || B < 1 || V < 1 || l_stride_r < 0 || l_stride_i < 0 || p_stride_r < 0 ||
+        p_stride_i < 0 || dtype < BDSA_F32 || dtype > BDSA_F16)
+        return BDSA_INVALID_ARG;
+    if (V > (1 << 21) || (int64_t)bs * B > (1 << 26)) return BDSA_UNSUPPORTED;
+    if (bs == 0) return BDSA_OK;
+    if (!logits || (!tokens && !probs) || (tokens && !u)) return BDSA_INVALID_ARG;
+    // rows of the output must not overlap one another: one index outside the other
+    if (probs) {
+        const bool i_in = (B == 1 || p_stride_i >= V) &&
+                          (bs == 1 || p_stride_r >= (B > 1 ? (B - 1) * p_stride_i : 0) + V);
+        const bool r_in = (bs == 1 || p_stride_r >= V) &&
+                          (B == 1 || p_stride_i >= (bs > 1 ? (bs - 1) * p_stride_r : 0) + V);
+        if (!i_in && !r_in) return BDSA_INVALID_ARG;
+    }
+    if (!aligned(logits, dtype == BDSA_F32 ? 4 : 2) || !aligned(probs, 4) || !aligned(tokens, 4) ||
+        !aligned(u, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
+        !aligned(min_p, 4))
+        return BDSA_MISALIGNED;
+    bdsa::SampleArgs a;
+    a.logits = logits;
+    a.lsr = l_stride_r;
+    a.lsi = l_stride_i;
+    a.u = u;
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.bs = bs;
+    a.B = B;
+    a.V = V;
+    a.tokens = tokens;
+    a.probs = probs;
+    a.psr = p_stride_r;
+    a.psi = p_stride_i;
+    a.dev_status = dev_status;
+    a.ncta = a.slice = 0;
+    return bdsa::launch_token_sample(a, dtype, bdsa::device_num_sms(num_sms),
+                                     static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

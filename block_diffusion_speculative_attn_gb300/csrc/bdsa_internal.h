@@ -134,6 +134,40 @@ struct KvMatArgs {
 size_t kvmat_workspace_bytes(int bs, int B, int H);
 int launch_kv_materialize(const KvMatArgs &a, cudaStream_t stream);
 
+// ---------------------------------------------------------------- block tables
+struct TableArgs {
+    const int32_t *seq_lens, *new_lens, *owned, *shared;  // [bs]; shared may be null
+    int32_t *block_table;                                 // [bs, max_pages]
+    int32_t *free_pages;                                  // ring of num_pages cells
+    const int32_t *free_state;                            // {head, count}
+    int32_t *owned_out, *free_state_out, *cu_tokens;      // [bs], {head, count}, [bs + 1]
+    int32_t *slot_map, *positions;                        // [max_tokens] each, or null
+    int64_t max_tokens;
+    int max_pages, num_pages, bs, page_size;
+    int vec;  // slot_map and positions are 16-byte aligned
+    int32_t *dev_status;
+};
+
+int launch_block_table(const TableArgs &a, int num_sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- sampling
+struct SampleArgs {
+    const void *logits;                  // row (r, i) at r * lsr + i * lsi elements
+    int64_t lsr, lsi;
+    const float *u;                      // [bs, B], or null without tokens
+    const float *temperature;            // [bs] each, or null (off)
+    const int32_t *top_k;
+    const float *top_p, *min_p;
+    int bs, B, V;
+    int32_t *tokens;                     // [bs, B], or null
+    float *probs;                        // row (r, i) at r * psr + i * psi, or null
+    int64_t psr, psi;
+    int32_t *dev_status;
+    int ncta, slice;                     // set by the launcher
+};
+
+int launch_token_sample(const SampleArgs &a, int dtype, int num_sms, cudaStream_t stream);
+
 // ---------------------------------------------------------------- misc
 int device_num_sms(int requested);
 

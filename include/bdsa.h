@@ -498,6 +498,104 @@ int32_t bdsa_tree_accept(const int32_t *block_ids, const int32_t *parent, const 
                          int32_t *bonus_id, int32_t *new_seq_lens, int32_t num_sms,
                          int32_t *dev_status, void *stream);
 
+/* ------------------------------------------------------------------------ */
+/* bdsa_block_table_update
+ *
+ * "From DFlash to dLLM Self-Spec (II): SGLang Spec V2", section 2.3.5 (the
+ * caller reserves pages for at least L_r + B tokens before a step): grows and
+ * shrinks the block tables that every other call reads, from request lengths,
+ * on the GPU, and lists the cache slot of every new token.
+ *
+ * seq_lens [bs] (L_r, tokens already in the cache), new_lens [bs] (n_r, tokens
+ * about to be written), owned [bs] (pages in the request's block-table row),
+ * shared [bs] or NULL (leading pages of the row that belong to somebody else,
+ * such as a shared prefix: never released), block_table [bs, max_pages_per_req]
+ * (updated in place), free_pages [num_pages] (a ring of free page ids, updated
+ * in place), free_state {head, count}: the free pages are
+ * free_pages[(head + i) % num_pages], i < count.  For request r
+ *   need  = ceil((L_r + n_r) / page_size)
+ *   need > owned: need - owned pages are popped from the head of the ring, in
+ *           request order, into entries [owned, need) of the row; a request
+ *           that the remaining pages do not cover, and every later one that
+ *           needs a page, gets none (dev_status reports it)
+ *   need < owned: entries [max(need, shared), owned) are pushed behind the
+ *           ring's tail, in request and page order, and become -1; they can be
+ *           popped from the next call on
+ *   owned_out[r] = the row's pages after that
+ *   cu_tokens[r] = n_0 + ... + n_{r-1}  (cu_tokens[bs] = the total)
+ *   token o < n_r, at t = cu_tokens[r] + o: positions[t] = L_r + o and
+ *   slot_map[t] = block_table[r, p / page_size] * page_size + p % page_size,
+ *   p = L_r + o (-1 where the row has no such page)
+ * and free_state_out = the ring's new {head, count}.  slot_map and positions
+ * (either may be NULL) hold max_tokens entries; entries past the total are left
+ * as they were, tokens past max_tokens are not written and reported.
+ * A request with a negative length, L_r + n_r past 2^31 - 1, owned outside
+ * [0, max_pages_per_req], a negative shared, or a need above max_pages_per_req keeps its row and is
+ * reported (slots and positions -1, unless only shared or the need is wrong); a
+ * popped id outside the pool becomes -1 and is reported.  A free_state outside the
+ * ring pops and pushes nothing and is passed on; when owned and free pages
+ * together exceed num_pages nothing is pushed (both reported).
+ * Outputs must not overlap inputs: owned_out and free_state_out are memory of
+ * their own.  With the same owned and free_state the call repeats itself (pops
+ * leave the ring's cells as they are) as long as nothing is released.
+ * Supported: 0 <= bs <= BDSA_TABLE_MAX_REQUESTS, any page_size >= 1,
+ * num_pages * page_size < 2^31.  One launch, no workspace.
+ */
+enum { BDSA_TABLE_MAX_REQUESTS = 16384 };
+
+int32_t bdsa_block_table_update(const int32_t *seq_lens, const int32_t *new_lens,
+                                const int32_t *owned, const int32_t *shared,
+                                int32_t *block_table, int32_t max_pages_per_req,
+                                int32_t num_pages, int32_t bs, int32_t page_size,
+                                int32_t *free_pages, const int32_t *free_state,
+                                int32_t *owned_out, int32_t *free_state_out, int32_t *cu_tokens,
+                                int32_t *slot_map, int32_t *positions, int64_t max_tokens,
+                                int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* bdsa_token_sample
+ *
+ * "From DFlash to dLLM Self-Spec (IV)", section 4.3.1 (acceptance compares the
+ * distributions p and q the tokens are drawn from) and "... (II)", section
+ * 2.2.3 (the draft pass draws the mask slots' tokens): turns logits into those
+ * distributions and draws from them, with given uniforms.
+ *
+ * For row (r, i), logits l (V of them, at r * l_stride_r + i * l_stride_i
+ * elements of `dtype`), and request r's temperature T, top_k k, top_p p and
+ * min_p m (each [bs]; a NULL array switches it off):
+ *   w_x = exp((l_x - max l) / T); order: l descending, index ascending
+ *   n_k = k if 0 < k < V, else V
+ *   n_p = the shortest prefix of the first n_k whose weight is at least p times
+ *         theirs, at least one (p >= 1 or NaN: n_k)
+ *   n_m = the number of w_x >= m (m <= 0 or NaN: V)
+ *   kept: the first max(1, min(n_k, n_p, n_m)) of the order
+ *   probs[r, i, x] = w_x / S on the kept x, 0 elsewhere (S their weight)
+ *   tokens[r, i] = the smallest kept x with the kept weight of indices <= x
+ *         above u[r, i] * S
+ * T = 0 is greedy: the first largest logit alone (T < 1e-30 otherwise acts as
+ * 1e-30).  NaN logits count as -inf; -inf logits are never kept with weight; if
+ * the largest is +inf, the +inf logits share the distribution equally.  A row
+ * without a logit above -inf, or with a negative, NaN or infinite T, gets token
+ * -1 and zero probs and is reported (BDSA_DEVICE_OUT_OF_RANGE).  u outside
+ * [0, 1) is clamped (NaN: 0).
+ * Arithmetic: weights to about 2^-39 of the largest, held and summed exactly as
+ * integers in units of 2^-41 of it (a weight below half a unit counts as zero
+ * in S and the cuts); probs carry two fp32 roundings.  The result does not
+ * depend on the grid.
+ * tokens ([bs, B]) or probs may be NULL, not both; u is needed for tokens.
+ * probs rows must not overlap.  Supported: V <= 2^21, bs * B <= 2^26; rows may
+ * start at any element.  One launch, no workspace; outputs must not overlap
+ * inputs.
+ */
+enum { BDSA_F32 = 0, BDSA_BF16 = 1, BDSA_F16 = 2 };
+
+int32_t bdsa_token_sample(const void *logits, int32_t dtype, int64_t l_stride_r,
+                          int64_t l_stride_i, const float *u, const float *temperature,
+                          const int32_t *top_k, const float *top_p, const float *min_p,
+                          int32_t bs, int32_t B, int32_t V, int32_t *tokens, float *probs,
+                          int64_t p_stride_r, int64_t p_stride_i, int32_t num_sms,
+                          int32_t *dev_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

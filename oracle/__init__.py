@@ -385,3 +385,131 @@ def tree_accept(block_ids, parent, p, u, seq_lens, *, p_strides=None, V=None, nt
                            _ptr(out["path"]), _ptr(out["out_tokens"]), _ptr(out["bonus_id"]),
                            _ptr(out["new_seq_lens"]), _ptr(out["flags"]), int(nthreads))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Serving operators around the step (numpy, fp64, one row or request at a time).
+
+def token_sample(logits, u=None, temperature=None, top_k=None, top_p=None, min_p=None):
+    """Filtered distributions and draws of one [bs, B, V] array of logits (any
+    float type; widened to fp64), parameters [bs] or None.
+
+    Returns (tokens [bs, B] int32, probs [bs, B, V] fp64, near [bs, B] bool):
+    `near` marks rows with a decision (cut or draw) within 1e-9 of its border.
+    """
+    x = np.asarray(logits).astype(np.float64)
+    bs, B, V = x.shape
+    tokens = np.full((bs, B), -1, np.int32)
+    probs = np.zeros((bs, B, V))
+    near = np.zeros((bs, B), bool)
+    for r in range(bs):
+        T = 1.0 if temperature is None else float(temperature[r])
+        if not (0.0 <= T < np.inf):
+            continue
+        for i in range(B):
+            l = np.where(np.isnan(x[r, i]), -np.inf, x[r, i])
+            m = l.max()
+            if m == -np.inf:
+                continue
+            order = np.argsort(-l, kind="stable")
+            if m == np.inf:
+                w = (l == np.inf).astype(np.float64)
+            elif T == 0.0:
+                w = (np.arange(V) == order[0]).astype(np.float64)
+            else:
+                w = np.exp((l - m) / max(T, 1e-30))
+            ws = w[order]
+            n = V
+            if top_k is not None and 0 < int(top_k[r]) < V:
+                n = int(top_k[r])
+            if top_p is not None and float(top_p[r]) < 1.0:
+                c = np.cumsum(ws[:n])
+                goal = float(top_p[r]) * c[-1]
+                near[r, i] |= bool((np.abs(c - goal) < 1e-9 * c[-1]).any())
+                n = 1 + int((c[:n - 1] < goal).sum())
+            if min_p is not None and float(min_p[r]) > 0.0:
+                near[r, i] |= bool((np.abs(ws - float(min_p[r])) < 1e-9 * float(min_p[r])).any())
+                n = min(n, int((ws >= float(min_p[r])).sum()))
+            kept = np.zeros(V, bool)
+            kept[order[:max(n, 1)]] = True
+            w = np.where(kept, w, 0.0)
+            c = np.cumsum(w)
+            probs[r, i] = w / c[-1]
+            if u is not None:
+                uu = float(u[r, i])
+                uu = 0.0 if not uu > 0.0 else min(uu, 1.0)
+                goal = uu * c[-1]
+                pos = np.flatnonzero(w > 0)
+                k = int(np.searchsorted(c[pos], goal, side="right"))
+                tokens[r, i] = pos[min(k, len(pos) - 1)]
+                near[r, i] |= bool((np.abs(c[pos] - goal) < 1e-9 * c[-1]).any()) and uu < 1.0
+    return tokens, probs, near
+
+
+def block_table_update(seq_lens, new_lens, owned, block_table, free_pages, free_state, page_size,
+                       max_tokens, shared=None):
+    """One allocation step, request by request.  Returns a dict: block_table,
+    free_pages, owned, free_state, cu_tokens, slot_map, positions (the last two
+    hold -7 past the total), n_bad (requests or tokens that could not be served)."""
+    table, ring = np.array(block_table, np.int64), np.array(free_pages, np.int64)
+    old = ring.copy()
+    bs, max_pages = table.shape
+    pool = len(ring)
+    head, count = (int(v) for v in free_state)
+    state_ok = 0 <= head < pool and 0 <= count <= pool
+    h, left = (head, count) if state_ok else (0, 0)
+    tail = h + left
+    own_out = np.array(owned, np.int64)
+    pushes, bad, stopped, slots, poss, cu = [], 0, False, [], [], [0]
+    for r in range(bs):
+        L, n, own = int(seq_lens[r]), int(new_lens[r]), int(owned[r])
+        sh = 0 if shared is None else int(shared[r])
+        wrong = L < 0 or n < 0 or L + n >= 2 ** 31 or own < 0 or own > max_pages
+        need = -(-(L + n) // page_size)
+        if wrong or sh < 0 or need > max_pages:
+            bad += 1
+        elif need > own:
+            if stopped or need - own > left:
+                stopped = True
+                bad += 1
+            else:
+                for j in range(own, need):
+                    pg = int(old[h % pool])
+                    if not 0 <= pg < pool:
+                        pg = -1
+                        bad += 1
+                    table[r, j] = pg
+                    h, left = h + 1, left - 1
+                own_out[r] = need
+        else:
+            pushes += [(r, j) for j in range(max(need, min(sh, own)), own)]
+        for o in range(max(n, 0)):
+            p = L + o
+            if wrong:
+                slots.append(-1)
+                poss.append(-1)
+                continue
+            pg = table[r, p // page_size] if p // page_size < own_out[r] else -1
+            ok = 0 <= pg < pool
+            bad += not ok
+            slots.append(int(pg) * page_size + p % page_size if ok else -1)
+            poss.append(p)
+        cu.append(cu[-1] + max(n, 0))
+    if state_ok and count + len(pushes) <= pool:
+        for k, (r, j) in enumerate(pushes):
+            ring[(tail + k) % pool] = table[r, j]
+            bad += not 0 <= table[r, j] < pool
+            table[r, j] = -1
+            own_out[r] -= 1
+        left += len(pushes)
+    elif pushes:
+        bad += 1
+    bad += not state_ok
+    bad += cu[-1] > max_tokens
+    out = [np.full(max_tokens, -7, np.int64) for _ in range(2)]
+    for dst, src in zip(out, (slots, poss)):
+        k = min(max_tokens, len(src))
+        dst[:k] = src[:k]
+    return dict(block_table=table, free_pages=ring, owned=own_out,
+                free_state=np.array([h % pool, left] if state_ok else [head, count]),
+                cu_tokens=np.array(cu), slot_map=out[0], positions=out[1], n_bad=int(bad))

@@ -1,0 +1,84 @@
+"""Host-side refusals of the serving operators (CPU: every call here fails its
+checks, or has nothing to do, before it reaches a CUDA API)."""
+import ctypes
+
+import pytest
+import torch
+
+import block_diffusion_speculative_attn_gb300 as bdsa
+
+A = 0x100000  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    from block_diffusion_speculative_attn_gb300 import build
+    build.build()
+    return bdsa.lib()
+
+
+def _table(L, **kw):
+    a = dict(seq=A, new=A + 0x1000, own=A + 0x2000, shared=None, bt=A, mp=4, np=8, bs=2, ps=16,
+             ring=A, state=A, own_out=A + 0x3000, state_out=A + 0x4000, cu=A, slot=A, pos=A,
+             mt=10)
+    a.update(kw)
+    return L.bdsa_block_table_update(a["seq"], a["new"], a["own"], a["shared"], a["bt"], a["mp"],
+                                     a["np"], a["bs"], a["ps"], a["ring"], a["state"],
+                                     a["own_out"], a["state_out"], a["cu"], a["slot"], a["pos"],
+                                     a["mt"], None, None)
+
+
+def test_table_refusals(L):
+    assert _table(L, bs=-1) == 1
+    assert _table(L, ps=0) == 1
+    assert _table(L, mp=0) == 1
+    assert _table(L, np=0) == 1
+    assert _table(L, mt=-1) == 1
+    for name in ("seq", "new", "own", "bt", "ring", "state", "own_out", "state_out", "cu"):
+        assert _table(L, **{name: None}) == 1, name
+    assert _table(L, own_out=A + 0x2000) == 1        # in place: read while written
+    assert _table(L, own_out=A + 0x2004) == 1        # overlapping
+    assert _table(L, state_out=A + 4) == 1
+    assert _table(L, bs=16385) == 2
+    assert _table(L, np=1 << 28, ps=16) == 2         # slots past int32
+    assert _table(L, mt=1 << 31) == 2
+    assert _table(L, slot=A + 2) == 3
+
+
+def _sample(L, **kw):
+    a = dict(l=A, dt=0, lsr=8000, lsi=1000, u=A, T=A, k=A, p=A, m=A, bs=4, B=8, V=1000, tok=A,
+             pr=A, psr=8000, psi=1000, sms=152)
+    a.update(kw)
+    return L.bdsa_token_sample(a["l"], a["dt"], a["lsr"], a["lsi"], a["u"], a["T"], a["k"],
+                               a["p"], a["m"], a["bs"], a["B"], a["V"], a["tok"], a["pr"],
+                               a["psr"], a["psi"], a["sms"], None, None)
+
+
+def test_sample_refusals(L):
+    assert _sample(L, bs=0) == 0
+    assert _sample(L, bs=-1) == 1
+    assert _sample(L, B=0) == 1
+    assert _sample(L, V=0) == 1
+    assert _sample(L, dt=3) == 1
+    assert _sample(L, dt=-1) == 1
+    assert _sample(L, lsi=-1) == 1
+    assert _sample(L, l=None) == 1
+    assert _sample(L, u=None) == 1                   # tokens need uniforms
+    assert _sample(L, tok=None, pr=None) == 1
+    assert _sample(L, psi=999) == 1                  # rows of probs overlap
+    assert _sample(L, psr=7999) == 1
+    assert _sample(L, psr=1000, psi=1000) == 1
+    assert _sample(L, psr=0) == 1
+    assert _sample(L, V=(1 << 21) + 1, psi=1 << 22, psr=1 << 26) == 2
+    assert _sample(L, bs=1 << 24, psr=0, bt=0) in (1, 2)
+    assert _sample(L, l=A + 2) == 3
+    assert _sample(L, l=A + 1, dt=1) == 3
+    assert _sample(L, pr=A + 2) == 3
+
+
+def test_python_checks_need_no_gpu():
+    i = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        bdsa.block_table_update(i, i, i, i.view(2, 2), i, i[:2], page_size=4, total_tokens=4)
+    with pytest.raises(ValueError):
+        bdsa.token_sample(torch.zeros(1, 1, 8), torch.zeros(1, 1))
