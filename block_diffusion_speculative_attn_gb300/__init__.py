@@ -16,12 +16,14 @@ Calls (all asynchronous on the current stream):
   kv_materialize    draft K/V of the committed rows (projection, K norm, RoPE, paged write)
   tree_prepare      token-tree layout: depths, positions, cache slots, ancestor masks
   block_attn_paged(tree_mask=...)  tree attention (block row sees its ancestors)
+  block_attn_paged(group_offsets=, prefix_lens=)  groups of requests share a prefix
   tree_accept       lossless tree acceptance walk (stochastic or greedy)
   block_table_update  block tables grown / shrunk from request lengths, slots of new tokens
   token_sample      logits -> p (temperature, top-k, top-p, min-p) and tokens from given uniforms
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -42,7 +44,8 @@ EXPORTS = ("bdsa_status_string", "bdsa_version", "bdsa_prepare_block",
            "bdsa_spec_accept", "bdsa_spec_accept_noalloc", "bdsa_idlm_prepare",
            "bdsa_idlm_accept", "bdsa_kv_materialize_workspace_bytes", "bdsa_kv_materialize",
            "bdsa_tree_prepare", "bdsa_block_attn_paged_tree", "bdsa_tree_accept",
-           "bdsa_block_table_update", "bdsa_token_sample")
+           "bdsa_block_table_update", "bdsa_token_sample",
+           "bdsa_block_attn_prefix_workspace_bytes", "bdsa_block_attn_paged_prefix")
 
 _lib = None
 
@@ -104,6 +107,12 @@ def lib() -> ctypes.CDLL:
     L.bdsa_tree_accept.argtypes = [P, P, P, i64, i64, P, P, i32, i32, i32, P, P, P, P, P, i32,
                                    P, P]
     L.bdsa_tree_accept.restype = i32
+    L.bdsa_block_attn_prefix_workspace_bytes.argtypes = [i32] * 8
+    L.bdsa_block_attn_prefix_workspace_bytes.restype = sz
+    L.bdsa_block_attn_paged_prefix.argtypes = [P, P, P, P, i32, i32, P, P, P, i32, i32, i32, i32,
+                                               i32, i32, i32, i32, f32, i32, P, P, P, sz, i32, P,
+                                               P]
+    L.bdsa_block_attn_paged_prefix.restype = i32
     L.bdsa_block_table_update.argtypes = [P, P, P, P, P, i32, i32, i32, i32, P, P, P, P, P, P, P,
                                           i64, P, P]
     L.bdsa_block_table_update.restype = i32
@@ -166,17 +175,32 @@ def block_attn_workspace_bytes(bs, B, Hq, Hkv, D, max_ctx_len, sms: int = 0) -> 
     return int(lib().bdsa_block_attn_workspace_bytes(bs, B, Hq, Hkv, D, max_ctx_len, sms))
 
 
+def block_attn_prefix_workspace_bytes(bs, B, Hq, Hkv, D, max_ctx_len, num_groups,
+                                      sms: int = 0) -> int:
+    return int(lib().bdsa_block_attn_prefix_workspace_bytes(bs, B, Hq, Hkv, D, max_ctx_len,
+                                                            num_groups, sms))
+
+
 def block_attn_paged(q, k_cache, v_cache, block_table, seq_lens, *, B: int, page_size: int,
                      scale: float, mode: int, max_ctx_len: int, num_pages: int | None = None,
                      out=None, lse=None, workspace=None, dev_status=None, sms: int = 0,
-                     k_new=None, v_new=None, tree_mask=None):
+                     k_new=None, v_new=None, tree_mask=None, group_offsets=None,
+                     prefix_lens=None):
     """bdsa_block_attn_paged.  q [bs*B, Hq, D] bf16, caches [slots, Hkv, D] bf16.
 
     With k_new / v_new ([bs*B, Hkv, D] bf16) it is bdsa_block_attn_paged_append:
     the block's own keys and values are written into the caches in the same
-    launch.  Returns out [bs*B, Hq, D] bf16 (lse is filled when given, fp32
-    [bs*B, Hq]).
+    launch.  With group_offsets int32 [groups + 1] and prefix_lens int32 [groups]
+    it is bdsa_block_attn_paged_prefix: the requests of a group share their first
+    prefix_lens keys, which are attended once for the group.  Returns out
+    [bs*B, Hq, D] bf16 (lse is filled when given, fp32 [bs*B, Hq]).
     """
+    if group_offsets is not None or prefix_lens is not None:
+        if k_new is not None or v_new is not None or tree_mask is not None:
+            raise ValueError("a shared prefix goes with neither the fused append nor a tree")
+        return _block_attn_prefix(q, k_cache, v_cache, block_table, seq_lens, B, page_size, scale,
+                                  mode, max_ctx_len, num_pages, out, lse, workspace, dev_status,
+                                  sms, group_offsets, prefix_lens)
     _dev(q, "q", torch.bfloat16)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
@@ -227,6 +251,49 @@ def block_attn_paged(q, k_cache, v_cache, block_table, seq_lens, *, B: int, page
             float(scale), int(mode), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, sms,
             _ptr(dev_status), _stream(q.device))
         _check("bdsa_block_attn_paged_append", st)
+    return out
+
+
+def _block_attn_prefix(q, k_cache, v_cache, block_table, seq_lens, B, page_size, scale, mode,
+                       max_ctx_len, num_pages, out, lse, workspace, dev_status, sms,
+                       group_offsets, prefix_lens):
+    if group_offsets is None or prefix_lens is None:
+        raise ValueError("group_offsets and prefix_lens go together")
+    dev, i32, bf16 = _dev(q, "q", torch.bfloat16).device, torch.int32, torch.bfloat16
+    bs, max_pages = _dev(block_table, "block_table", i32).shape
+    if q.dim() != 3 or q.shape[0] != bs * B:
+        raise ValueError(f"q must have shape [{bs * B}, Hq, D], got {tuple(q.shape)}")
+    Hq, D = q.shape[1], q.shape[2]
+    if k_cache.dim() != 3 or k_cache.shape[2] != D:
+        raise ValueError(f"k_cache must have shape [slots, Hkv, {D}]")
+    slots, Hkv = k_cache.shape[0], k_cache.shape[1]
+    if num_pages is None:
+        num_pages = slots // page_size
+    if num_pages * page_size > slots:
+        raise ValueError("the caches hold fewer than num_pages pages")
+    ng = prefix_lens.numel()
+    need = block_attn_prefix_workspace_bytes(bs, B, Hq, Hkv, D, max_ctx_len, ng, sms)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be contiguous memory on {dev}")
+    if out is None:
+        out = torch.empty_like(q)
+    if block_table.device != dev:
+        raise ValueError(f"block_table is on {block_table.device}, expected {dev}")
+    with _on(dev):
+        st = lib().bdsa_block_attn_paged_prefix(
+            q.data_ptr(), _arg(k_cache, "k_cache", bf16, (slots, Hkv, D), dev),
+            _arg(v_cache, "v_cache", bf16, (slots, Hkv, D), dev), block_table.data_ptr(),
+            max_pages, num_pages, _arg(seq_lens, "seq_lens", i32, (bs,), dev),
+            _arg(group_offsets, "group_offsets", i32, (ng + 1,), dev),
+            _arg(prefix_lens, "prefix_lens", i32, (ng,), dev), ng, int(max_ctx_len), bs, B, Hq,
+            Hkv, D, page_size, float(scale), int(mode), _arg(out, "out", bf16, q.shape, dev),
+            _arg(lse, "lse", torch.float32, (bs * B, Hq), dev),
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), sms,
+            _status_arg(dev_status, dev), _stream(dev))
+    _check("bdsa_block_attn_paged_prefix", st)
     return out
 
 
@@ -465,6 +532,13 @@ def tree_accept(block_ids, parent, p, u, seq_lens, *, p_strides=None, V: int | N
 
 
 # ---------------------------------------------------------------------------
+def _on(device):
+    """Context in which `device` is current (nothing to do when it is already)."""
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
 def _arg(t, name: str, dtype, shape, device):
     """A contiguous CUDA tensor of this dtype and shape on `device`, or None."""
     if t is None:
@@ -513,7 +587,7 @@ def block_table_update(seq_lens, new_lens, owned, block_table, free_pages, free_
         out = dict(owned=own, free_state=state, cu_tokens=cu, slot_map=slot, positions=pos)
     outs = [_arg(out[k], k, i32, n, dev) for k, n in
             zip(TABLE_KEYS, ((bs,), (2,), (bs + 1,), (total_tokens,), (total_tokens,)))]
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib().bdsa_block_table_update(
             *ins, block_table.data_ptr(), max_pages, num_pages, bs, int(page_size),
             _arg(free_pages, "free_pages", i32, (num_pages,), dev),
@@ -566,7 +640,7 @@ def token_sample(logits, u=None, *, temperature=None, top_k=None, top_p=None, mi
             raise ValueError(f"probs must be float32 {(bs, B, V)} on {dev}")
     if tokens is None and probs is None:
         raise ValueError("nothing to do: neither u nor probs")
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib().bdsa_token_sample(
             logits.data_ptr(), _LOGIT_DTYPES[logits.dtype], lsr, lsi,
             _arg(u, "u", f32, (bs, B), dev), _arg(temperature, "temperature", f32, (bs,), dev),

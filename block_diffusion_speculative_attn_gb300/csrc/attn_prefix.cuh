@@ -1,0 +1,94 @@
+// attn_prefix.cuh -- what the two kernels of a shared-prefix call agree on: which
+// keys of a request belong to its group's prefix, the prefix work units with
+// their cost offsets, and where the partials of a unit's pieces are.
+//
+// Group g holds requests [off[g], off[g + 1]) and shares its first
+// P' = floor(P_g / 128) * 128 keys.  Its query rows of one KV head, (token, head
+// of the group) in token order, are cut into tiles of npt whole tokens (at most
+// kPrefixRows rows); a unit is two tiles over all P' keys.  Units are numbered
+// (group, KV head, tile pair); each is charged kPrefixUnitCost virtual tiles and
+// its P' / 128 real ones, and CTA b of S takes the cost range [b Wc / S,
+// (b + 1) Wc / S).  The piece that holds a unit's first tile goes to per-row
+// buffers (a row has one such piece); any other piece is the first of its CTA
+// and goes to that CTA's slot.
+#pragma once
+
+#include "attn_common.cuh"
+#include "bdsa_internal.h"
+
+namespace bdsa {
+namespace {
+
+constexpr int kPrefixRows = 128;     // query rows of a tile
+// Virtual tiles a unit switch is charged (a Q load, an epilogue).
+constexpr int kPrefixUnitCost = 2;
+// A CTA takes at least this cost: below it the pieces' partials and their merge
+// cost more than the CTAs gain.
+constexpr int kPrefixMinCost = 6;
+
+// The keys of request r (length L) its group shares, in whole tiles; g its
+// group, or -1 (and 0 keys) when the groups do not place it or its prefix is
+// not inside its length.
+__device__ __forceinline__ int request_prefix(const PrefixParams &x, int r, int L, int &g) {
+    int lo = 0, hi = x.ng;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(x.group_offsets + mid) <= r) lo = mid;
+        else hi = mid;
+    }
+    const int P = __ldg(x.prefix_lens + lo);
+    const bool ok = __ldg(x.group_offsets + lo) <= r && r < __ldg(x.group_offsets + lo + 1) &&
+                    __ldg(x.group_offsets + lo) >= 0 && P >= 0 && P <= L;
+    g = ok ? lo : -1;
+    return ok ? P & ~(kBN - 1) : 0;
+}
+
+// Group g's first request, tokens and shared tiles (no tokens when its bounds
+// are not within [0, bs]).
+__device__ __forceinline__ void group_shape(const PrefixParams &x, int g, int B, int &r0,
+                                            int &tokens, int &nt) {
+    const int o0 = __ldg(x.group_offsets + g), o1 = __ldg(x.group_offsets + g + 1);
+    const int P = __ldg(x.prefix_lens + g);
+    const bool ok = o0 >= 0 && o0 < o1 && o1 <= x.bs && P >= kBN;
+    r0 = ok ? o0 : 0;
+    tokens = ok ? (o1 - o0) * B : 0;
+    nt = ok ? P / kBN : 0;
+}
+__device__ __forceinline__ int group_pairs(const PrefixParams &x, int tokens) {
+    return (tokens + 2 * x.npt - 1) / (2 * x.npt);
+}
+
+__device__ __forceinline__ long long prefix_range_start(long long b, long long Wc, long long S) {
+    return b * Wc / S;
+}
+// The CTA whose cost range holds cost c.
+__device__ __forceinline__ int prefix_cta_of(long long c, long long Wc, long long S) {
+    return (int)(((c + 1) * S - 1) / Wc);
+}
+
+// The unit that holds block row i_blk of request r, KV head h (valid once the
+// prefix grid has finished).
+struct PrefixUnit {
+    long long cost, Wc, S;  // the unit's cost offset; the schedule's total and CTAs
+                            // (S < 0: the group offsets are wrong)
+    int nt;                 // its tiles (0: no shared prefix)
+    int row;                // the block row's first row within the unit's 2 * kPrefixRows
+};
+__device__ __forceinline__ PrefixUnit prefix_unit(const PrefixParams &x, int g, int r, int i_blk,
+                                                  int B, int G, int Hkv, int h) {
+    PrefixUnit u{0, 1, __ldcg(x.head + 1), 0, 0};
+    if (g < 0 || u.S < 0) return u;
+    int r0, tokens;
+    group_shape(x, g, B, r0, tokens, u.nt);
+    if (u.nt == 0) return u;
+    const int t = (r - r0) * B + i_blk;   // token within the group
+    const int tile = t / x.npt, pair = tile >> 1;
+    u.row = (tile & 1) * kPrefixRows + (t % x.npt) * G;
+    u.Wc = __ldcg(x.head);
+    u.cost = __ldcg(x.goff + g) +
+             ((long long)h * group_pairs(x, tokens) + pair) * (kPrefixUnitCost + u.nt);
+    return u;
+}
+
+}  // namespace
+}  // namespace bdsa

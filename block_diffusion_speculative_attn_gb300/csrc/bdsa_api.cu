@@ -94,7 +94,9 @@ int32_t attn_call(const bdsa_bf16 *q, const bdsa_bf16 *k_new, const bdsa_bf16 *v
                   int32_t max_ctx_len, int32_t bs, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
                   int32_t page_size, float softmax_scale, int32_t mode, const uint64_t *tree_mask,
                   bdsa_bf16 *out, float *lse, void *workspace, size_t workspace_bytes,
-                  int32_t num_sms, int32_t *dev_status, void *stream) {
+                  int32_t num_sms, int32_t *dev_status, void *stream,
+                  const int32_t *group_offsets = nullptr, const int32_t *prefix_lens = nullptr,
+                  int32_t num_groups = 0) {
     const bool mode_ok = tree_mask == nullptr
                              ? (mode == BDSA_MODE_DRAFT || mode == BDSA_MODE_VERIFY)
                              : mode == BDSA_MODE_TREE;
@@ -145,6 +147,9 @@ int32_t attn_call(const bdsa_bf16 *q, const bdsa_bf16 *k_new, const bdsa_bf16 *v
     a.workspace = workspace;
     a.workspace_bytes = workspace_bytes;
     a.dev_status = dev_status;
+    if (group_offsets)
+        return bdsa::launch_prefix_attn(a, group_offsets, prefix_lens, num_groups,
+                                        static_cast<cudaStream_t>(stream));
     return bdsa::launch_block_attn(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -196,6 +201,33 @@ int32_t bdsa_block_attn_paged_append(const bdsa_bf16 *q, const bdsa_bf16 *k_new,
     return attn_call(q, k_new, v_new, k_cache, v_cache, block_table, max_pages_per_req, num_pages,
                      seq_lens, max_ctx_len, bs, B, Hq, Hkv, D, page_size, softmax_scale, mode,
                      nullptr, out, lse, workspace, workspace_bytes, num_sms, dev_status, stream);
+}
+
+size_t bdsa_block_attn_prefix_workspace_bytes(int32_t bs, int32_t B, int32_t Hq, int32_t Hkv,
+                                              int32_t D, int32_t max_ctx_len, int32_t num_groups,
+                                              int32_t num_sms) {
+    if (bs <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_ctx_len < 0 || num_groups <= 0)
+        return 0;
+    return bdsa::prefix_plan(bs, B, Hq, Hkv, D, num_groups, bdsa::device_num_sms(num_sms))
+        .workspace;
+}
+
+int32_t bdsa_block_attn_paged_prefix(const bdsa_bf16 *q, const bdsa_bf16 *k_cache,
+                                     const bdsa_bf16 *v_cache, const int32_t *block_table,
+                                     int32_t max_pages_per_req, int32_t num_pages,
+                                     const int32_t *seq_lens, const int32_t *group_offsets,
+                                     const int32_t *prefix_lens, int32_t num_groups,
+                                     int32_t max_ctx_len, int32_t bs, int32_t B, int32_t Hq,
+                                     int32_t Hkv, int32_t D, int32_t page_size,
+                                     float softmax_scale, int32_t mode, bdsa_bf16 *out,
+                                     float *lse, void *workspace, size_t workspace_bytes,
+                                     int32_t num_sms, int32_t *dev_status, void *stream) {
+    if (bs > 0 && (!group_offsets || !prefix_lens || num_groups < 1)) return BDSA_INVALID_ARG;
+    if (num_groups > bs && bs > 0) return BDSA_INVALID_ARG;
+    return attn_call(q, nullptr, nullptr, k_cache, v_cache, block_table, max_pages_per_req,
+                     num_pages, seq_lens, max_ctx_len, bs, B, Hq, Hkv, D, page_size,
+                     softmax_scale, mode, nullptr, out, lse, workspace, workspace_bytes, num_sms,
+                     dev_status, stream, group_offsets, prefix_lens, num_groups);
 }
 
 int32_t bdsa_idlm_prepare(const int32_t *pending, const int32_t *specs, const int32_t *mode,

@@ -40,6 +40,29 @@ struct AttnArgs {
 // Returns a bdsa_status code.
 int launch_block_attn(const AttnArgs &a, cudaStream_t stream);
 
+// Shared prefix: attn_prefix.cuh describes the units and partials.
+struct PrefixParams {
+    const int32_t *group_offsets, *prefix_lens;  // [ng + 1], [ng]
+    int ng, bs;
+    int npt;                    // whole tokens in a 128-row tile
+    long long *head;            // {total cost, CTAs}, written by the prefix kernel
+    long long *goff;            // [ng] cost offset of each group's first unit
+    float *row_lse, *row_o;     // [bs * B * Hq], [.., D]: first pieces
+    float *slot_lse, *slot_o;   // [grid, 256], [.., D]: the other pieces, one slot a CTA
+};
+
+struct PrefixPlan {
+    AttnPlan attn;
+    size_t off_head, off_goff, off_row_lse, off_slot_lse, off_row_o, off_slot_o;
+    size_t workspace;
+};
+
+PrefixPlan prefix_plan(int bs, int B, int Hq, int Hkv, int D, int num_groups, int num_sms);
+int launch_prefix_partials(const AttnArgs &a, const PrefixParams &x, int grid,
+                           cudaStream_t stream);
+int launch_prefix_attn(const AttnArgs &a, const int32_t *group_offsets,
+                       const int32_t *prefix_lens, int num_groups, cudaStream_t stream);
+
 // ---------------------------------------------------------------- prepare
 int launch_prepare_block(const int32_t *verified_id, const int32_t *seq_lens,
                          const int32_t *block_table, int max_pages, int num_pages, int bs, int B,

@@ -65,17 +65,16 @@
 #include <mutex>
 #include <utility>
 
+#include "attn_common.cuh"
+#include "attn_prefix.cuh"
 #include "bdsa_device.cuh"
 #include "bdsa_internal.h"
 
 namespace bdsa {
 namespace {
 
-constexpr int kBN = 128;                  // keys per tile
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;          // S at columns 0 / 128, O at 256 / 384
-constexpr float kRescaleLog2 = 8.0f;      // rescale O only when the max grows by > 2^8
-constexpr float kLn2 = 0.6931471805599453f;
 
 // W8: the 128-row tile with eight softmax warps, two threads a row: its
 // 128-column softmax is bound by instruction latency, which one warp per SM
@@ -184,6 +183,7 @@ struct Params {
     int out_v8;              // out is 32-byte aligned: the M = 128 epilogue stores 32 bytes
     int unit_cost;           // virtual tiles a unit switch is charged in the schedule
     float scale_log2;
+    PrefixParams pfx;        // shared-prefix calls: where the prefix partials are
 };
 
 // The fused append's buffers, a kernel argument of their own (left out of
@@ -202,71 +202,6 @@ __device__ __forceinline__ uint64_t ld_acquire_gpu_u64(const uint64_t *p) {
     uint64_t v;
     asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
     return v;
-}
-
-// 32-byte global load bypassing L1 (one whole sector per lane); p 32-byte aligned.
-__device__ __forceinline__ void ld_cg_v8(const float *p, float *v) {
-    asm volatile("ld.global.cg.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
-                   "=f"(v[6]), "=f"(v[7])
-                 : "l"(p)
-                 : "memory");
-}
-
-// 32-byte global store (one whole sector per lane).
-__device__ __forceinline__ void st_global_v8(void *p, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d, uint32_t e, uint32_t f, uint32_t g,
-                                             uint32_t h) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a),
-                 "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
-                 : "memory");
-}
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-                 "r"(d)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t *>(&v);
-}
-
-// Pairs of fp32 values in one 64-bit register, for the f32x2 arithmetic of
-// the sm_100 family (two results per instruction), and the three-input max:
-// the softmax at 128 columns a thread is bound by instruction issue, and
-// these halve its max, scale and sum instructions.
-__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 f2_unpack(uint64_t r) {
-    float2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
-    return v;
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
 }
 
 // One 32-column chunk of this thread's share of a TMEM accumulator block.
@@ -316,6 +251,14 @@ __device__ __forceinline__ long vreq_keys(const Params &prm, int rv, long L) {
     if constexpr (!kRT) return L + prm.B;
     return L + min(prm.B, vreq_node0<kRT>(prm, rv) + prm.npt);
 }
+// Shared-prefix calls (kPre): the keys of virtual request rv that its group has
+// already attended, a multiple of the tile.
+template <bool kRT, bool kPre>
+__device__ __forceinline__ int vreq_p0(const Params &prm, int rv, int L) {
+    if constexpr (!kPre) return 0;
+    int g;
+    return request_prefix(prm.pfx, vreq_r<kRT>(prm, rv), L, g);
+}
 template <bool kRT>
 __device__ __forceinline__ int vreq_count(const Params &prm) { return kRT ? prm.bs_v : prm.bs; }
 template <bool kRT>
@@ -340,6 +283,7 @@ struct Sched {
     long long x0, x1, W, Wc;
     long long wsum[12];      // per-warp partial sums of the scan (<= 384 threads)
     int appended;            // attention with the fused append: 32 x pieces whose rows are written
+    int p00;                 // the first unit's keys start here (shared prefix)
 };
 static_assert(sizeof(Sched) <= 176, "the attention kernel keeps Sched in 176 bytes");
 
@@ -347,13 +291,14 @@ static_assert(sizeof(Sched) <= 176, "the attention kernel keeps Sched in 176 byt
 // order; u is the unit's index within its virtual request.
 struct Cursor {
     int r, u, nt, L;
+    int p0;      // first key of the unit (0 without a shared prefix)
     long u_off;  // global index of the unit's first tile
 };
 
 // A maximal run of one unit's tiles inside a CTA's range: r the virtual
 // request, u the unit within it, h its KV head.
 struct Piece {
-    int r, u, h, a, e, nt, L;
+    int r, u, h, a, e, nt, L, p0;
     long u_off;
 };
 
@@ -365,6 +310,7 @@ __device__ __forceinline__ Piece piece_at(const Params &prm, const Cursor &c, lo
     pc.h = vreq_h0<kRT>(prm, c.r) + c.u;
     pc.nt = c.nt;
     pc.L = c.L;
+    pc.p0 = c.p0;
     pc.u_off = c.u_off;
     pc.a = (int)(x - c.u_off);
     pc.e = (int)min((long)c.nt, (long)pc.a + (x1 - x));
@@ -387,7 +333,7 @@ __device__ __forceinline__ long range_start(int b, long W, int S, uint64_t magic
 // counts of a contiguous block of requests, a scan gives each block's first
 // tile, and the threads whose blocks hold the CTA's cost bounds map them to
 // real tiles.  Two __syncthreads; results in *sch.
-template <int NT, bool kRT>
+template <int NT, bool kRT, bool kPre = false>
 __device__ void schedule(const Params &prm, int b, int S, Sched *sch) {
     static_assert(NT % 32 == 0 && NT <= 384, "scan partials hold 12 warps");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -395,8 +341,10 @@ __device__ void schedule(const Params &prm, int b, int S, Sched *sch) {
     const int per = (bs + NT - 1) / NT;
     const int i0 = min(bs, tid * per), i1 = min(bs, i0 + per);
     long long sum = 0;
-    for (int i = i0; i < i1; ++i)
-        sum += tiles_of_keys(vreq_keys<kRT>(prm, i, vreq_L<kRT>(prm, i)));
+    for (int i = i0; i < i1; ++i) {
+        const int L = vreq_L<kRT>(prm, i);
+        sum += tiles_of_keys(vreq_keys<kRT>(prm, i, L) - vreq_p0<kRT, kPre>(prm, i, L));
+    }
     long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -427,7 +375,8 @@ __device__ void schedule(const Params &prm, int b, int S, Sched *sch) {
         long long tp = pre;  // tiles before request i
         for (int i = i0; i < i1; ++i) {
             const int L = vreq_L<kRT>(prm, i);
-            const int nt = tiles_of_keys(vreq_keys<kRT>(prm, i, L));
+            const int p0 = vreq_p0<kRT, kPre>(prm, i, L);
+            const int nt = tiles_of_keys(vreq_keys<kRT>(prm, i, L) - p0);
             const long long ci = Hkv * (tp + uc * i);
             const long long span = nt + uc;  // cost of one unit of request i
             if (c < ci + Hkv * span) {
@@ -440,6 +389,7 @@ __device__ void schedule(const Params &prm, int b, int S, Sched *sch) {
                     sch->u0 = h;
                     sch->nt0 = nt;
                     sch->L0 = L;
+                    sch->p00 = p0;
                     sch->u_off0 = u_off;
                     sch->cu0 = ci + (long long)h * span;
                     sch->x0 = x;
@@ -461,31 +411,20 @@ __device__ void schedule(const Params &prm, int b, int S, Sched *sch) {
 }
 
 // Move the cursor past a finished unit.
-template <bool kRT>
+template <bool kRT, bool kPre = false>
 __device__ __forceinline__ void next_unit(Cursor &c, const Params &prm) {
     c.u_off += c.nt;
     if (++c.u == vreq_units<kRT>(prm)) {
         c.u = 0;
         if (++c.r < vreq_count<kRT>(prm)) {
             c.L = vreq_L<kRT>(prm, c.r);
-            c.nt = tiles_of_keys(vreq_keys<kRT>(prm, c.r, c.L));
+            c.p0 = vreq_p0<kRT, kPre>(prm, c.r, c.L);
+            c.nt = tiles_of_keys(vreq_keys<kRT>(prm, c.r, c.L) - c.p0);
         }
     }
 }
 __device__ __forceinline__ int cta_of(long x, long W, int S) {
     return (int)(((x + 1) * (long)S - 1) / W);
-}
-
-constexpr int kMaxBoxes = kBN / 8;  // page_size >= 8
-
-// Number of TMA boxes of tile t0 that hold keys of the request (never past its
-// block-table row).
-__device__ __forceinline__ int boxes_of(long n_keys, long t0, int rows_box, int log2_ps,
-                                        int max_pages) {
-    const long valid = max(0L, min((long)kBN, n_keys - t0));
-    int nbox = (int)((valid + rows_box - 1) / rows_box);
-    while (nbox > 0 && ((t0 + (long)(nbox - 1) * rows_box) >> log2_ps) >= max_pages) --nbox;
-    return nbox;
 }
 
 // Fused append, one warp: the block's own keys and values of request r, KV
@@ -532,8 +471,10 @@ __device__ void append_piece_rows(const Params &prm, const AppendParams &app, co
 }
 
 // kTree: the TREE mask (block keys by tree_mask bits), in an instantiation of
-// its own so that the DRAFT / VERIFY tile loop carries none of its code.
-template <int D, int M, bool kAppend, bool kTree>
+// its own so that the DRAFT / VERIFY tile loop carries none of its code.  kPre:
+// a unit's keys start at its group's shared prefix, whose share of the softmax
+// the prefix kernel (prefix_attn.cu) left in partials that the epilogue folds in.
+template <int D, int M, bool kAppend, bool kTree, bool kPre = false>
 __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                                           : Cfg<D, M, M == 128>::kThreads,
                                   1)
@@ -625,7 +566,10 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
     const uint32_t tmem = *tmem_slot;
 
     // ---- inputs written by earlier kernels on the stream are read from here on
-    grid_dependency_wait();
+    // (kPre: the preceding grid is this call's prefix kernel, which lets this one
+    // launch only once everything before it has finished; its own partials are
+    // waited for where they are read)
+    if constexpr (!kPre) grid_dependency_wait();
     // The merge kernel may start now: its schedule reads only this call's
     // inputs.  With the owner merge there is no merge kernel, and the next
     // kernel on the stream is left to start when this grid ends: launched
@@ -634,7 +578,7 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
     if (!prm.owner_merge) grid_launch_dependents();
     const int S = gridDim.x;
     const int b = blockIdx.x;
-    schedule<NT, kTree>(prm, b, S, sch);
+    schedule<NT, kTree, kPre>(prm, b, S, sch);
     if (warp == kKProducerWarp && sch->x0 < sch->x1) {
         // Warm L2 with the block-table entries of this CTA's range: its first
         // request's row from the first tile's page (lanes 0-15, 512 entries)
@@ -644,7 +588,9 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
         // context-length reads (Qwen3-8B-shaped verify call 64.3 -> 62.3 us
         // mean, A/B over 200 steps).
         const long r = (long)vreq_r<kTree>(prm, sch->r0) + (lane >> 4);
-        const long p0 = (long)(((sch->x0 - sch->u_off0) * kBN) >> prm.log2_ps) & ~31L;
+        const long p0 = (long)(((sch->x0 - sch->u_off0) * kBN + (kPre ? sch->p00 : 0)) >>
+                               prm.log2_ps) &
+                        ~31L;
         const long e = (lane < 16 ? p0 : 0L) + (long)(lane & 15) * 32;  // 32 entries a line
         if (r < prm.bs && e < prm.max_pages)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(prm.block_table + r * prm.max_pages + e));
@@ -656,6 +602,7 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
         cur0.u = sch->u0;
         cur0.nt = sch->nt0;
         cur0.L = sch->L0;
+        cur0.p0 = kPre ? sch->p00 : 0;
         cur0.u_off = sch->u_off0;
     }
 
@@ -700,7 +647,7 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                 // own rows waits until the append warp has written this piece.
                 const int j_app = (kAppend && pc.L >= 0) ? max(pc.a, pc.L / kBN) : pc.e;
                 for (int j = pc.a; j < pc.e; ++j, ++g) {
-                    const long t0 = (long)j * kBN;
+                    const long t0 = (long)j * kBN + pc.p0;
                     if (kAppend && j == j_app) {
                         ok = wait_counter_geq(&sch->appended, 32 * (k + 1), abort_flag,
                                               prm.dev_status);
@@ -734,7 +681,7 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                     issued = g + 1;
                 }
                 x += pc.e - pc.a;
-                if (pc.e == pc.nt) next_unit<kTree>(cur, prm);
+                if (pc.e == pc.nt) next_unit<kTree, kPre>(cur, prm);
             }
             // Drain: the last load issued into each buffer must have landed before exit.
             for (long i = max(0L, q_issued - C::NQ); i < q_issued; ++i)
@@ -830,7 +777,7 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                     have = true;
                 }
                 x += n;
-                if (pc.e == pc.nt) next_unit<kTree>(cur, prm);
+                if (pc.e == pc.nt) next_unit<kTree, kPre>(cur, prm);
             }
             if (ok && have) ok = issue_pv(pend);
             // Drain: every MMA issued above has completed before TMEM is released.
@@ -850,7 +797,7 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
             fence_proxy_async_global();
             red_release_add_shared(&sch->appended, 1);
             x += pc.e - pc.a;
-            if (pc.e == pc.nt) next_unit<kTree>(cur, prm);
+            if (pc.e == pc.nt) next_unit<kTree, kPre>(cur, prm);
         }
     } else if (warp < kSoftmaxWarps) {
         // ------------------------------------------------ softmax + epilogue
@@ -1121,7 +1068,11 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
         // then reset to 0, so a CUDA graph replaying this call's ticket never
         // finds one already set.
         int n_own = 0;  // units merged by this CTA as owner (phases of MR)
-        auto owner_gather = [&](Epi &e, const Piece &pc, float lr) -> bool {
+        //
+        // kPre: a unit's output also takes in its group's prefix partials,
+        // whether this CTA holds the whole unit or owns a cut one.
+        bool pfx_ready = false;
+        auto owner_gather = [&](Epi &e, const Piece &pc, float lr, int grp) -> bool {
             const long long cu =
                 (long long)pc.u_off +
                 (long long)prm.unit_cost * ((long long)pc.r * vreq_units<kTree>(prm) + pc.u);
@@ -1133,7 +1084,46 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
             bool bad = e.bad, okg = true;
 #pragma unroll
             for (int c = 0; c < OC; ++c) madd[c] = 0.f;
+            // one more piece of the row: log2-sum-exp ls, normalised output at src
+            auto fold = [&](float ls, const float *src) {
+                // this thread's OC columns of the row: 32-byte loads (whole
+                // sectors), all in flight before the first is used
+                float po[OC];
+#pragma unroll
+                for (int v = 0; v < OC / 8; ++v) ld_cg_v8(src + 8 * v, &po[8 * v]);
+                if (ls == -INFINITY) return;  // no key of that piece is visible to the row
+                const float m_new = fmaxf(m_run, ls);
+                const float a = m_run == -INFINITY ? 0.f : exp2f(m_run - m_new);
+                const float wj = exp2f(ls - m_new);
+                s_own *= a;
+                den = den * a + wj;
+#pragma unroll
+                for (int c = 0; c < OC; ++c) madd[c] = fmaf(madd[c], a, wj * po[c]);
+                m_run = m_new;
+            };
             int bb = b + 1;
+            if constexpr (kPre) {
+                if (!e.owner) bb = S;
+                if (!pfx_ready) grid_dependency_wait();
+                pfx_ready = true;
+                const PrefixUnit pu = prefix_unit(prm.pfx, grp, e.r, i_blk, B, G, prm.Hkv, pc.h);
+                bad = bad || pu.S < 0;
+                if (pu.nt > 0 && valid_row && !bad) {
+                    const long long c0 = pu.cost + kPrefixUnitCost;
+                    const int q0 = prefix_cta_of(c0, pu.Wc, pu.S);
+                    const int q1 = prefix_cta_of(c0 + pu.nt - 1, pu.Wc, pu.S);
+                    for (int q = q0; q <= q1; ++q) {
+                        const long src =
+                            q == q0 ? e.orow
+                                    : (long)q * 2 * kPrefixRows + pu.row + row % G;
+                        const float ls =
+                            __ldcg((q == q0 ? prm.pfx.row_lse : prm.pfx.slot_lse) + src);
+                        if (ls == INFINITY) bad = true;  // a page outside the pool
+                        else fold(ls, (q == q0 ? prm.pfx.row_o : prm.pfx.slot_o) + src * D +
+                                          half * OC);
+                    }
+                }
+            }
             for (; okg && bb < S; ++bb) {
                 const long long cb = range_start(bb, Wc, S, prm.magic_S);
                 if (cb > last) break;
@@ -1158,37 +1148,26 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                     }
                     if (!okg) break;
                 }
-                // this thread's OC columns of the row: 32-byte loads (whole
-                // sectors), all in flight before the first is used
                 const float *src = prm.part_o + ((long)sl * prm.rows + row) * D + half * OC;
-                float po[OC];
-#pragma unroll
-                for (int v = 0; v < OC / 8; ++v) ld_cg_v8(src + 8 * v, &po[8 * v]);
                 const float ls = __ldcg(prm.part_lse + (long)sl * prm.rows + row);
                 bad = bad || __ldcg(prm.part_bad + sl) != 0;
-                if (ls == -INFINITY) continue;  // no key of that piece is visible to the row
-                const float m_new = fmaxf(m_run, ls);
-                const float a = m_run == -INFINITY ? 0.f : exp2f(m_run - m_new);
-                const float wj = exp2f(ls - m_new);
-                s_own *= a;
-                den = den * a + wj;
-#pragma unroll
-                for (int c = 0; c < OC; ++c) madd[c] = fmaf(madd[c], a, wj * po[c]);
-                m_run = m_new;
+                fold(ls, src);
             }
             // every softmax warp has read the words (a bounded wait on MR, one
             // phase per owned unit) before thread 0 resets them
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::MR));
-            if (tid == 0 &&
-                mbar_wait(bar(C::MR), (uint32_t)(n_own & 1), abort_flag, prm.dev_status)) {
-                for (int q = b + 1; q < bb && q < S; ++q) {
-                    const long long cb = range_start(q, Wc, S, prm.magic_S);
-                    if (cb < range_start(q + 1, Wc, S, prm.magic_S))
-                        prm.part_ready[2 * q] = 0ull;
+            if (!kPre || e.owner) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::MR));
+                if (tid == 0 &&
+                    mbar_wait(bar(C::MR), (uint32_t)(n_own & 1), abort_flag, prm.dev_status)) {
+                    for (int q = b + 1; q < bb && q < S; ++q) {
+                        const long long cb = range_start(q, Wc, S, prm.magic_S);
+                        if (cb < range_start(q + 1, Wc, S, prm.magic_S))
+                            prm.part_ready[2 * q] = 0ull;
+                    }
                 }
+                ++n_own;
             }
-            ++n_own;
             okg = __all_sync(0xffffffffu, okg);
             bad = __any_sync(0xffffffffu, bad);
             const bool good = !bad && den > 0.f;
@@ -1216,8 +1195,13 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
             // tile of a request agrees), or an id outside the pool, makes the
             // unit's output zeros.  Each tile's ids are loaded during the tile
             // and checked during the next one (or the epilogue).
-            const bool shape_bad =
+            bool shape_bad =
                 pc.L < 0 || ((long)pc.L + B + ps - 1) / ps > (long)prm.max_pages;
+            int grp = -1;  // the request's group (kPre)
+            if constexpr (kPre) {
+                request_prefix(prm.pfx, rr, pc.L, grp);
+                shape_bad = shape_bad || grp < 0;
+            }
             const int32_t *bt_row = prm.block_table + (long)rr * prm.max_pages;
             bool page_bad = false, pend = false;
             int32_t pend_pg = 0;
@@ -1240,7 +1224,7 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
             // dominant V row).
             uint64_t lacc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
             for (int j = pc.a; j < pc.e; ++j, ++g) {
-                const long t0 = (long)j * kBN;
+                const long t0 = (long)j * kBN + pc.p0;
                 const int sb = (int)(g & 1);
                 // TREE: the mask words this tile's block keys need (at most
                 // three from word wb), loaded before the wait for S
@@ -1478,8 +1462,8 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                 e.k = k;
                 if (e.bad && tid == 0) report_status(prm.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
                 if constexpr (kOwner) {
-                    if (e.owner) {
-                        ok = owner_gather(e, pc, lr);
+                    if (e.owner || (kPre && e.complete)) {
+                        ok = owner_gather(e, pc, lr, grp);
                         if (!ok) break;
                     } else {
 #pragma unroll
@@ -1490,7 +1474,7 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                 if (!ok) break;
             }
             x += pc.e - pc.a;
-            if (pc.e == pc.nt) next_unit<kTree>(cur, prm);
+            if (pc.e == pc.nt) next_unit<kTree, kPre>(cur, prm);
         }
     }
 
@@ -1661,25 +1645,6 @@ __global__ void __launch_bounds__(kMergeThreads, 4) attn_merge_kernel(const Para
 }
 
 // ------------------------------------------------------------------ host side
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
 // A ticket unique to each call and never 0: a partial slot's ready word holds
 // the ticket of the call that last wrote it, so it cannot show the current
 // call's ticket before this call publishes the slot.  The counter starts at a
@@ -1711,24 +1676,6 @@ bool expire_owner_waits() {
     return v != nullptr && v[0] == '1' && v[1] == '\0';
 }
 
-// Launch with the programmatic-stream-serialization attribute, so the kernel
-// may start its prologue while the previous kernel on the stream finishes.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                       cudaStream_t stream, Args &&...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
 // Virtual tiles a unit switch costs in the schedule (A/B over the bench's
 // workloads against the cost two, which every tile size had before): three
 // for the DRAFT / VERIFY tiles (Qwen3-8B-shaped verify call 64.5 -> 63.7 us,
@@ -1741,7 +1688,8 @@ int unit_cost_for(int M, bool tree) {
 }
 
 template <int D, int M>
-int launch_impl(const AttnArgs &a, const AttnPlan &plan, cudaStream_t stream) {
+int launch_impl(const AttnArgs &a, const AttnPlan &plan, cudaStream_t stream,
+                const PrefixParams *pfx = nullptr) {
     using C = Cfg<D, M, M == 128>;
     EncodeTiledFn enc = encode_fn();
     if (enc == nullptr) return BDSA_CUDA_ERROR;
@@ -1857,8 +1805,10 @@ int launch_impl(const AttnArgs &a, const AttnPlan &plan, cudaStream_t stream) {
     prm.box_rows = box_rows;
     prm.mode = a.mode;
     prm.scale_log2 = a.scale * 1.4426950408889634f;
+    prm.pfx = PrefixParams{};
     prm.magic_S = UINT64_MAX / (uint64_t)plan.grid;
     prm.unit_cost = unit_cost_for(M, n_rt > 1 || a.mode == BDSA_MODE_TREE);
+    if (pfx != nullptr) prm.pfx = *pfx;
     AppendParams app;
     app.k_new = a.k_new;
     app.v_new = a.v_new;
@@ -1866,13 +1816,14 @@ int launch_impl(const AttnArgs &a, const AttnPlan &plan, cudaStream_t stream) {
     app.v_cache = const_cast<uint16_t *>(a.v_cache);
     const bool append = a.k_new != nullptr;
     const bool tree = a.mode == BDSA_MODE_TREE;
-    auto kernel = tree ? block_attn_kernel<D, M, false, true>
-                       : (append ? block_attn_kernel<D, M, true, false>
-                                 : block_attn_kernel<D, M, false, false>);
-    const int inst = tree ? 2 : (append ? 1 : 0);
+    auto kernel = pfx ? block_attn_kernel<D, M, false, false, true>
+                  : tree ? block_attn_kernel<D, M, false, true>
+                         : (append ? block_attn_kernel<D, M, true, false>
+                                   : block_attn_kernel<D, M, false, false>);
+    const int inst = pfx ? 3 : tree ? 2 : (append ? 1 : 0);
     const int smem = C::kSmem;
     const int threads = append ? C::kThreadsAppend : C::kThreads;
-    static bool attr_set[3] = {false, false, false};  // per instantiation
+    static bool attr_set[4] = {false, false, false, false};  // per instantiation
     if (!attr_set[inst]) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
             cudaSuccess)
@@ -1889,8 +1840,6 @@ int launch_impl(const AttnArgs &a, const AttnPlan &plan, cudaStream_t stream) {
         return BDSA_CUDA_ERROR;
     return BDSA_OK;
 }
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
@@ -1924,6 +1873,63 @@ int launch_block_attn(const AttnArgs &a, cudaStream_t stream) {
         return m64 ? launch_impl<128, 64>(a, plan, stream) : launch_impl<128, 128>(a, plan, stream);
     if (a.D == 64)
         return m64 ? launch_impl<64, 64>(a, plan, stream) : launch_impl<64, 128>(a, plan, stream);
+    return BDSA_UNSUPPORTED;
+}
+
+// The shared-prefix call: the prefix kernel's partials (prefix_attn.cu), then
+// the block attention over the keys behind the prefix.  The owner merge wants
+// the whole grid resident, so there are at most as many CTAs as SMs.
+PrefixPlan prefix_plan(int bs, int B, int Hq, int Hkv, int D, int num_groups, int num_sms) {
+    PrefixPlan p;
+    p.attn = attn_plan(bs, B, Hq, Hkv, D, 0, num_sms);
+    size_t off = p.attn.workspace;
+    const size_t rows = (size_t)bs * B * Hq, slots = (size_t)p.attn.grid * 2 * kPrefixRows;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += align256(bytes);
+        return at;
+    };
+    p.off_head = take(2 * sizeof(int64_t));
+    p.off_goff = take((size_t)num_groups * sizeof(int64_t));
+    p.off_row_lse = take(rows * sizeof(float));
+    p.off_slot_lse = take(slots * sizeof(float));
+    p.off_row_o = take(rows * D * sizeof(float));
+    p.off_slot_o = take(slots * D * sizeof(float));
+    p.workspace = off;
+    return p;
+}
+
+int launch_prefix_attn(const AttnArgs &a, const int32_t *group_offsets,
+                       const int32_t *prefix_lens, int num_groups, cudaStream_t stream) {
+    AttnArgs b = a;
+    const int sms = device_num_sms(0);
+    if (b.num_sms > sms) b.num_sms = sms;
+    const PrefixPlan plan =
+        prefix_plan(b.bs, b.B, b.Hq, b.Hkv, b.D, num_groups, b.num_sms);
+    if (b.workspace == nullptr || b.workspace_bytes < plan.workspace)
+        return BDSA_WORKSPACE_TOO_SMALL;
+    char *ws = static_cast<char *>(b.workspace);
+    PrefixParams x;
+    x.group_offsets = group_offsets;
+    x.prefix_lens = prefix_lens;
+    x.ng = num_groups;
+    x.bs = b.bs;
+    x.npt = kPrefixRows / (b.Hq / b.Hkv);
+    x.head = reinterpret_cast<long long *>(ws + plan.off_head);
+    x.goff = reinterpret_cast<long long *>(ws + plan.off_goff);
+    x.row_lse = reinterpret_cast<float *>(ws + plan.off_row_lse);
+    x.slot_lse = reinterpret_cast<float *>(ws + plan.off_slot_lse);
+    x.row_o = reinterpret_cast<float *>(ws + plan.off_row_o);
+    x.slot_o = reinterpret_cast<float *>(ws + plan.off_slot_o);
+    const int st = launch_prefix_partials(b, x, plan.attn.grid, stream);
+    if (st != BDSA_OK) return st;
+    const bool m64 = (b.Hq / b.Hkv) * b.B <= 64;
+    if (b.D == 128)
+        return m64 ? launch_impl<128, 64>(b, plan.attn, stream, &x)
+                   : launch_impl<128, 128>(b, plan.attn, stream, &x);
+    if (b.D == 64)
+        return m64 ? launch_impl<64, 64>(b, plan.attn, stream, &x)
+                   : launch_impl<64, 128>(b, plan.attn, stream, &x);
     return BDSA_UNSUPPORTED;
 }
 

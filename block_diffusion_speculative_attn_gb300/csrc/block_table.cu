@@ -269,8 +269,9 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableArg
 
 int launch_block_table(const TableArgs &a, int num_sms, cudaStream_t stream) {
     const size_t smem = (size_t)3 * (a.bs + 1) * sizeof(int);
-    // more than the default 48 KB of dynamic shared memory, on this device
-    if (smem > 48 * 1024 &&
+    // past the default 48 KB of shared memory (static and dynamic together), on
+    // this device
+    if (smem > 44 * 1024 &&
         cudaFuncSetAttribute(block_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem) != cudaSuccess)
         return BDSA_CUDA_ERROR;

@@ -499,6 +499,49 @@ int32_t bdsa_tree_accept(const int32_t *block_ids, const int32_t *parent, const 
                          int32_t *dev_status, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* bdsa_block_attn_paged_prefix
+ *
+ * bdsa_block_attn_paged for a batch whose requests share long prefixes (one
+ * system prompt, one document, several continuations of one context; "From
+ * DFlash to dLLM Self-Spec (II)", sections 2.2.3-2.2.4, the block forwards of a
+ * serving batch): the same outputs, with each group's shared keys read and
+ * multiplied once for the group instead of once a request.
+ *
+ * Group g holds the requests [group_offsets[g], group_offsets[g+1]), whose
+ * first prefix_lens[g] keys are the same tokens; group_offsets [num_groups + 1]
+ * runs up from 0 to bs, 1 <= num_groups <= bs (a request that shares with
+ * nobody is a group of one, with any prefix_lens up to its length; 0 shares
+ * nothing).  The first floor(prefix_lens[g] / 128) * 128 keys are read through
+ * the block-table row of the group's first request, the others through each
+ * request's own row, so the shared pages need only be in the first row.
+ * Everything else is as in bdsa_block_attn_paged, DRAFT and VERIFY.
+ * A request with prefix_lens[g] < 0 or above its length, and every request of a
+ * group whose shared pages (up to the 128-key limit) are outside the pool or
+ * the row, gets out = 0 and lse = -inf; group_offsets that do not run up from 0
+ * to bs give that for every request; all report BDSA_DEVICE_OUT_OF_RANGE.
+ * Two launches (the prefix of all groups, then the rest, which folds the
+ * prefix's share in), chained with programmatic dependent launch.  num_sms
+ * above the device's SM count counts as the device's.
+ * Workspace: at least bdsa_block_attn_prefix_workspace_bytes(...) bytes,
+ * 256-byte aligned: bdsa_block_attn_paged's, an fp32 partial (D + 1 values) of
+ * each query row and 256 rows' for each CTA.
+ */
+size_t bdsa_block_attn_prefix_workspace_bytes(int32_t bs, int32_t B, int32_t Hq, int32_t Hkv,
+                                              int32_t D, int32_t max_ctx_len, int32_t num_groups,
+                                              int32_t num_sms);
+
+int32_t bdsa_block_attn_paged_prefix(const bdsa_bf16 *q, const bdsa_bf16 *k_cache,
+                                     const bdsa_bf16 *v_cache, const int32_t *block_table,
+                                     int32_t max_pages_per_req, int32_t num_pages,
+                                     const int32_t *seq_lens, const int32_t *group_offsets,
+                                     const int32_t *prefix_lens, int32_t num_groups,
+                                     int32_t max_ctx_len, int32_t bs, int32_t B, int32_t Hq,
+                                     int32_t Hkv, int32_t D, int32_t page_size,
+                                     float softmax_scale, int32_t mode, bdsa_bf16 *out,
+                                     float *lse, void *workspace, size_t workspace_bytes,
+                                     int32_t num_sms, int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* bdsa_block_table_update
  *
  * "From DFlash to dLLM Self-Spec (II): SGLang Spec V2", section 2.3.5 (the

@@ -76,6 +76,44 @@ def test_sample_refusals(L):
     assert _sample(L, pr=A + 2) == 3
 
 
+def _prefix(L, **kw):
+    a = dict(q=A, k=A, v=A, bt=A, mp=40, np=80, sl=A, go=A, pl=A, ng=2, mc=100, bs=2, B=8, Hq=8,
+             Hkv=2, D=128, ps=16, scale=0.1, mode=1, out=A, lse=None, ws=None, wsb=0, sms=152)
+    a.update(kw)
+    return L.bdsa_block_attn_paged_prefix(a["q"], a["k"], a["v"], a["bt"], a["mp"], a["np"],
+                                          a["sl"], a["go"], a["pl"], a["ng"], a["mc"], a["bs"],
+                                          a["B"], a["Hq"], a["Hkv"], a["D"], a["ps"], a["scale"],
+                                          a["mode"], a["out"], a["lse"], a["ws"], a["wsb"],
+                                          a["sms"], None, None)
+
+
+def test_prefix_refusals(L):
+    assert _prefix(L, bs=0) == 0
+    assert _prefix(L, go=None) == 1
+    assert _prefix(L, pl=None) == 1
+    assert _prefix(L, ng=0) == 1
+    assert _prefix(L, ng=3) == 1                     # more groups than requests
+    assert _prefix(L, mode=2) == 1                   # no trees
+    assert _prefix(L, q=None) == 1
+    assert _prefix(L, scale=0.0) == 1
+    assert _prefix(L, D=96) == 2
+    assert _prefix(L, Hq=64, Hkv=2) == 2             # G * B > 128
+    assert _prefix(L, ps=24) == 2
+    assert _prefix(L, out=A + 2) == 3
+
+
+def test_prefix_workspace(L):
+    f = L.bdsa_block_attn_prefix_workspace_bytes
+    al = lambda x: (x + 255) // 256 * 256
+    bs, B, Hq, Hkv, D, ng, sms = 32, 16, 32, 8, 128, 3, 152
+    rows, slots = bs * B * Hq, 256 * sms
+    want = L.bdsa_block_attn_workspace_bytes(bs, B, Hq, Hkv, D, 4096, sms)
+    want += al(16) + al(8 * ng) + al(4 * rows) + al(4 * slots) + al(4 * rows * D) + \
+        al(4 * slots * D)
+    assert f(bs, B, Hq, Hkv, D, 4096, ng, sms) == want
+    assert f(bs, B, Hq, Hkv, D, 4096, 0, sms) == 0
+
+
 def test_python_checks_need_no_gpu():
     i = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError):
