@@ -23,7 +23,6 @@ Calls (all asynchronous on the current stream):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -259,41 +258,40 @@ def _block_attn_prefix(q, k_cache, v_cache, block_table, seq_lens, B, page_size,
                        group_offsets, prefix_lens):
     if group_offsets is None or prefix_lens is None:
         raise ValueError("group_offsets and prefix_lens go together")
-    dev, i32, bf16 = _dev(q, "q", torch.bfloat16).device, torch.int32, torch.bfloat16
-    bs, max_pages = _dev(block_table, "block_table", i32).shape
+    i32, bf16 = torch.int32, torch.bfloat16
+    index = _dev(q, "q", bf16).get_device()
+    bs, max_pages = block_table.shape
     if q.dim() != 3 or q.shape[0] != bs * B:
         raise ValueError(f"q must have shape [{bs * B}, Hq, D], got {tuple(q.shape)}")
-    Hq, D = q.shape[1], q.shape[2]
+    _, Hq, D = q.shape
     if k_cache.dim() != 3 or k_cache.shape[2] != D:
         raise ValueError(f"k_cache must have shape [slots, Hkv, {D}]")
-    slots, Hkv = k_cache.shape[0], k_cache.shape[1]
+    cache = k_cache.shape
     if num_pages is None:
-        num_pages = slots // page_size
-    if num_pages * page_size > slots:
+        num_pages = cache[0] // page_size
+    if num_pages * page_size > cache[0]:
         raise ValueError("the caches hold fewer than num_pages pages")
     ng = prefix_lens.numel()
-    need = block_attn_prefix_workspace_bytes(bs, B, Hq, Hkv, D, max_ctx_len, ng, sms)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be contiguous memory on {dev}")
+    if workspace is None:
+        workspace = torch.empty(
+            block_attn_prefix_workspace_bytes(bs, B, Hq, cache[1], D, max_ctx_len, ng, sms),
+            dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous memory on cuda:{index}")
     if out is None:
         out = torch.empty_like(q)
-    if block_table.device != dev:
-        raise ValueError(f"block_table is on {block_table.device}, expected {dev}")
-    with _on(dev):
-        st = lib().bdsa_block_attn_paged_prefix(
-            q.data_ptr(), _arg(k_cache, "k_cache", bf16, (slots, Hkv, D), dev),
-            _arg(v_cache, "v_cache", bf16, (slots, Hkv, D), dev), block_table.data_ptr(),
-            max_pages, num_pages, _arg(seq_lens, "seq_lens", i32, (bs,), dev),
-            _arg(group_offsets, "group_offsets", i32, (ng + 1,), dev),
-            _arg(prefix_lens, "prefix_lens", i32, (ng,), dev), ng, int(max_ctx_len), bs, B, Hq,
-            Hkv, D, page_size, float(scale), int(mode), _arg(out, "out", bf16, q.shape, dev),
-            _arg(lse, "lse", torch.float32, (bs * B, Hq), dev),
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), sms,
-            _status_arg(dev_status, dev), _stream(dev))
-    _check("bdsa_block_attn_paged_prefix", st)
+    _launch(lib().bdsa_block_attn_paged_prefix, "bdsa_block_attn_paged_prefix", index,
+            q.data_ptr(), _arg(k_cache, "k_cache", bf16, cache, index),
+            _arg(v_cache, "v_cache", bf16, cache, index),
+            _arg(block_table, "block_table", i32, (bs, max_pages), index), max_pages, num_pages,
+            _arg(seq_lens, "seq_lens", i32, (bs,), index),
+            _arg(group_offsets, "group_offsets", i32, (ng + 1,), index),
+            _arg(prefix_lens, "prefix_lens", i32, (ng,), index), ng, int(max_ctx_len), bs, B, Hq,
+            cache[1], D, page_size, float(scale), int(mode),
+            _arg(out, "out", bf16, q.shape, index),
+            _arg(lse, "lse", torch.float32, (bs * B, Hq), index), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), sms,
+            _arg(dev_status, "dev_status", i32, (1,), index))
     return out
 
 
@@ -532,27 +530,31 @@ def tree_accept(block_ids, parent, p, u, seq_lens, *, p_strides=None, V: int | N
 
 
 # ---------------------------------------------------------------------------
-def _on(device):
-    """Context in which `device` is current (nothing to do when it is already)."""
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _launch(fn, name: str, index: int, *args):
+    """Call the library with CUDA device `index` current, on its current stream."""
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st != 0:
+        raise BdsaError(name, st)
 
 
-def _arg(t, name: str, dtype, shape, device):
-    """A contiguous CUDA tensor of this dtype and shape on `device`, or None."""
+def _arg(t, name: str, dtype, shape, index: int):
+    """Address of a contiguous tensor of this dtype and shape on CUDA device
+    `index`; None for None."""
     if t is None:
         return None
-    _dev(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError(f"{name} must be a tensor on cuda:{index}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
-
-
-def _status_arg(t, device):
-    return None if t is None else _arg(t, "dev_status", torch.int32, (1,), device)
 
 
 TABLE_KEYS = ("owned", "free_state", "cu_tokens", "slot_map", "positions")
@@ -571,29 +573,34 @@ def block_table_update(seq_lens, new_lens, owned, block_table, free_pages, free_
     (owned and free_state must not be the inputs' memory).
     """
     _dev(block_table, "block_table", torch.int32)
-    dev = block_table.device
+    index = block_table.get_device()
     bs, max_pages = block_table.shape
-    i32 = torch.int32
-    if total_tokens < 0:
+    i32, n = torch.int32, int(total_tokens)
+    if n < 0:
         raise ValueError("total_tokens must be >= 0")
-    num_pages = _dev(free_pages, "free_pages", i32).numel()
-    ins = [_arg(t, n, i32, (bs,), dev) for t, n in
-           ((seq_lens, "seq_lens"), (new_lens, "new_lens"), (owned, "owned"), (shared, "shared"))]
     if out is None:
-        pad = -total_tokens % 4  # slot_map and positions start on 16-byte boundaries
-        buf = torch.empty(2 * (total_tokens + pad) + 2 * bs + 3, dtype=i32, device=dev)
-        slot, _, pos, _, own, cu, state = buf.split([total_tokens, pad, total_tokens, pad, bs,
-                                                     bs + 1, 2])
+        pad = -n % 4  # slot_map and positions start on 16-byte boundaries
+        buf = torch.empty(2 * (n + pad) + 2 * bs + 3, dtype=i32, device=block_table.device)
+        if pad:
+            slot, _, pos, _, own, cu, state = buf.split((n, pad, n, pad, bs, bs + 1, 2))
+        else:
+            slot, pos, own, cu, state = buf.split((n, n, bs, bs + 1, 2))
         out = dict(owned=own, free_state=state, cu_tokens=cu, slot_map=slot, positions=pos)
-    outs = [_arg(out[k], k, i32, n, dev) for k, n in
-            zip(TABLE_KEYS, ((bs,), (2,), (bs + 1,), (total_tokens,), (total_tokens,)))]
-    with _on(dev):
-        st = lib().bdsa_block_table_update(
-            *ins, block_table.data_ptr(), max_pages, num_pages, bs, int(page_size),
-            _arg(free_pages, "free_pages", i32, (num_pages,), dev),
-            _arg(free_state, "free_state", i32, (2,), dev), *outs, int(total_tokens),
-            _status_arg(dev_status, dev), _stream(dev))
-    _check("bdsa_block_table_update", st)
+        p = buf.data_ptr()
+        q = p + 8 * (n + pad)
+        outs = (q, q + 8 * bs + 4, q + 4 * bs, p if n else None, p + 4 * (n + pad) if n else None)
+    else:
+        outs = [_arg(out[k], k, i32, sh, index) for k, sh in
+                zip(TABLE_KEYS, ((bs,), (2,), (bs + 1,), (n,), (n,)))]
+    num_pages = free_pages.numel()
+    _launch(lib().bdsa_block_table_update, "bdsa_block_table_update", index,
+            _arg(seq_lens, "seq_lens", i32, (bs,), index),
+            _arg(new_lens, "new_lens", i32, (bs,), index), _arg(owned, "owned", i32, (bs,), index),
+            _arg(shared, "shared", i32, (bs,), index), block_table.data_ptr(), max_pages,
+            num_pages, bs, int(page_size),
+            _arg(free_pages, "free_pages", i32, (num_pages,), index),
+            _arg(free_state, "free_state", i32, (2,), index), *outs, n,
+            _arg(dev_status, "dev_status", i32, (1,), index))
     return out
 
 
@@ -626,7 +633,7 @@ def token_sample(logits, u=None, *, temperature=None, top_k=None, top_p=None, mi
     if logits.dtype not in _LOGIT_DTYPES:
         raise TypeError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
     bs, B, V = logits.shape
-    dev, f32, i32 = logits.device, torch.float32, torch.int32
+    dev, index, f32, i32 = logits.device, logits.get_device(), torch.float32, torch.int32
     if u is None and tokens is not None:
         raise ValueError("tokens are drawn from u")
     if u is not None and tokens is None:
@@ -636,18 +643,16 @@ def token_sample(logits, u=None, *, temperature=None, top_k=None, top_p=None, mi
     psr = psi = 0
     if probs is not None:
         psr, psi = _rows(probs, "probs")
-        if probs.dtype != f32 or tuple(probs.shape) != (bs, B, V) or probs.device != dev:
+        if probs.dtype is not f32 or probs.shape != (bs, B, V) or probs.get_device() != index:
             raise ValueError(f"probs must be float32 {(bs, B, V)} on {dev}")
     if tokens is None and probs is None:
         raise ValueError("nothing to do: neither u nor probs")
-    with _on(dev):
-        st = lib().bdsa_token_sample(
-            logits.data_ptr(), _LOGIT_DTYPES[logits.dtype], lsr, lsi,
-            _arg(u, "u", f32, (bs, B), dev), _arg(temperature, "temperature", f32, (bs,), dev),
-            _arg(top_k, "top_k", i32, (bs,), dev), _arg(top_p, "top_p", f32, (bs,), dev),
-            _arg(min_p, "min_p", f32, (bs,), dev), bs, B, V,
-            _arg(tokens, "tokens", i32, (bs, B), dev),
+    _launch(lib().bdsa_token_sample, "bdsa_token_sample", index, logits.data_ptr(),
+            _LOGIT_DTYPES[logits.dtype], lsr, lsi, _arg(u, "u", f32, (bs, B), index),
+            _arg(temperature, "temperature", f32, (bs,), index),
+            _arg(top_k, "top_k", i32, (bs,), index), _arg(top_p, "top_p", f32, (bs,), index),
+            _arg(min_p, "min_p", f32, (bs,), index), bs, B, V,
+            _arg(tokens, "tokens", i32, (bs, B), index),
             None if probs is None else probs.data_ptr(), psr, psi, sms,
-            _status_arg(dev_status, dev), _stream(dev))
-    _check("bdsa_token_sample", st)
+            _arg(dev_status, "dev_status", i32, (1,), index))
     return tokens, probs

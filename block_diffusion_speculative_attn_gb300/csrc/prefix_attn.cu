@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                         const long t0 = (long)j * kBN;
                         // pages past the row (reported by the softmax) load nothing
                         int32_t slot[kMaxBoxes];
-    #pragma unroll
+#pragma unroll
                         for (int bx = 0; bx < kMaxBoxes; ++bx) {
                             if (bx >= nbox) break;
                             const long t = t0 + (long)bx * rows_box, page = t >> prm.log2_ps;
@@ -352,12 +352,13 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                                        prm.dev_status);
                         if (!ok) break;
                         mbar_arrive_expect_tx(bar(FULL + st), (uint32_t)C::kTile);
-    #pragma unroll
+#pragma unroll
                         for (int bx = 0; bx < kMaxBoxes; ++bx) {
                             if (bx >= nbox) break;
                             for (int c = 0; c < C::DH; ++c)
-                                tma_load_2d(dst0 + st * C::kTile + c * C::kSlab + bx * rows_box * 128,
-                                            tmap, pc.h * D + c * 64, slot[bx], bar(FULL + st));
+                                tma_load_2d(
+                                    dst0 + st * C::kTile + c * C::kSlab + bx * rows_box * 128,
+                                    tmap, pc.h * D + c * 64, slot[bx], bar(FULL + st));
                         }
                     }
                 }
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                 };
                 auto issue_s = [&](int t, long gk) {
                     const int ks = (int)(gk % C::NK);
-    #pragma unroll
+#pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         umma_bf16(tmem + kS + t * 128,
                                   smem_desc_sw128(sbase + C::kOffQ + t * C::kTile +
@@ -396,10 +397,11 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                 };
                 auto issue_pv = [&](int t, long gv, bool first) {
                     const int vs = (int)(gv % C::NV);
-    #pragma unroll
+#pragma unroll
                     for (int kk = 0; kk < kBN / 16; ++kk)
                         umma_bf16_ts(tmem + kO + t * 128, tmem + kS + t * 128 + kk * 8,
-                                     smem_desc_sw128(sbase + C::kOffV + vs * C::kTile + kk * 16 * 128,
+                                     smem_desc_sw128(sbase + C::kOffV + vs * C::kTile +
+                                                         kk * 16 * 128,
                                                      C::kSlab, 1024),
                                      idesc_pv, (first && kk == 0) ? 0u : 1u);
                 };
@@ -417,7 +419,8 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                     if (!ok) break;
                     umma_commit(bar(C::KE + (int)(g % C::NK)));
                     for (int j = 0; ok && j < n; ++j, ++g) {
-                        if (j + 1 < n) wait(C::KF + (int)((g + 1) % C::NK), (uint32_t)((g + 1) / C::NK));
+                        const long gn = g + 1;  // the next tile's K
+                        if (j + 1 < n) wait(C::KF + (int)(gn % C::NK), (uint32_t)(gn / C::NK));
                         wait(C::VF + (int)(g % C::NV), (uint32_t)(g / C::NV));
                         for (int t = 0; ok && t < nact; ++t) {
                             if (j == 0 && kt[t] > 0) wait(C::OE + t, kt[t] - 1);

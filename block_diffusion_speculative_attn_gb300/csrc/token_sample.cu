@@ -10,21 +10,31 @@
 //   token   = the smallest kept index whose cumulative weight, in index order,
 //             exceeds u * S (the draw rule of the acceptance calls)
 //
-// Arithmetic.  Every weight is held as a 64-bit integer in units of 2^-41 of
-// the row's largest weight, from an exponential good to about 2^-39 (a table of
-// 2^(j/128) and a short series on the float-float remainder).  Integer sums are
-// exact in any order, so the partial sums of threads, warps and CTAs combine
-// freely (shared-memory atomics among them) and a row gives the same answer
-// however it is cut; a draw over 150 k tokens misses the exactly summed one
-// about once in 10^7 rows, where fp32 weights would miss once in a thousand.
+// Arithmetic.  A weight is a float-float (hi + lo, good to about 2^-30 of
+// itself) from a 16-entry table of 2^(j/16) and a short polynomial; sums are
+// kept as 64-bit integers in units of 2^-41 of the row's largest weight.
+// Integer sums are exact in any order, so the partial sums of threads, warps and
+// CTAs combine freely (shared-memory atomics among them) and a row gives the
+// same answer however it is cut.  fp32 weights would not do: over 150 k tokens
+// their rounding moves one draw in about a thousand to a neighbouring token,
+// against one in 10^5 here.
 //
 // Layout.  One thread-block cluster per row, its CTAs the vocabulary slices,
-// each slice resident in shared memory: the logits are read from HBM once,
-// every later pass runs on chip.  The cut is found by radix selection on the
-// logits' ordered bit patterns: each level is a histogram (count and weight) of
-// the keys in the current range over kBins bins, summed over the cluster
-// through distributed shared memory; the bin that holds the cut becomes the
-// next range, until it is a single key.
+// each slice resident in shared memory as fp32: the logits are read from HBM
+// once, every later pass runs on chip.
+//   no filter   one pass for the weights (kept in place of the logits) and their
+//               sum, one that scales and stores them;
+//   filters     a pivot below which nothing can be kept, from the threads' own
+//               maxima (the k-th largest of them is at most the k-th largest
+//               logit, and their weights bound the weight above a pivot from
+//               below); the few logits above it are sorted and cut exactly, the
+//               row is zeros but for the kept ones;
+//   otherwise   (more than kListMax candidates: flat rows, long runs of ties, a
+//               slice that does not fit) radix selection on the logits' ordered
+//               bit patterns: each level is a histogram (count and weight) over
+//               the current key range, summed over the cluster through
+//               distributed shared memory; the bin that holds the cut becomes
+//               the next range, until it is a single key.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -41,14 +51,15 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 512;  // one a thread
 constexpr int kMaxCluster = 8;
+constexpr int kListMax = 1024;  // candidates the sorted list holds
 constexpr int kUnitLog2 = 41;  // a weight's unit is 2^-41 of the row's largest
 constexpr uint32_t kAll = 0xffffffffu;
 
-// ------------------------------------------------------------ 2^(j / 128)
-// hi + lo: the factor as two floats; fix: in units of 2^-kUnitLog2.
+// ------------------------------------------------------------ 2^(j / 16)
+// The factor as hi + lo.  Sixteen 8-byte entries fill the 32 banks of shared
+// memory once, so a warp's lookups never conflict.
 struct ExpTable {
-    float hi[128], lo[128];
-    uint64_t fix[128];
+    float2 v[16];
 };
 constexpr double exp2_series(double x) {  // 2^x for 0 <= x < 1 (Taylor series of e^(x ln 2))
     const double y = x * 0.69314718055994530942;
@@ -61,11 +72,10 @@ constexpr double exp2_series(double x) {  // 2^x for 0 <= x < 1 (Taylor series o
 }
 constexpr ExpTable make_exp_table() {
     ExpTable t{};
-    for (int j = 0; j < 128; ++j) {
-        const double v = exp2_series(j / 128.0);
-        t.hi[j] = (float)v;
-        t.lo[j] = (float)(v - (double)t.hi[j]);
-        t.fix[j] = (uint64_t)(v * (double)(1ull << kUnitLog2) + 0.5);
+    for (int j = 0; j < 16; ++j) {
+        const double v = exp2_series(j / 16.0);
+        t.v[j].x = (float)v;
+        t.v[j].y = (float)(v - (double)(float)v);
     }
     return t;
 }
@@ -76,45 +86,107 @@ struct RowScale {
     float lmax, ch, cl;
 };
 
-// w = 2^(c (l - lmax)): returns it in units of 2^-41 and, in wf, as a float.
-// l - lmax is taken exactly (TwoSum), the product with c as hi + lo, the
-// integer and 1/128 parts go to the shift and the table, and the remainder r,
-// |r| <= 1/256, to 2^r - 1 = s + s^2/2 + s^3/6 + s^4/24, s = r ln 2.
+// One lane value, or a packed pair, with the same operations.
+struct V1 {
+    float a;
+};
+struct V2 {
+    uint64_t a;
+};
+__device__ __forceinline__ V1 operator+(V1 x, V1 y) { return {x.a + y.a}; }
+__device__ __forceinline__ V1 operator*(V1 x, V1 y) { return {x.a * y.a}; }
+__device__ __forceinline__ V1 vfma(V1 x, V1 y, V1 z) { return {fmaf(x.a, y.a, z.a)}; }
+__device__ __forceinline__ V2 operator+(V2 x, V2 y) { return {f2_add(x.a, y.a)}; }
+__device__ __forceinline__ V2 operator*(V2 x, V2 y) { return {f2_mul(x.a, y.a)}; }
+__device__ __forceinline__ V2 vfma(V2 x, V2 y, V2 z) { return {f2_fma(x.a, y.a, z.a)}; }
+template <class V>
+__device__ __forceinline__ V splat(float x);
+template <>
+__device__ __forceinline__ V1 splat<V1>(float x) { return {x}; }
+template <>
+__device__ __forceinline__ V2 splat<V2>(float x) { return {f2_pack(x, x)}; }
+
+// Table entry and power of two of k sixteenths (k <= 0), and whether the weight
+// is above fp32's normal range at all (false for -inf and NaN too).
+__device__ __forceinline__ float2 table_at(const ExpTable &tab, int k) { return tab.v[k & 15]; }
+__device__ __forceinline__ float pow2_at(int k) { return __int_as_float(((k >> 4) + 127) << 23); }
+constexpr float kMinLog2 = -124.f;
+
+__device__ __forceinline__ void lookup(const ExpTable &tab, V1 t, V1 &th, V1 &tl, V1 &sc) {
+    const int k = __float_as_int(t.a) - 0x4B400000;
+    const float2 e = table_at(tab, k);
+    th.a = e.x;
+    tl.a = e.y;
+    sc.a = pow2_at(k);
+}
+__device__ __forceinline__ void lookup(const ExpTable &tab, V2 t, V2 &th, V2 &tl, V2 &sc) {
+    const float2 u = f2_unpack(t.a);
+    const int k0 = __float_as_int(u.x) - 0x4B400000, k1 = __float_as_int(u.y) - 0x4B400000;
+    const float2 e0 = table_at(tab, k0), e1 = table_at(tab, k1);
+    th.a = f2_pack(e0.x, e1.x);
+    tl.a = f2_pack(e0.y, e1.y);
+    sc.a = f2_pack(pow2_at(k0), pow2_at(k1));
+}
+__device__ __forceinline__ void keep_normal(V1 yn, V1 &h, V1 &l) {
+    const bool ok = yn.a < -kMinLog2;
+    h.a = ok ? h.a : 0.f;
+    l.a = ok ? l.a : 0.f;
+}
+__device__ __forceinline__ void keep_normal(V2 yn, V2 &h, V2 &l) {
+    const float2 y = f2_unpack(yn.a);
+    float2 a = f2_unpack(h.a), b = f2_unpack(l.a);
+    if (!(y.x < -kMinLog2)) a.x = b.x = 0.f;
+    if (!(y.y < -kMinLog2)) a.y = b.y = 0.f;
+    h.a = f2_pack(a.x, a.y);
+    l.a = f2_pack(b.x, b.y);
+}
+
+// 2^(c (l - lmax)) as wh + wl, |wl| <= ulp(wh) / 2.  The difference is exact
+// (TwoSum: even of 16-bit logits it can need more than 24 bits), its product
+// with c is -yn + yl, y's sixteenths go to the table and the power of two, and
+// the rest r, |r| <= 1/32, with z = r + yl, to
+//   2^z - 1 = r L + (r Ll + yl L + z^2 (c2 + c3 z + c4 z^2 + c5 z^3)).
+template <class V>
+__device__ __forceinline__ void weight_ff(V l, const RowScale &rs, const ExpTable &tab, V &wh,
+                                          V &wl) {
+    const V one_n = splat<V>(-1.f), lmax = splat<V>(rs.lmax), ch = splat<V>(rs.ch);
+    const V dh = l + splat<V>(-rs.lmax);
+    const V yn = dh * splat<V>(-rs.ch);  // -y >= 0
+    V yl = vfma(dh, ch, yn);
+    yl = vfma(dh, splat<V>(rs.cl), yl);
+    const V bb = vfma(l, one_n, dh);
+    const V dl = vfma(lmax + bb, one_n, vfma(vfma(bb, one_n, dh), one_n, l));
+    yl = vfma(dl, ch, yl);
+    const V t = vfma(yn, splat<V>(-16.f), splat<V>(12582912.f));  // round to an integer
+    const V rn = vfma(t + splat<V>(-12582912.f), splat<V>(0.0625f), yn);  // -r, exact
+    const V r = rn * one_n;
+    constexpr float kL = 0.693147182464599609375f, kLl = -1.904654323148236017e-09f;
+    const V z = r + yl;
+    V h = vfma(z, splat<V>(1.3333558e-3f), splat<V>(9.6181291e-3f));
+    h = vfma(z, h, splat<V>(5.5504109e-2f));
+    h = vfma(z, h, splat<V>(2.40226507e-1f));
+    V lo = vfma(r, splat<V>(kLl), yl * splat<V>(kL));
+    lo = vfma(z * z, h, lo);
+    const V e = vfma(r, splat<V>(kL), lo);
+    V th, tl, sc;
+    lookup(tab, t, th, tl, sc);
+    const V b = vfma(th, e, tl);
+    const V s = th + b;                                // Fast2Sum: s + (b - (s - th)) exactly
+    const V q = vfma(vfma(th, one_n, s), one_n, b);
+    wh = s * sc;
+    wl = q * sc;
+    keep_normal(yn, wh, wl);
+}
+
+constexpr float kUnits = 2199023255552.f;  // 2^kUnitLog2
+
+// The weight in units of 2^-41 of the largest and, in wf, as a float.
 __device__ __forceinline__ uint64_t weight(float l, const RowScale &rs, const ExpTable &tab,
                                            float &wf) {
-    const float dh = l - rs.lmax;
-    const float yh = dh * rs.ch;
-    wf = 0.f;
-    if (!(yh > -125.f)) return 0;  // below every unit and fp32's range (also -inf and NaN)
-    const float bb = dh - l;
-    const float dl = (l - (dh - bb)) - (rs.lmax + bb);
-    const float yl = fmaf(dh, rs.ch, -yh) + fmaf(dh, rs.cl, dl * rs.ch);
-    const float t = fmaf(yh, 128.f, 12582912.f);  // round to an integer
-    const int k = __float_as_int(t) - 0x4B400000;
-    const float r = fmaf(t - 12582912.f, -0.0078125f, yh);
-    constexpr float kL2h = 0.693147182464599609375f, kL2l = -1.904654323148236017e-09f;
-    const float sh = r * kL2h;
-    const float sl = fmaf(r, kL2h, -sh) + fmaf(r, kL2l, yl * kL2h);
-    const float q = fmaf(sh * sh, fmaf(sh, fmaf(sh, 0.041666667f, 0.16666667f), 0.5f), sh * sl);
-    const float lo = sl + q;
-    const int idx = k & 127, n = k >> 7;  // n <= 0
-    const float th = tab.hi[idx], tl = tab.lo[idx];
-    const float ph = th * sh;
-    const float pl = fmaf(th, sh, -ph) + fmaf(th, lo, tl * sh);
-    wf = (th + (ph + (pl + tl))) * __int_as_float((n + 127) << 23);  // n >= -126: normal
-    // the correction ph + pl in units of 2^-41, from 2^-29 and 2^-38 steps
-    // (|ph| < 5.5e-3 and |pl| < 1.5e-5 keep both below 2^22 steps, where adding
-    // 1.5 * 2^23 rounds to an integer)
-    const float m1 = fmaf(ph, 536870912.f, 12582912.f);
-    const int i1 = __float_as_int(m1) - 0x4B400000;
-    const float rem = fmaf(m1 - 12582912.f, -1.862645149230957e-09f, ph) + pl;
-    const float m2 = fmaf(rem, 274877906944.f, 12582912.f);
-    const int i2 = __float_as_int(m2) - 0x4B400000;
-    const int64_t m = (int64_t)tab.fix[idx] + ((int64_t)i1 << 12) + ((int64_t)i2 << 3);
-    const int s = -n;
-    if (s == 0) return (uint64_t)m;
-    if (s > kUnitLog2 + 2) return 0;
-    return ((uint64_t)m + (1ull << (s - 1))) >> s;
+    V1 wh, wl;
+    weight_ff<V1>(V1{l}, rs, tab, wh, wl);
+    wf = wh.a;
+    return (uint64_t)(__float2ll_rn(wh.a * kUnits) + (long long)__float2int_rn(wl.a * kUnits));
 }
 
 // floor(x * v) and ceil(x * v) for a float 0 < x < 1 and an integer v < 2^63,
@@ -141,61 +213,39 @@ __device__ __forceinline__ uint64_t scaled(float x, uint64_t v, bool up) {
 }
 
 // ------------------------------------------------------------ logit types
-// Raw bits, their value, and a key that orders like the value with NaN as the
-// smallest (as -inf) and -0 equal to +0.
+// A logit as fp32 (NaN as -inf, -0 as +0), and the bits of its ordered pattern
+// that are the same for every value of the type.
 template <typename T>
 struct Logit;
 template <>
 struct Logit<float> {
     using Raw = uint32_t;
-    static constexpr Raw kNegInf = 0xff800000u;
-    static __device__ __forceinline__ float value(Raw r) {
-        const float v = __uint_as_float(r);
-        return v == v ? v : -INFINITY;
-    }
-    static __device__ __forceinline__ uint32_t key(Raw r) {
-        const uint32_t b = __float_as_uint(value(r) + 0.f);
-        return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
-    }
-    static __device__ __forceinline__ Raw from_key(uint32_t k) {
-        return k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu);
-    }
-};
-// 16-bit types: the key is the 16-bit pattern's.
-template <typename T>
-struct Logit16 {
-    using Raw = uint16_t;
-    static __device__ __forceinline__ uint32_t key16(float v, Raw r, Raw neg_inf) {
-        uint32_t b = v == v ? r : neg_inf;
-        if (v == 0.f) b = 0;
-        return (b ^ ((b >> 15) ? 0xffffu : 0x8000u)) & 0xffffu;
-    }
-    static __device__ __forceinline__ Raw from_key(uint32_t k) {
-        return (Raw)(k ^ ((k >> 15) ? 0x8000u : 0xffffu));
-    }
+    static constexpr int kKeyShift = 0;
+    static __device__ __forceinline__ float wide(Raw r) { return __uint_as_float(r); }
 };
 template <>
-struct Logit<__nv_bfloat16> : Logit16<__nv_bfloat16> {
-    static constexpr Raw kNegInf = 0xff80;
+struct Logit<__nv_bfloat16> {
+    using Raw = uint16_t;
+    static constexpr int kKeyShift = 16;
     static __device__ __forceinline__ float wide(Raw r) {
         return __uint_as_float((uint32_t)r << 16);
     }
-    static __device__ __forceinline__ float value(Raw r) {
-        const float v = wide(r);
-        return v == v ? v : -INFINITY;
-    }
-    static __device__ __forceinline__ uint32_t key(Raw r) { return key16(wide(r), r, kNegInf); }
 };
 template <>
-struct Logit<__half> : Logit16<__half> {
-    static constexpr Raw kNegInf = 0xfc00;
+struct Logit<__half> {
+    using Raw = uint16_t;
+    static constexpr int kKeyShift = 13;
     static __device__ __forceinline__ float wide(Raw r) { return __half2float(__ushort_as_half(r)); }
-    static __device__ __forceinline__ float value(Raw r) {
-        const float v = wide(r);
-        return v == v ? v : -INFINITY;
-    }
-    static __device__ __forceinline__ uint32_t key(Raw r) { return key16(wide(r), r, kNegInf); }
 };
+__device__ __forceinline__ float clean(float v) { return (v == v ? v : -INFINITY) + 0.f; }
+// Unsigned integers that order like the floats (no NaN, no -0).
+__device__ __forceinline__ uint32_t float_key(float v) {
+    const uint32_t b = __float_as_uint(v);
+    return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float key_float(uint32_t k) {
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
 
 // ------------------------------------------------------------ cluster
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -216,12 +266,9 @@ __device__ __forceinline__ const T *map_to_rank(const T *p, uint32_t rank) {
     return reinterpret_cast<const T *>(out);
 }
 
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int o) {
-    return __shfl_xor_sync(kAll, (unsigned long long)v, o);
-}
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += shfl_xor64(v, o);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, (unsigned long long)v, o);
     return v;
 }
 __device__ __forceinline__ uint64_t warp_scan64(uint64_t v, int lane) {
@@ -240,21 +287,36 @@ struct Hist {
     // counter reaches 2^32
     uint32_t m0[kBins], m1[kBins], m2[kBins];
 };
+// Candidates of the list path: this CTA's, and the cluster's in sorted order
+// (key descending, index ascending, as ~key << 32 | index) with their weights'
+// prefix sums.
+struct Lists {
+    float val[kListMax];
+    int idx[kListMax];
+    uint64_t sorted[kListMax];
+    uint64_t sum[kListMax];
+};
 
 struct Shared {
     ExpTable tab;
-    Hist hist[2];
+    union {
+        Hist hist[2];
+        Lists list;
+    };
+    float tmax[kThreads];         // largest logit of each thread's part of the slice
     uint64_t scan_c[kWarps], scan_m[kWarps];
-    uint64_t wsum[kWarps];        // kept weight of each warp's segment
+    uint64_t wsum[kWarps];        // weight of each warp's segment
     uint32_t wties[kWarps];       // cut-key elements of each warp's segment
+    float red[kWarps];
+    int p_count[2][kWarps];       // pivot search: the warps' shares, by step parity
+    float p_mass[2][kWarps];
+    int n_list, n_below, n_min;   // candidates; those below top-p's goal; past min-p
     // cluster exchange: written by this CTA, read by all, one use each
-    uint32_t x_max, x_min;
-    uint64_t x_sum;
-    uint32_t x_ties;
-    // the bin a select level chose
+    uint64_t x_all, x_sum;
+    uint32_t x_ties, x_min;
+    // the bin a select level chose; the list path's cut
     int bin;
     uint64_t bin_c, bin_m, bin_dc, bin_dm;
-    uint32_t red[2][kWarps];
 };
 
 // A position in the row's order: every key above `key`, and the first `ties`
@@ -269,57 +331,61 @@ struct Level {
     uint64_t c, m, dc, dm;
 };
 
+// This CTA's slice.  Positions x run over [0, n) = vocabulary indices e0 + x -
+// pad; resident slices hold them in shared memory as fp32, with -inf in the pad
+// positions in front and behind (n is a multiple of 128 then).
 template <typename T, bool kResident>
 struct Row {
     using L = Logit<T>;
-    using Raw = typename L::Raw;
-    const Raw *s;      // the slice: shared memory, or global memory
-    const Raw *g;
-    int n;             // elements of the slice
+    const float *s;
+    const typename L::Raw *g;
+    int n, pad, len;   // len: the slice's logits
     bool inf;          // the row's maximum is +inf: +inf counts as 0, the rest as -inf
-    __device__ __forceinline__ Raw raw(int i) const { return kResident ? s[i] : __ldg(g + i); }
-    __device__ __forceinline__ float value(Raw r) const {
-        const float v = L::value(r);
+    __device__ __forceinline__ float at(int x) const {
+        if (kResident) return s[x];
+        const float v = clean(L::wide(__ldg(g + x)));
         return inf ? (v == INFINITY ? 0.f : -INFINITY) : v;
+    }
+    static __device__ __forceinline__ uint32_t key(float v) { return float_key(v) >> L::kKeyShift; }
+    // a float of the type with this key
+    static __device__ __forceinline__ float value(uint32_t key) {
+        const float v = key_float(key << L::kKeyShift);
+        return key >> (31 - L::kKeyShift) ? v : key_float((key << L::kKeyShift) |
+                                                          ((1u << L::kKeyShift) - 1));
     }
 };
 
-// One histogram level over the keys in [klo, khi], bin 0 the highest keys.
-// kMass: weights too.  Every thread of every CTA of the cluster ends with its
-// bin's totals over the cluster.
-template <bool kMass, class R>
+// One histogram level over the keys in [klo, khi], bin 0 the highest keys.  Every
+// thread of every CTA of the cluster ends with its bin's totals over the cluster.
+template <class R>
 __device__ Level level_hist(const R &row, Shared &sm, int buf, uint32_t klo, uint32_t khi,
                             int shift, const RowScale &rs, uint32_t ncta) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Hist &h = sm.hist[buf];
     h.cnt[tid] = h.m0[tid] = h.m1[tid] = h.m2[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < row.n; i += kThreads) {
-        const auto raw = row.raw(i);
-        const uint32_t key = R::L::key(raw);
+    for (int x = tid; x < row.n; x += kThreads) {
+        const float v = row.at(x);
+        const uint32_t key = R::key(v);
         if (key < klo || key > khi) continue;
         const uint32_t b = (khi - key) >> shift;
+        float wf;
+        const uint64_t w = weight(v, rs, sm.tab, wf);
+        const uint32_t l0 = (uint32_t)w & 0x3fffu, l1 = (uint32_t)(w >> 14) & 0x3fffu;
+        const uint32_t l2 = (uint32_t)(w >> 28);
         atomicAdd(&h.cnt[b], 1u);
-        if (kMass) {
-            float wf;
-            const uint64_t w = weight(row.value(raw), rs, sm.tab, wf);
-            const uint32_t l0 = (uint32_t)w & 0x3fffu, l1 = (uint32_t)(w >> 14) & 0x3fffu;
-            const uint32_t l2 = (uint32_t)(w >> 28);
-            if (l0) atomicAdd(&h.m0[b], l0);
-            if (l1) atomicAdd(&h.m1[b], l1);
-            if (l2) atomicAdd(&h.m2[b], l2);
-        }
+        if (l0) atomicAdd(&h.m0[b], l0);
+        if (l1) atomicAdd(&h.m1[b], l1);
+        if (l2) atomicAdd(&h.m2[b], l2);
     }
     cluster_sync();
     Level lv{0, 0, 0, 0};
     for (uint32_t r = 0; r < ncta; ++r) {
         const Hist *o = map_to_rank(&h, r);
         lv.dc += o->cnt[tid];
-        if (kMass)
-            lv.dm += (uint64_t)o->m0[tid] + ((uint64_t)o->m1[tid] << 14) +
-                     ((uint64_t)o->m2[tid] << 28);
+        lv.dm += (uint64_t)o->m0[tid] + ((uint64_t)o->m1[tid] << 14) + ((uint64_t)o->m2[tid] << 28);
     }
-    uint64_t ic = warp_scan64(lv.dc, lane), im = kMass ? warp_scan64(lv.dm, lane) : 0;
+    uint64_t ic = warp_scan64(lv.dc, lane), im = warp_scan64(lv.dm, lane);
     if (lane == 31) {
         sm.scan_c[warp] = ic;
         sm.scan_m[warp] = im;
@@ -344,7 +410,7 @@ __device__ __forceinline__ int range_shift(uint32_t klo, uint32_t khi) {
 // The shortest prefix of the order with at least `target` elements (kMass
 // false) or at least `target` weight (kMass true; 0 < target <= the row's
 // weight).  `lv` is the level over [klo, khi].  above_m: the weight of the keys
-// above the cut's.
+// above the cut's; key_count: the elements with the cut's key.
 template <bool kMass, class R>
 __device__ Cut select_cut(const R &row, Shared &sm, int &buf, Level lv, uint32_t klo,
                           uint32_t khi, uint64_t target, const RowScale &rs, uint32_t ncta,
@@ -365,6 +431,7 @@ __device__ Cut select_cut(const R &row, Shared &sm, int &buf, Level lv, uint32_t
         }
         __syncthreads();
         const int b = sm.bin;
+        const uint64_t dc = sm.bin_dc, dm = sm.bin_dm;
         if (b < 0) {  // (never: the target is within the range's total)
             above_m = base_m;
             key_count = 0;
@@ -372,7 +439,6 @@ __device__ Cut select_cut(const R &row, Shared &sm, int &buf, Level lv, uint32_t
         }
         base_c += sm.bin_c;
         base_m += sm.bin_m;
-        const uint64_t dc = sm.bin_dc, dm = sm.bin_dm;
         __syncthreads();
         khi -= (uint32_t)b << shift;
         const uint32_t span = shift ? (1u << shift) - 1 : 0;
@@ -380,7 +446,7 @@ __device__ Cut select_cut(const R &row, Shared &sm, int &buf, Level lv, uint32_t
         if (shift == 0) {
             Cut c;
             c.key = khi;
-            const uint64_t w = dm / dc;  // equal keys, equal weights
+            const uint64_t w = kMass ? dm / dc : 0;  // equal keys, equal weights
             c.ties = kMass ? (target - base_m + w - 1) / w : target - base_c;
             above_m = base_m;
             key_count = dc;
@@ -388,8 +454,78 @@ __device__ Cut select_cut(const R &row, Shared &sm, int &buf, Level lv, uint32_t
         }
         buf ^= 1;
         shift = range_shift(klo, khi);
-        lv = level_hist<true>(row, sm, buf, klo, khi, shift, rs, ncta);
+        lv = level_hist(row, sm, buf, klo, khi, shift, rs, ncta);
     }
+}
+
+// Ascending bitonic sort of a[0, n) (n a power of two) by the whole CTA.
+__device__ __forceinline__ void bitonic_sort(uint64_t *a, int n) {
+    for (int k = 2; k <= n; k <<= 1) {
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            for (int p = threadIdx.x; p < n / 2; p += kThreads) {
+                const int i = ((p & ~(j - 1)) << 1) | (p & (j - 1)), q = i | j;
+                const uint64_t x = a[i], y = a[q];
+                if ((x > y) == ((i & k) == 0)) {
+                    a[i] = y;
+                    a[q] = x;
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// Inclusive prefix sums of v over the CTA's threads (0 elsewhere), in thread order.
+__device__ __forceinline__ uint64_t block_scan64(uint64_t v, Shared &sm) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t t = warp_scan64(v, lane);
+    if (lane == 31) sm.scan_m[warp] = t;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) t += sm.scan_m[w];
+    __syncthreads();
+    return t;
+}
+// Prefix sums of a[0, n), n <= kListMax, in place (two entries a thread).
+__device__ __forceinline__ void scan_list(uint64_t *a, int n, Shared &sm) {
+    static_assert(kListMax == 2 * kThreads, "two entries a thread");
+    const int i = 2 * threadIdx.x;
+    const uint64_t x = i < n ? a[i] : 0, y = i + 1 < n ? a[i + 1] : 0;
+    const uint64_t t = block_scan64(x + y, sm);
+    if (i < n) a[i] = t - y;
+    if (i + 1 < n) a[i + 1] = t;
+    __syncthreads();
+}
+
+// The weight of positions [x0, x1) of a resident slice (multiples of 128), summed
+// by one warp, four positions a lane and step.  kStore: the weights replace the
+// logits.  Returns the lane's sum in units.
+template <bool kStore>
+__device__ __forceinline__ uint64_t sum_weights(float *s, int x0, int x1, const RowScale &rs,
+                                                const ExpTable &tab, int lane) {
+    const V2 neg = splat<V2>(-1.f);
+    V2 acc = splat<V2>(0.f), low = splat<V2>(0.f);
+    auto add = [&](V2 h, V2 l) {  // TwoSum
+        const V2 t = acc + h;
+        const V2 hh = vfma(acc, neg, t);
+        const V2 err = vfma(vfma(hh, neg, t), neg, acc) + vfma(hh, neg, h);
+        acc = t;
+        low = low + (err + l);
+    };
+    for (int x = x0 + 4 * lane; x < x1; x += 128) {
+        const float4 v = *reinterpret_cast<const float4 *>(s + x);
+        V2 h0, l0, h1, l1;
+        weight_ff<V2>(V2{f2_pack(v.x, v.y)}, rs, tab, h0, l0);
+        weight_ff<V2>(V2{f2_pack(v.z, v.w)}, rs, tab, h1, l1);
+        add(h0, l0);
+        add(h1, l1);
+        if (kStore) {
+            const float2 a = f2_unpack(h0.a), b = f2_unpack(h1.a);
+            *reinterpret_cast<float4 *>(s + x) = make_float4(a.x, a.y, b.x, b.y);
+        }
+    }
+    const float2 a = f2_unpack(acc.a), b = f2_unpack(low.a);
+    return (uint64_t)(__float2ll_rn(a.x * kUnits) + __float2ll_rn(a.y * kUnits) +
+                      __float2ll_rn(b.x * kUnits) + __float2ll_rn(b.y * kUnits));
 }
 
 template <typename T, bool kResident>
@@ -399,103 +535,126 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
     using Raw = typename L::Raw;
     extern __shared__ __align__(16) uint8_t s_dyn[];
     __shared__ Shared sm;
+    float *slice = reinterpret_cast<float *>(s_dyn);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ncta = (uint32_t)a.ncta, rank = ncta > 1 ? cluster_rank() : 0u;
     const long rowi = blockIdx.x / ncta;
     const int r = (int)(rowi / a.B), i = (int)(rowi % a.B);
     const Raw *grow = static_cast<const Raw *>(a.logits) + r * a.lsr + i * a.lsi;
     const int e0 = min(a.V, (int)rank * a.slice), e1 = min(a.V, e0 + a.slice);
+    constexpr int kVec = 16 / (int)sizeof(Raw);
+    const Raw *gs = grow + e0;  // the slice
     R row;
-    row.g = grow + e0;
-    row.n = e1 - e0;
+    row.g = gs;
+    row.s = slice;
+    row.len = e1 - e0;
+    // logits from the 16-byte boundary at or before the slice; a resident slice
+    // keeps that offset
+    const int mis = (int)((reinterpret_cast<uintptr_t>(gs) & 15) / sizeof(Raw));
+    row.pad = kResident ? mis : 0;
+    row.n = kResident ? (row.len + row.pad + 127) & ~127 : row.len;
     row.inf = false;
 
     // ---- this row's parameters
-    float temp = a.temperature ? a.temperature[r] : 1.f;
+    const float temp = a.temperature ? a.temperature[r] : 1.f;
     const int top_k = a.top_k ? a.top_k[r] : 0;
     const float top_p = a.top_p ? a.top_p[r] : 1.f;
     const float min_p = a.min_p ? a.min_p[r] : 0.f;
     const bool bad_temp = !(temp >= 0.f) || temp == INFINITY;
     const bool greedy = temp == 0.f;
     const bool one = greedy || min_p > 1.f;  // only the first of the order is kept
-
-    for (int j = tid; j < 128; j += kThreads) {
-        sm.tab.hi[j] = g_exp_table.hi[j];
-        sm.tab.lo[j] = g_exp_table.lo[j];
-        sm.tab.fix[j] = g_exp_table.fix[j];
-    }
-    // ---- the slice into shared memory, its largest key and smallest key above
-    // -inf's.  The copy keeps the slice's offset from a 16-byte boundary.
-    constexpr int kVec = 16 / (int)sizeof(Raw);
-    const uint32_t kNegInf = L::key(L::kNegInf);
-    uint32_t kmax = 0, kmin = 0xffffffffu;
-    auto take = [&](Raw v) {
-        const uint32_t k = L::key(v);
-        kmax = max(kmax, k);
-        if (k > kNegInf) kmin = min(kmin, k);
-    };
-    const int mis = (int)((reinterpret_cast<uintptr_t>(row.g) & 15) / sizeof(Raw));
-    const int head = min(row.n, mis ? kVec - mis : 0);
-    const int nvec = (row.n - head) / kVec, tail0 = head + nvec * kVec;
-    Raw *dst = reinterpret_cast<Raw *>(s_dyn) + mis;
-    row.s = dst;
-    if (tid < head) {
-        const Raw v = __ldg(row.g + tid);
-        if (kResident) dst[tid] = v;
-        take(v);
-    }
-    if (tid < row.n - tail0) {
-        const Raw v = __ldg(row.g + tail0 + tid);
-        if (kResident) dst[tail0 + tid] = v;
-        take(v);
-    }
-    const uint4 *gv = reinterpret_cast<const uint4 *>(row.g + head);
-    uint4 *sv = reinterpret_cast<uint4 *>(dst + head);
-#pragma unroll 4
-    for (int x = tid; x < nvec; x += kThreads) {
-        const uint4 q = __ldg(gv + x);
-        if (kResident) sv[x] = q;
-        const Raw *e = reinterpret_cast<const Raw *>(&q);
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) take(e[k]);
-    }
-    kmax = __reduce_max_sync(kAll, kmax);
-    kmin = __reduce_min_sync(kAll, kmin);
-    if (lane == 0) {
-        sm.red[0][warp] = kmax;
-        sm.red[1][warp] = kmin;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        kmax = __reduce_max_sync(kAll, lane < kWarps ? sm.red[0][lane] : 0u);
-        kmin = __reduce_min_sync(kAll, lane < kWarps ? sm.red[1][lane] : 0xffffffffu);
-        if (lane == 0) {
-            sm.x_max = kmax;
-            sm.x_min = kmin;
-        }
-    }
-    cluster_sync();
-    kmax = 0;
-    kmin = 0xffffffffu;
-    for (uint32_t c = 0; c < ncta; ++c) {
-        kmax = max(kmax, *map_to_rank(&sm.x_max, c));
-        kmin = min(kmin, *map_to_rank(&sm.x_min, c));
-    }
+    const bool use_k = one || (top_k > 0 && top_k < a.V);
+    const bool use_p = !one && top_p < 1.f;
+    const bool use_m = !one && min_p > 0.f;
+    const bool filtered = use_k || use_p || use_m;
     float *prow = a.probs ? a.probs + r * a.psr + i * a.psi + e0 : nullptr;
-    if (bad_temp || kmax <= kNegInf) {  // no distribution (uniform over the cluster)
+    if (tid < 16) sm.tab.v[tid] = g_exp_table.v[tid];
+    if (tid == 0) sm.n_list = sm.n_below = sm.n_min = 0;
+
+    // ---- the slice into shared memory, the largest logit of each thread's part
+    float mx = -INFINITY;
+    {
+        const int head = min(row.len, mis ? kVec - mis : 0);
+        const int nvec = (row.len - head) / kVec, tail = head + nvec * kVec;
+        float *dst = slice + row.pad;
+        if (tid < head) {
+            mx = clean(L::wide(__ldg(gs + tid)));
+            if (kResident) dst[tid] = mx;
+        }
+        if (tid < row.len - tail) {
+            const float v = clean(L::wide(__ldg(gs + tail + tid)));
+            if (kResident) dst[tail + tid] = v;
+            mx = fmaxf(mx, v);
+        }
+        if (kResident) {
+            if (tid < row.pad) slice[tid] = -INFINITY;
+            if (tid < row.n - row.pad - row.len) dst[row.len + tid] = -INFINITY;
+        }
+        const uint4 *gv = reinterpret_cast<const uint4 *>(gs + head);
+        float *sv = dst + head;
+        auto take = [&](uint4 q, int x) {
+            const Raw *e = reinterpret_cast<const Raw *>(&q);
+#pragma unroll
+            for (int k = 0; k < kVec; k += 4) {
+                float4 v;
+                v.x = clean(L::wide(e[k]));
+                v.y = clean(L::wide(e[k + 1]));
+                v.z = clean(L::wide(e[k + 2]));
+                v.w = clean(L::wide(e[k + 3]));
+                mx = max3f(max3f(mx, v.x, v.y), v.z, v.w);
+                if (kResident) *reinterpret_cast<float4 *>(sv + x * kVec + k) = v;
+            }
+        };
+        constexpr int kU = 4;  // loads in flight a thread
+        int x = tid;
+        for (; x + (kU - 1) * kThreads < nvec; x += kU * kThreads) {
+            uint4 q[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) q[u] = __ldcs(gv + x + u * kThreads);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) take(q[u], x + u * kThreads);
+        }
+        for (; x < nvec; x += kThreads) take(__ldcs(gv + x), x);
+    }
+    sm.tmax[tid] = mx;
+    cluster_sync();
+    // every CTA takes the row's thread maxima: ncta a thread
+    float tm[kMaxCluster];
+    mx = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) {
+        tm[c] = c < ncta ? map_to_rank(sm.tmax, c)[tid] : -INFINITY;
+        mx = fmaxf(mx, tm[c]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+    if (lane == 0) sm.red[warp] = mx;
+    __syncthreads();
+    mx = sm.red[lane % kWarps];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+    if (bad_temp || mx == -INFINITY) {  // no distribution (uniform over the cluster)
         if (prow)
-            for (int x = tid; x < row.n; x += kThreads) prow[x] = 0.f;
+            for (int x = tid; x < row.len; x += kThreads) prow[x] = 0.f;
         if (rank == 0 && tid == 0) {
             if (a.tokens) a.tokens[rowi] = -1;
             report_status(a.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
         }
-        cluster_sync();  // x_max / x_min have been read everywhere
+        cluster_sync();  // tmax has been read everywhere
         return;
     }
     RowScale rs;
-    rs.lmax = L::value(L::from_key(kmax));
-    row.inf = rs.lmax == INFINITY;
-    if (row.inf) rs.lmax = 0.f;
+    rs.lmax = mx;
+    if (mx == INFINITY) {  // the +inf logits share the weight
+        row.inf = true;
+        rs.lmax = 0.f;
+        if (kResident)
+            for (int x = tid; x < row.n; x += kThreads)
+                slice[x] = slice[x] == INFINITY ? 0.f : -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) tm[c] = tm[c] == INFINITY ? 0.f : -INFINITY;
+        __syncthreads();
+    }
     {
         // temperatures below 1e-30 act as 1e-30 (greedy rows weigh every kept
         // logit alike: only one is kept)
@@ -503,16 +662,336 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
         rs.ch = (float)c;
         rs.cl = (float)(c - (double)rs.ch);
     }
-    if (row.inf) kmin = kmax;  // only the +inf logits have weight
+    const float u = a.tokens ? a.u[rowi] : 0.f;
+    // floor(u * total), below total; u outside [0, 1) is clamped
+    auto draw_target = [&](uint64_t total) -> uint64_t {
+        return u > 0.f ? (u < 1.f ? scaled(u, total, false) : total - 1) : 0;
+    };
+    const int seg = ((row.n + kWarps - 1) / kWarps + 127) & ~127;
+    const int w0 = min(row.n, warp * seg), w1 = min(row.n, w0 + seg);
 
-    // ---- the cut
-    Cut cut{0, ~0ull};  // everything
+    // ================================================= no filter
+    if (kResident && !filtered) {
+        uint64_t sum = prow ? sum_weights<true>(slice, w0, w1, rs, sm.tab, lane)
+                            : sum_weights<false>(slice, w0, w1, rs, sm.tab, lane);
+        sum = warp_sum64(sum);
+        if (lane == 0) sm.wsum[warp] = sum;
+        __syncthreads();
+        if (tid == 0) {
+            uint64_t t = 0;
+            for (int w = 0; w < kWarps; ++w) t += sm.wsum[w];
+            sm.x_sum = t;
+        }
+        cluster_sync();
+        uint64_t total = 0, before = 0;
+        for (uint32_t c = 0; c < ncta; ++c) {
+            const uint64_t t = *map_to_rank(&sm.x_sum, c);
+            if (c < rank) before += t;
+            total += t;
+        }
+        if (a.tokens) {
+            const uint64_t target = draw_target(total);
+            for (int w = 0; w < warp; ++w) before += sm.wsum[w];
+            if (before <= target && target < before + sum) {
+                // this warp's segment holds the draw: its weights again, from
+                // the input (single weights round to units, so the last
+                // positive one takes a target past their sum)
+                int last = -1;
+                bool found = false;
+                for (int x0 = w0; x0 < w1 && !found; x0 += 128) {
+                    uint64_t w[4], s4 = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int e = x0 + 4 * lane + k - row.pad;
+                        float v = e >= 0 && e < row.len ? clean(L::wide(__ldg(gs + e))) : -INFINITY;
+                        if (row.inf) v = v == INFINITY ? 0.f : -INFINITY;
+                        float wf;
+                        w[k] = weight(v, rs, sm.tab, wf);
+                        s4 += w[k];
+                    }
+                    const uint64_t inc = warp_scan64(s4, lane);
+                    const unsigned hit = __ballot_sync(kAll, before + inc > target);
+                    const unsigned pos = __ballot_sync(kAll, s4 > 0);
+                    const int src = hit ? __ffs(hit) - 1 : pos ? 31 - __clz(pos) : -1;
+                    if (lane == src) {
+                        uint64_t c = before + inc - s4;
+                        for (int k = 0; k < 4; ++k) {
+                            c += w[k];
+                            if (w[k]) last = x0 + 4 * lane + k;
+                            if (c > target) break;
+                        }
+                    }
+                    if (src >= 0) last = __shfl_sync(kAll, last, src);
+                    found = hit != 0;
+                    before += __shfl_sync(kAll, (unsigned long long)inc, 31);
+                }
+                if (lane == 0) a.tokens[rowi] = e0 + last - row.pad;
+            }
+        }
+        if (prow) {
+            const float inv = (float)((double)(1ull << kUnitLog2) / (double)total);
+            float *out = prow - row.pad;
+            if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+                for (int x = w0 + 4 * lane; x < w1; x += 128) {
+                    const float4 v = *reinterpret_cast<const float4 *>(slice + x);
+                    if (x >= row.pad && x + 4 <= row.pad + row.len) {
+                        __stcs(reinterpret_cast<float4 *>(out + x),
+                               make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                    } else {
+                        const float e[4] = {v.x, v.y, v.z, v.w};
+                        for (int k = 0; k < 4; ++k)
+                            if (x + k >= row.pad && x + k < row.pad + row.len)
+                                out[x + k] = e[k] * inv;
+                    }
+                }
+            } else {
+                __syncwarp();
+                for (int x = w0 + lane; x < w1; x += 32)
+                    if (x >= row.pad && x < row.pad + row.len) out[x] = slice[x] * inv;
+            }
+        }
+        cluster_sync();  // x_sum has been read everywhere
+        return;
+    }
+
+    // ================================================= filters, by a sorted list
+    const uint64_t wmin =
+        use_m ? (min_p >= 1.f ? 1ull << kUnitLog2 : scaled(min_p, 1ull << kUnitLog2, true)) : 0;
+    const uint64_t want_k = one ? 1u : (uint64_t)top_k;
+    uint64_t all_sum = 0;  // the row's weight (top-p without top-k)
+    if (kResident && filtered) {
+        if (use_p && !use_k) {
+            uint64_t sum = warp_sum64(
+                sum_weights<false>(slice, w0, w1, rs, sm.tab, lane));
+            if (lane == 0) sm.wsum[warp] = sum;
+            __syncthreads();
+            if (tid == 0) {
+                uint64_t t = 0;
+                for (int w = 0; w < kWarps; ++w) t += sm.wsum[w];
+                sm.x_all = t;
+            }
+            cluster_sync();
+            for (uint32_t c = 0; c < ncta; ++c) all_sum += *map_to_rank(&sm.x_all, c);
+        }
+        // ---- pivot: nothing below it is kept
+        float pivot = -INFINITY;
+        bool list = true;
+        // (top-p within top-k takes its share of all k, min-p's losers included)
+        const bool by_m = use_m && !(use_k && use_p);
+        if (by_m) {
+            // w >= m iff l >= lmax + T ln m, less the rounding of both sides
+            const float t = __logf(fminf(min_p, 1.f)) / (rs.ch * 0.693147181f);
+            pivot = rs.lmax + t * (t < 0.f ? 1.0001f : 1.f) - 1e-4f * fabsf(rs.lmax) - 1e-5f;
+        }
+        if ((use_k || use_p) && a.V > kListMax) {
+            // the largest p with enough of the threads' maxima at or above it:
+            // want_k of them, or weight for the top-p goal (a margin covers the
+            // fp32 sums; the exact cut below checks it)
+            const float goal = use_k ? 0.f
+                                     : fminf(top_p, 1.f) * (float)all_sum * (1.f / kUnits) * 1.0001f;
+            uint32_t lo = float_key(-INFINITY), hi = float_key(rs.lmax);
+            const int need = (int)min(want_k, (uint64_t)kListMax + 1);
+            float tw[kMaxCluster];
+            if (!use_k) {
+#pragma unroll
+                for (int c = 0; c < kMaxCluster; ++c) weight(tm[c], rs, sm.tab, tw[c]);
+            }
+            // lo passes (every maximum), unless there are too few of them
+            bool lo_ok = false;
+            for (int step = 0; step < 33; ++step) {
+                // the first step asks about lo itself
+                const uint32_t mid = step == 0 ? lo + 1 : lo + (hi - lo + 1) / 2;
+                const float p = key_float(mid);
+                int n = 0;
+                float w = 0.f;
+#pragma unroll
+                for (int c = 0; c < kMaxCluster; ++c) {
+                    if (tm[c] >= p) {
+                        ++n;
+                        if (!use_k) w += tw[c];
+                    }
+                }
+                n = __reduce_add_sync(kAll, n);
+                if (!use_k) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(kAll, w, o);
+                }
+                if (lane == 0) {
+                    sm.p_count[step & 1][warp] = n;
+                    sm.p_mass[step & 1][warp] = w;
+                }
+                __syncthreads();
+                // (the same order of additions in every CTA of the cluster: they
+                // must agree on the pivot)
+                n = 0;
+                w = 0.f;
+#pragma unroll
+                for (int q = 0; q < kWarps; ++q) {
+                    n += sm.p_count[step & 1][q];
+                    w += sm.p_mass[step & 1][q];
+                }
+                const bool ok = use_k ? n >= need : w >= goal;
+                if (step == 0) {
+                    if (!ok) break;
+                    lo_ok = true;
+                }
+                if (ok) lo = mid;
+                else hi = mid - 1;
+                if (lo >= hi) break;
+                // near enough: a few more candidates cost less than the search
+                if (use_k && ok && n <= need + need / 4 + 16) break;
+            }
+            if (lo_ok) pivot = fmaxf(pivot, key_float(lo));
+            else list = by_m;
+        }
+        // ---- candidates of the slice
+        if (list) {
+            for (int x = 4 * tid; x < row.n; x += 4 * kThreads) {
+                const float4 v = *reinterpret_cast<const float4 *>(slice + x);
+                if (max3f(fmaxf(v.x, v.y), v.z, v.w) < pivot) continue;
+                const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (e[k] < pivot || e[k] == -INFINITY) continue;
+                    const int at = atomicAdd(&sm.n_list, 1);
+                    if (at < kListMax) {
+                        sm.list.val[at] = e[k];
+                        sm.list.idx[at] = e0 + x + k - row.pad;
+                    }
+                }
+            }
+        }
+        cluster_sync();
+        int n = 0;
+        if (list) {
+            for (uint32_t c = 0; c < ncta; ++c) {
+                const Shared *o = reinterpret_cast<const Shared *>(map_to_rank(&sm, c));
+                const int m = o->n_list;
+                if (n + m <= kListMax) {
+                    for (int x = tid; x < m; x += kThreads)
+                        sm.list.sorted[n + x] =
+                            (uint64_t)~float_key(o->list.val[x]) << 32 | (uint32_t)o->list.idx[x];
+                }
+                n += m;
+            }
+            list = n <= kListMax && n > 0;
+        }
+        // ---- the exact cut
+        if (list) {  // (uniform over the cluster)
+            int np = 2;
+            while (np < n) np <<= 1;
+            for (int x = n + tid; x < np; x += kThreads) sm.list.sorted[x] = ~0ull;
+            __syncthreads();
+            bitonic_sort(sm.list.sorted, np);
+            uint64_t *cum = sm.list.sum;
+            for (int x = tid; x < n; x += kThreads) {
+                float wf;
+                cum[x] = weight(key_float(~(uint32_t)(sm.list.sorted[x] >> 32)), rs, sm.tab, wf);
+            }
+            __syncthreads();
+            // (min-p: weights fall with the rank, so the first n_m pass)
+            int nm = 0;
+            for (int x = tid; x < n; x += kThreads) nm += cum[x] >= wmin;
+            scan_list(cum, n, sm);
+            int nk = n;
+            if (use_k) nk = (int)min((uint64_t)n, want_k);
+            int keep = nk;
+            if (use_p) {
+                const uint64_t base = use_k ? cum[nk - 1] : all_sum;
+                const uint64_t goal =
+                    top_p > 0.f ? max((uint64_t)1, scaled(top_p, base, true)) : 1;
+                // (the list may stop short of the goal only when the pivot of
+                // min-p cut it: min-p then keeps no more than the list)
+                int below = 0;
+                for (int x = tid; x < nk; x += kThreads) below += cum[x] < goal;
+                below = __reduce_add_sync(kAll, below);
+                if (lane == 0) atomicAdd(&sm.n_below, below);
+                __syncthreads();
+                keep = min(keep, sm.n_below + 1);
+                if (!use_k && !use_m && sm.n_below == n) list = false;  // short of the goal
+            }
+            if (use_m) {
+                nm = __reduce_add_sync(kAll, nm);
+                if (lane == 0) atomicAdd(&sm.n_min, nm);
+                __syncthreads();
+                keep = min(keep, sm.n_min);
+            }
+            keep = max(keep, 1);
+            if (list) {
+                const uint64_t total = cum[keep - 1];
+                const float inv = (float)((double)(1ull << kUnitLog2) / (double)total);
+                if (prow) {
+                    // zeros, then the kept ones of this slice
+                    const int lead =
+                        min(row.len, (int)((16 - (reinterpret_cast<uintptr_t>(prow) & 15)) / 4) & 3);
+                    const int quads = (row.len - lead) / 4;
+                    if (tid < lead) prow[tid] = 0.f;
+                    for (int x = tid; x < quads; x += kThreads)
+                        __stcs(reinterpret_cast<float4 *>(prow + lead) + x,
+                               make_float4(0.f, 0.f, 0.f, 0.f));
+                    if (tid < row.len - lead - 4 * quads) prow[lead + 4 * quads + tid] = 0.f;
+                    __syncthreads();
+                    for (int x = tid; x < keep; x += kThreads) {
+                        const uint64_t sv = sm.list.sorted[x];
+                        const int e = (int)(uint32_t)sv - e0;
+                        if (e < 0 || e >= row.len) continue;
+                        float wf;
+                        weight(key_float(~(uint32_t)(sv >> 32)), rs, sm.tab, wf);
+                        prow[e] = wf * inv;
+                    }
+                }
+                if (a.tokens && rank == 0) {
+                    // the kept ones in index order: index << 32 | rank, their
+                    // weights the differences of the rank order's sums
+                    const uint64_t target = draw_target(total);
+                    __syncthreads();
+                    int kp = 2;
+                    while (kp < keep) kp <<= 1;
+                    for (int x = tid; x < kp; x += kThreads)
+                        sm.list.sorted[x] =
+                            x < keep ? sm.list.sorted[x] << 32 | (uint32_t)x : ~0ull;
+                    __syncthreads();
+                    bitonic_sort(sm.list.sorted, kp);
+                    uint64_t w[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int x = 2 * tid + k;
+                        const uint32_t q = x < keep ? (uint32_t)sm.list.sorted[x] : 0u;
+                        w[k] = x < keep ? cum[q] - (q ? cum[q - 1] : 0) : 0;
+                    }
+                    const uint64_t t = block_scan64(w[0] + w[1], sm);
+                    const uint64_t t0 = t - w[1];
+                    if (t0 > target && t0 - w[0] <= target)
+                        a.tokens[rowi] = (int)(sm.list.sorted[2 * tid] >> 32);
+                    if (t > target && t0 <= target)
+                        a.tokens[rowi] = (int)(sm.list.sorted[2 * tid + 1] >> 32);
+                }
+                cluster_sync();  // the lists have been read everywhere
+                return;
+            }
+        }
+        cluster_sync();  // the lists have been read everywhere: the histograms may follow
+    }
+
+    // ================================================= any row, by selection
+    Cut cut{0, ~0ull};       // everything
     uint64_t key_count = 0;  // elements with the cut's key
-    const bool use_k = one || (top_k > 0 && top_k < a.V);
-    const bool use_p = !one && top_p < 1.f;
     if (use_k || use_p) {
+        // the smallest key above -inf's
+        const uint32_t kmax = R::key(rs.lmax), kinf = R::key(-INFINITY);
+        uint32_t kmin = kmax;
+        for (int x = tid; x < row.n; x += kThreads) {
+            const uint32_t k = R::key(row.at(x));
+            if (k > kinf) kmin = min(kmin, k);
+        }
+        kmin = __reduce_min_sync(kAll, kmin);
+        if (tid == 0) sm.x_min = kmax;
+        __syncthreads();
+        if (lane == 0) atomicMin(&sm.x_min, kmin);
+        cluster_sync();
+        for (uint32_t c = 0; c < ncta; ++c) kmin = min(kmin, *map_to_rank(&sm.x_min, c));
         int buf = 0;
-        const Level lv = level_hist<true>(row, sm, buf, kmin, kmax, range_shift(kmin, kmax), rs, ncta);
+        const Level lv = level_hist(row, sm, buf, kmin, kmax, range_shift(kmin, kmax), rs, ncta);
         // totals of the range (the last thread's inclusive prefix)
         if (tid == kThreads - 1) {
             sm.bin_c = lv.c + lv.dc;
@@ -522,17 +1001,17 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
         const uint64_t all_c = sm.bin_c, all_m = sm.bin_m;
         __syncthreads();
         uint64_t total = all_m, above = 0;
-        const uint64_t k = one ? 1u : (uint64_t)top_k;
-        if (use_k && k < all_c) {
-            cut = select_cut<false>(row, sm, buf, lv, kmin, kmax, k, rs, ncta, above, key_count);
+        if (use_k && want_k < all_c) {
+            cut = select_cut<false>(row, sm, buf, lv, kmin, kmax, want_k, rs, ncta, above,
+                                    key_count);
             float wf;
-            total = above + cut.ties * weight(row.value(L::from_key(cut.key)), rs, sm.tab, wf);
+            total = above + cut.ties * weight(R::value(cut.key), rs, sm.tab, wf);
         }
         if (use_p) {
-            uint64_t target = top_p > 0.f ? scaled(top_p, total, true) : 1;
-            if (target < 1) target = 1;
+            const uint64_t target = top_p > 0.f ? max((uint64_t)1, scaled(top_p, total, true)) : 1;
             uint64_t kc2 = 0;
-            const Cut c2 = select_cut<true>(row, sm, buf, lv, kmin, kmax, target, rs, ncta, above, kc2);
+            const Cut c2 =
+                select_cut<true>(row, sm, buf, lv, kmin, kmax, target, rs, ncta, above, kc2);
             if (c2.key > cut.key || (c2.key == cut.key && c2.ties < cut.ties)) {
                 cut = c2;
                 key_count = kc2;
@@ -543,12 +1022,10 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
     // ---- the cut's ties: the first cut.ties of key_count by index.  A warp
     // owns the contiguous segment [w0, w1) of the slice; tie_end: the warp's
     // elements with the cut's key are kept below this index.
-    const int seg = ((row.n + kWarps - 1) / kWarps + 31) & ~31;
-    const int w0 = min(row.n, warp * seg), w1 = min(row.n, w0 + seg);
     int tie_end = w1;
     if (cut.ties < key_count) {
         uint32_t mine = 0;
-        for (int x = w0 + lane; x < w1; x += 32) mine += L::key(row.raw(x)) == cut.key;
+        for (int x = w0 + lane; x < w1; x += 32) mine += R::key(row.at(x)) == cut.key;
         mine = __reduce_add_sync(kAll, mine);
         if (lane == 0) sm.wties[warp] = mine;
         __syncthreads();
@@ -567,29 +1044,24 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
             uint32_t seen = 0;
             for (int x0 = w0; x0 < w1 && seen < left; x0 += 32) {
                 const int x = x0 + lane;
-                const unsigned m = __ballot_sync(kAll, x < w1 && L::key(row.raw(x)) == cut.key);
+                const unsigned m = __ballot_sync(kAll, x < w1 && R::key(row.at(x)) == cut.key);
                 const uint32_t n = __popc(m);
-                if (seen + n >= left) {
-                    // the (left - seen)-th set bit of m ends the kept ties
-                    tie_end = x0 + (int)__fns(m, 0, (int)(left - seen)) + 1;
-                }
+                // the (left - seen)-th set bit of m ends the kept ties
+                if (seen + n >= left) tie_end = x0 + (int)__fns(m, 0, (int)(left - seen)) + 1;
                 seen += n;
             }
         }
     }
 
-    // ---- kept weight, the draw
-    const bool use_m = min_p > 0.f;
-    const uint64_t wmin = use_m ? (min_p >= 1.f ? 1ull << kUnitLog2
-                                                : scaled(min_p, 1ull << kUnitLog2, true))
-                                : 0;
-    auto kept = [&](int x, Raw raw, float &wf) -> uint64_t {
+    // ---- kept weight, the draw, the distribution
+    auto kept = [&](int x, float &wf) -> uint64_t {
+        const float v = row.at(x);
         wf = 0.f;
         if (use_k || use_p) {
-            const uint32_t key = L::key(raw);
+            const uint32_t key = R::key(v);
             if (key < cut.key || (key == cut.key && x >= tie_end)) return 0;
         }
-        const uint64_t w = weight(row.value(raw), rs, sm.tab, wf);
+        const uint64_t w = weight(v, rs, sm.tab, wf);
         if (w < wmin) {
             wf = 0.f;
             return 0;
@@ -599,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
     uint64_t sum = 0;
     for (int x = w0 + lane; x < w1; x += 32) {
         float wf;
-        sum += kept(x, row.raw(x), wf);
+        sum += kept(x, wf);
     }
     sum = warp_sum64(sum);
     if (lane == 0) sm.wsum[warp] = sum;
@@ -617,34 +1089,31 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
         total += t;
     }
     if (a.tokens) {
-        const float u = a.u[rowi];
-        // floor(u * total), below total; u outside [0, 1) is clamped
-        uint64_t target = u > 0.f ? (u < 1.f ? scaled(u, total, false) : total - 1) : 0;
+        const uint64_t target = draw_target(total);
         for (int w = 0; w < warp; ++w) before += sm.wsum[w];
         if (before <= target && target < before + sum) {
             // this warp: lane sums over contiguous runs, the lane, the element
             const int run = seg / 32, x0 = min(w1, w0 + lane * run), x1 = min(w1, x0 + run);
             uint64_t ls = 0;
             float wf;
-            for (int x = x0; x < x1; ++x) ls += kept(x, row.raw(x), wf);
+            for (int x = x0; x < x1; ++x) ls += kept(x, wf);
             uint64_t c = before + warp_scan64(ls, lane) - ls;
             if (c <= target && target < c + ls) {
                 int x = x0;
                 for (;; ++x) {
-                    c += kept(x, row.raw(x), wf);
+                    c += kept(x, wf);
                     if (c > target || x + 1 >= x1) break;
                 }
-                a.tokens[rowi] = e0 + x;
+                a.tokens[rowi] = e0 + x - row.pad;
             }
         }
     }
-    // ---- the distribution
     if (prow) {
         const float inv = (float)((double)(1ull << kUnitLog2) / (double)total);
         for (int x = w0 + lane; x < w1; x += 32) {  // (tie_end is the segment's)
             float wf;
-            kept(x, row.raw(x), wf);
-            prow[x] = wf * inv;
+            kept(x, wf);
+            if (x >= row.pad && x < row.pad + row.len) prow[x - row.pad] = wf * inv;
         }
     }
     cluster_sync();  // this CTA's shared memory has been read everywhere
@@ -653,20 +1122,20 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
 template <typename T>
 int launch_typed(const SampleArgs &in, int num_sms, cudaStream_t stream) {
     SampleArgs a = in;
-    constexpr int kMaxSlice = 96 * 1024;  // bytes: two CTAs an SM
-    const long bytes = (long)a.V * (long)sizeof(T);
-    // CTAs a row: enough that a slice stays resident, and more while they
-    // still spread the rows over the GPU (a slice of at least 4096 logits)
+    constexpr long kMaxSlice = 80 * 1024;  // bytes: two CTAs an SM
+    const long bytes = (long)a.V * 4;      // as fp32
+    // CTAs a row: enough that two slices fit an SM, and more while they still
+    // spread the rows over the GPU (a slice of at least 4096 logits)
     const long rows = (long)a.bs * a.B;
     int ncta = 1;
     while (ncta < kMaxCluster &&
-           ((bytes + ncta - 1) / ncta > kMaxSlice ||
-            (rows * ncta * 2 <= 2 * num_sms && a.V / (2 * ncta) >= 4096)))
+           (bytes > kMaxSlice * ncta || (rows * ncta <= num_sms && a.V / (2 * ncta) >= 4096)))
         ncta *= 2;
     a.ncta = ncta;
     a.slice = (int)((((long)a.V + ncta - 1) / ncta + 31) & ~31L);
-    const size_t smem = (size_t)a.slice * sizeof(T) + 16;
-    const bool resident = smem <= 200 * 1024;
+    // pad in front (up to 7 logits) and up to a multiple of 128 behind
+    const size_t smem = ((size_t)a.slice + 7 + 127) / 128 * 512;
+    const bool resident = smem <= 190 * 1024;
     auto kernel = resident ? token_sample_kernel<T, true> : token_sample_kernel<T, false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              resident ? (int)smem : 0) != cudaSuccess)

@@ -621,9 +621,9 @@ int32_t bdsa_block_table_update(const int32_t *seq_lens, const int32_t *new_lens
  * without a logit above -inf, or with a negative, NaN or infinite T, gets token
  * -1 and zero probs and is reported (BDSA_DEVICE_OUT_OF_RANGE).  u outside
  * [0, 1) is clamped (NaN: 0).
- * Arithmetic: weights to about 2^-39 of the largest, held and summed exactly as
- * integers in units of 2^-41 of it (a weight below half a unit counts as zero
- * in S and the cuts); probs carry two fp32 roundings.  The result does not
+ * Arithmetic: weights to about 2^-30 of themselves, summed as integers in units
+ * of 2^-41 of the largest (a weight below half a unit counts as zero in the
+ * cuts and the draw); probs carry three fp32 roundings.  The result does not
  * depend on the grid.
  * tokens ([bs, B]) or probs may be NULL, not both; u is needed for tokens.
  * probs rows must not overlap.  Supported: V <= 2^21, bs * B <= 2^26; rows may
