@@ -106,26 +106,29 @@ __device__ __forceinline__ V1 splat<V1>(float x) { return {x}; }
 template <>
 __device__ __forceinline__ V2 splat<V2>(float x) { return {f2_pack(x, x)}; }
 
-// Table entry and power of two of k sixteenths (k <= 0), and whether the weight
-// is above fp32's normal range at all (false for -inf and NaN too).
-__device__ __forceinline__ float2 table_at(const ExpTable &tab, int k) { return tab.v[k & 15]; }
-__device__ __forceinline__ float pow2_at(int k) { return __int_as_float(((k >> 4) + 127) << 23); }
+// Table entry and power of two of k sixteenths, from t = k + 1.5 * 2^23 (k <= 0):
+// the float's low bits are k's, and 2^19 of them shift the constant's out.
+__device__ __forceinline__ float2 table_at(const ExpTable &tab, float t) {
+    return tab.v[__float_as_uint(t) & 15u];
+}
+__device__ __forceinline__ float pow2_at(float t) {
+    return __uint_as_float(((__float_as_uint(t) << 19) & 0xff800000u) + 0x3f800000u);
+}
+// Weights below 2^-124 (and those of -inf and NaN) are zero.
 constexpr float kMinLog2 = -124.f;
 
 __device__ __forceinline__ void lookup(const ExpTable &tab, V1 t, V1 &th, V1 &tl, V1 &sc) {
-    const int k = __float_as_int(t.a) - 0x4B400000;
-    const float2 e = table_at(tab, k);
+    const float2 e = table_at(tab, t.a);
     th.a = e.x;
     tl.a = e.y;
-    sc.a = pow2_at(k);
+    sc.a = pow2_at(t.a);
 }
 __device__ __forceinline__ void lookup(const ExpTable &tab, V2 t, V2 &th, V2 &tl, V2 &sc) {
     const float2 u = f2_unpack(t.a);
-    const int k0 = __float_as_int(u.x) - 0x4B400000, k1 = __float_as_int(u.y) - 0x4B400000;
-    const float2 e0 = table_at(tab, k0), e1 = table_at(tab, k1);
+    const float2 e0 = table_at(tab, u.x), e1 = table_at(tab, u.y);
     th.a = f2_pack(e0.x, e1.x);
     tl.a = f2_pack(e0.y, e1.y);
-    sc.a = f2_pack(pow2_at(k0), pow2_at(k1));
+    sc.a = f2_pack(pow2_at(u.x), pow2_at(u.y));
 }
 __device__ __forceinline__ void keep_normal(V1 yn, V1 &h, V1 &l) {
     const bool ok = yn.a < -kMinLog2;
@@ -213,8 +216,8 @@ __device__ __forceinline__ uint64_t scaled(float x, uint64_t v, bool up) {
 }
 
 // ------------------------------------------------------------ logit types
-// A logit as fp32 (NaN as -inf, -0 as +0), and the bits of its ordered pattern
-// that are the same for every value of the type.
+// A logit as fp32 (NaN as -inf), and the low bits of its ordered pattern that are
+// the same for every value of the type and sign.
 template <typename T>
 struct Logit;
 template <>
@@ -235,12 +238,14 @@ template <>
 struct Logit<__half> {
     using Raw = uint16_t;
     static constexpr int kKeyShift = 13;
-    static __device__ __forceinline__ float wide(Raw r) { return __half2float(__ushort_as_half(r)); }
+    static __device__ __forceinline__ float wide(Raw r) {
+        return __half2float(__ushort_as_half(r));
+    }
 };
-__device__ __forceinline__ float clean(float v) { return (v == v ? v : -INFINITY) + 0.f; }
-// Unsigned integers that order like the floats (no NaN, no -0).
+__device__ __forceinline__ float clean(float v) { return fmaxf(v, -INFINITY); }
+// Unsigned integers that order like the floats (no NaN; -0 as +0).
 __device__ __forceinline__ uint32_t float_key(float v) {
-    const uint32_t b = __float_as_uint(v);
+    const uint32_t b = __float_as_uint(v + 0.f);
     return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float key_float(uint32_t k) {
@@ -293,8 +298,7 @@ struct Hist {
 struct Lists {
     float val[kListMax];
     int idx[kListMax];
-    uint64_t sorted[kListMax];
-    uint64_t sum[kListMax];
+    uint64_t a[kListMax], b[kListMax];
 };
 
 struct Shared {
@@ -308,8 +312,7 @@ struct Shared {
     uint64_t wsum[kWarps];        // weight of each warp's segment
     uint32_t wties[kWarps];       // cut-key elements of each warp's segment
     float red[kWarps];
-    int p_count[2][kWarps];       // pivot search: the warps' shares, by step parity
-    float p_mass[2][kWarps];
+    float tlow[kWarps];
     int n_list, n_below, n_min;   // candidates; those below top-p's goal; past min-p
     // cluster exchange: written by this CTA, read by all, one use each
     uint64_t x_all, x_sum;
@@ -355,29 +358,56 @@ struct Row {
     }
 };
 
+// Runs body(x) for the positions x of [x0, x1) with pred(logit), one warp, in no
+// particular order: each lane picks its positions of 32 * 32 first and the lanes
+// then run their picks together, so that a warp's steps are the fullest lane's
+// picks instead of every position with a picked neighbour.
+template <class R, class P, class B>
+__device__ __forceinline__ void for_selected(const R &row, int x0, int x1, int lane, P pred,
+                                             B body) {
+    for (int base = x0; base < x1; base += 1024) {
+        uint32_t mask = 0;
+        const int steps = min(32, (x1 - base + 31) / 32);
+        for (int j = 0; j < steps; ++j) {
+            const int x = base + 32 * j + lane;
+            if (x < x1 && pred(row.at(x), x)) mask |= 1u << j;
+        }
+        while (mask) {
+            const int j = __ffs(mask) - 1;
+            mask &= mask - 1;
+            body(base + 32 * j + lane);
+        }
+    }
+    __syncwarp();
+}
+
 // One histogram level over the keys in [klo, khi], bin 0 the highest keys.  Every
 // thread of every CTA of the cluster ends with its bin's totals over the cluster.
 template <class R>
-__device__ Level level_hist(const R &row, Shared &sm, int buf, uint32_t klo, uint32_t khi,
-                            int shift, const RowScale &rs, uint32_t ncta) {
+__device__ Level level_hist(const R &row, int w0, int w1, Shared &sm, int buf, uint32_t klo,
+                            uint32_t khi, int shift, const RowScale &rs, uint32_t ncta) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Hist &h = sm.hist[buf];
     h.cnt[tid] = h.m0[tid] = h.m1[tid] = h.m2[tid] = 0;
     __syncthreads();
-    for (int x = tid; x < row.n; x += kThreads) {
-        const float v = row.at(x);
-        const uint32_t key = R::key(v);
-        if (key < klo || key > khi) continue;
-        const uint32_t b = (khi - key) >> shift;
-        float wf;
-        const uint64_t w = weight(v, rs, sm.tab, wf);
-        const uint32_t l0 = (uint32_t)w & 0x3fffu, l1 = (uint32_t)(w >> 14) & 0x3fffu;
-        const uint32_t l2 = (uint32_t)(w >> 28);
-        atomicAdd(&h.cnt[b], 1u);
-        if (l0) atomicAdd(&h.m0[b], l0);
-        if (l1) atomicAdd(&h.m1[b], l1);
-        if (l2) atomicAdd(&h.m2[b], l2);
-    }
+    for_selected(
+        row, w0, w1, lane,
+        [&](float v, int) {
+            const uint32_t key = R::key(v);
+            return key >= klo && key <= khi;
+        },
+        [&](int x) {
+            const float v = row.at(x);
+            const uint32_t b = (khi - R::key(v)) >> shift;
+            float wf;
+            const uint64_t w = weight(v, rs, sm.tab, wf);
+            const uint32_t l0 = (uint32_t)w & 0x3fffu, l1 = (uint32_t)(w >> 14) & 0x3fffu;
+            const uint32_t l2 = (uint32_t)(w >> 28);
+            atomicAdd(&h.cnt[b], 1u);
+            if (l0) atomicAdd(&h.m0[b], l0);
+            if (l1) atomicAdd(&h.m1[b], l1);
+            if (l2) atomicAdd(&h.m2[b], l2);
+        });
     cluster_sync();
     Level lv{0, 0, 0, 0};
     for (uint32_t r = 0; r < ncta; ++r) {
@@ -412,9 +442,9 @@ __device__ __forceinline__ int range_shift(uint32_t klo, uint32_t khi) {
 // weight).  `lv` is the level over [klo, khi].  above_m: the weight of the keys
 // above the cut's; key_count: the elements with the cut's key.
 template <bool kMass, class R>
-__device__ Cut select_cut(const R &row, Shared &sm, int &buf, Level lv, uint32_t klo,
-                          uint32_t khi, uint64_t target, const RowScale &rs, uint32_t ncta,
-                          uint64_t &above_m, uint64_t &key_count) {
+__device__ Cut select_cut(const R &row, int w0, int w1, Shared &sm, int &buf, Level lv,
+                          uint32_t klo, uint32_t khi, uint64_t target, const RowScale &rs,
+                          uint32_t ncta, uint64_t &above_m, uint64_t &key_count) {
     int shift = range_shift(klo, khi);
     uint64_t base_c = 0, base_m = 0;
     for (;;) {
@@ -454,7 +484,7 @@ __device__ Cut select_cut(const R &row, Shared &sm, int &buf, Level lv, uint32_t
         }
         buf ^= 1;
         shift = range_shift(klo, khi);
-        lv = level_hist(row, sm, buf, klo, khi, shift, rs, ncta);
+        lv = level_hist(row, w0, w1, sm, buf, klo, khi, shift, rs, ncta);
     }
 }
 
@@ -473,6 +503,40 @@ __device__ __forceinline__ void bitonic_sort(uint64_t *a, int n) {
             __syncthreads();
         }
     }
+}
+
+// Threads an entry of a list of n <= kThreads gets when all entries are compared
+// with all: a power of two, at most a warp.
+__device__ __forceinline__ int list_parts(int n) {
+    int p = 32;
+    while (p > 1 && p * n > kThreads) p >>= 1;
+    return p;
+}
+
+// Sorts the distinct keys a[0, n) ascending, n <= kListMax, room for a power of
+// two; b is scratch of the same size.  Returns where the result is (a or b).
+// Up to kThreads keys each find their rank by comparing with all the others (for
+// the usual hundred or two a few dozen steps without a barrier); more are sorted
+// by a bitonic network.
+__device__ __forceinline__ uint64_t *sort_list(uint64_t *a, uint64_t *b, int n) {
+    const int tid = threadIdx.x;
+    if (n <= kThreads) {
+        const int parts = list_parts(n), x = tid / parts, part = tid % parts;
+        const uint64_t key = x < n ? a[x] : 0;
+        int rank = 0;
+        if (x < n)
+            for (int y = part; y < n; y += parts) rank += a[y] < key;
+        for (int o = parts >> 1; o > 0; o >>= 1) rank += __shfl_xor_sync(kAll, rank, o);
+        if (x < n && part == 0) b[rank] = key;
+        __syncthreads();
+        return b;
+    }
+    int np = 2;
+    while (np < n) np <<= 1;
+    for (int x = n + tid; x < np; x += kThreads) a[x] = ~0ull;
+    __syncthreads();
+    bitonic_sort(a, np);
+    return a;
 }
 
 // Inclusive prefix sums of v over the CTA's threads (0 elsewhere), in thread order.
@@ -526,6 +590,15 @@ __device__ __forceinline__ uint64_t sum_weights(float *s, int x0, int x1, const 
     const float2 a = f2_unpack(acc.a), b = f2_unpack(low.a);
     return (uint64_t)(__float2ll_rn(a.x * kUnits) + __float2ll_rn(a.y * kUnits) +
                       __float2ll_rn(b.x * kUnits) + __float2ll_rn(b.y * kUnits));
+}
+
+// 2^kUnitLog2 / total, rounded once (to within 2^-46).
+__device__ __forceinline__ float inverse(uint64_t total) {
+    const float hi = __ull2float_rz(total);  // hi <= total, both in units
+    const float lo = __ull2float_rn(total - (uint64_t)hi);
+    const float i0 = __fdiv_rn(kUnits, hi);
+    // i0 + (kUnits - i0 (hi + lo)) / hi
+    return i0 + __fdividef(fmaf(-i0, lo, fmaf(-i0, hi, kUnits)), hi);
 }
 
 template <typename T, bool kResident>
@@ -619,20 +692,31 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
     sm.tmax[tid] = mx;
     cluster_sync();
     // every CTA takes the row's thread maxima: ncta a thread
-    float tm[kMaxCluster];
+    float tm[kMaxCluster], lowest = INFINITY;
     mx = -INFINITY;
 #pragma unroll
     for (int c = 0; c < kMaxCluster; ++c) {
         tm[c] = c < ncta ? map_to_rank(sm.tmax, c)[tid] : -INFINITY;
         mx = fmaxf(mx, tm[c]);
+        if (tm[c] > -INFINITY) lowest = fminf(lowest, tm[c]);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
-    if (lane == 0) sm.red[warp] = mx;
+    for (int o = 16; o > 0; o >>= 1) {
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+        lowest = fminf(lowest, __shfl_xor_sync(kAll, lowest, o));
+    }
+    if (lane == 0) {
+        sm.red[warp] = mx;
+        sm.tlow[warp] = lowest;
+    }
     __syncthreads();
     mx = sm.red[lane % kWarps];
+    lowest = sm.tlow[lane % kWarps];
 #pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+    for (int o = kWarps / 2; o > 0; o >>= 1) {
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+        lowest = fminf(lowest, __shfl_xor_sync(kAll, lowest, o));
+    }
     if (bad_temp || mx == -INFINITY) {  // no distribution (uniform over the cluster)
         if (prow)
             for (int x = tid; x < row.len; x += kThreads) prow[x] = 0.f;
@@ -653,14 +737,20 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
                 slice[x] = slice[x] == INFINITY ? 0.f : -INFINITY;
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c) tm[c] = tm[c] == INFINITY ? 0.f : -INFINITY;
+        lowest = 0.f;
         __syncthreads();
     }
     {
         // temperatures below 1e-30 act as 1e-30 (greedy rows weigh every kept
         // logit alike: only one is kept)
-        const double c = 1.4426950408889634 / (double)fmaxf(greedy ? 1.f : temp, 1e-30f);
-        rs.ch = (float)c;
-        rs.cl = (float)(c - (double)rs.ch);
+        // log2(e) / T as two floats by a corrected fp32 division (a double one
+        // costs every thread of the CTA some twenty fp64 instructions, which
+        // this GPU runs at 1/64 of the fp32 rate)
+        constexpr float kL2e = 1.44269502162933349609375f, kL2el = 1.925963033500011e-08f;
+        const float t = fmaxf(greedy ? 1.f : temp, 1e-30f);
+        rs.ch = __fdiv_rn(kL2e, t);
+        const float rest = fmaf(-rs.ch, t, kL2e) + kL2el;
+        rs.cl = __fdiv_rn(rest, t);
     }
     const float u = a.tokens ? a.u[rowi] : 0.f;
     // floor(u * total), below total; u outside [0, 1) is clamped
@@ -729,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
             }
         }
         if (prow) {
-            const float inv = (float)((double)(1ull << kUnitLog2) / (double)total);
+            const float inv = inverse(total);
             float *out = prow - row.pad;
             if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
                 for (int x = w0 + 4 * lane; x < w1; x += 128) {
@@ -758,7 +848,8 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
     const uint64_t wmin =
         use_m ? (min_p >= 1.f ? 1ull << kUnitLog2 : scaled(min_p, 1ull << kUnitLog2, true)) : 0;
     const uint64_t want_k = one ? 1u : (uint64_t)top_k;
-    uint64_t all_sum = 0;  // the row's weight (top-p without top-k)
+    uint64_t all_sum = 0;        // the row's weight (top-p without top-k)
+    float pivot_k = -INFINITY;   // at least want_k logits are at or above it
     if (kResident && filtered) {
         if (use_p && !use_k) {
             uint64_t sum = warp_sum64(
@@ -784,65 +875,71 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
             pivot = rs.lmax + t * (t < 0.f ? 1.0001f : 1.f) - 1e-4f * fabsf(rs.lmax) - 1e-5f;
         }
         if ((use_k || use_p) && a.V > kListMax) {
-            // the largest p with enough of the threads' maxima at or above it:
-            // want_k of them, or weight for the top-p goal (a margin covers the
-            // fp32 sums; the exact cut below checks it)
-            const float goal = use_k ? 0.f
-                                     : fminf(top_p, 1.f) * (float)all_sum * (1.f / kUnits) * 1.0001f;
-            uint32_t lo = float_key(-INFINITY), hi = float_key(rs.lmax);
-            const int need = (int)min(want_k, (uint64_t)kListMax + 1);
-            float tw[kMaxCluster];
-            if (!use_k) {
+            // A histogram of the threads' maxima over equal parts of [lowest,
+            // lmax], from the top: the pivot is the lower end of the first bin
+            // where want_k maxima are reached (want_k logits at least are then
+            // at or above it), or where their weights -- taken at the bin's
+            // middle, an estimate the exact cut checks -- reach top-p's goal.
+            // A bin that goes far past want_k is cut again.
+            uint32_t *cnt = sm.hist[0].cnt;
+            float lo = lowest, hi = rs.lmax;
+            uint32_t above = 0;  // maxima above hi
+            const uint32_t need = (uint32_t)min(want_k, (uint64_t)1 << 20);
+            const float goal = 1.002f * fminf(top_p, 1.f) * (float)all_sum;
+            for (int level = 0; level < 3; ++level) {
+                const float scale = hi > lo ? (float)kBins / (hi - lo) : 0.f;
+                cnt[tid] = 0;
+                if (tid == 0) sm.bin = -1;
+                __syncthreads();
 #pragma unroll
-                for (int c = 0; c < kMaxCluster; ++c) weight(tm[c], rs, sm.tab, tw[c]);
-            }
-            // lo passes (every maximum), unless there are too few of them
-            bool lo_ok = false;
-            for (int step = 0; step < 33; ++step) {
-                // the first step asks about lo itself
-                const uint32_t mid = step == 0 ? lo + 1 : lo + (hi - lo + 1) / 2;
-                const float p = key_float(mid);
-                int n = 0;
-                float w = 0.f;
-#pragma unroll
-                for (int c = 0; c < kMaxCluster; ++c) {
-                    if (tm[c] >= p) {
-                        ++n;
-                        if (!use_k) w += tw[c];
-                    }
+                for (int c = 0; c < kMaxCluster; ++c)
+                    if (tm[c] >= lo && tm[c] <= hi)
+                        atomicAdd(cnt + min(kBins - 1, (int)((hi - tm[c]) * scale)), 1u);
+                __syncthreads();
+                const uint32_t n = cnt[tid];
+                // counts in the low half, weights (units of 2^-19 of the largest
+                // and maximum, 2^31 at most together) in the high half
+                uint64_t v = n;
+                if (!use_k && n) {
+                    float wf;
+                    weight(hi - ((float)tid + 0.5f) * (hi - lo) * (1.f / kBins), rs, sm.tab, wf);
+                    v += (uint64_t)((float)n * wf * 524288.f) << 32;
                 }
-                n = __reduce_add_sync(kAll, n);
-                if (!use_k) {
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(kAll, w, o);
-                }
-                if (lane == 0) {
-                    sm.p_count[step & 1][warp] = n;
-                    sm.p_mass[step & 1][warp] = w;
+                const uint64_t inc = block_scan64(v, sm);
+                const uint32_t upto = above + (uint32_t)inc;
+                const bool in = use_k ? upto >= need && upto - n < need
+                                      : (float)(inc >> 32) >= goal * (524288.f / kUnits) &&
+                                            (float)((inc - v) >> 32) <
+                                                goal * (524288.f / kUnits);
+                if (in) {
+                    sm.bin = tid;
+                    sm.bin_c = upto;
+                    sm.bin_dc = n;
                 }
                 __syncthreads();
-                // (the same order of additions in every CTA of the cluster: they
-                // must agree on the pivot)
-                n = 0;
-                w = 0.f;
-#pragma unroll
-                for (int q = 0; q < kWarps; ++q) {
-                    n += sm.p_count[step & 1][q];
-                    w += sm.p_mass[step & 1][q];
+                const int bin = sm.bin;
+                if (bin < 0) {  // too few maxima (a later level: the last pivot stands)
+                    if (level == 0) lo = -INFINITY;
+                    break;
                 }
-                const bool ok = use_k ? n >= need : w >= goal;
-                if (step == 0) {
-                    if (!ok) break;
-                    lo_ok = true;
-                }
-                if (ok) lo = mid;
-                else hi = mid - 1;
-                if (lo >= hi) break;
-                // near enough: a few more candidates cost less than the search
-                if (use_k && ok && n <= need + need / 4 + 16) break;
+                // the bin's ends, both lowered by more than a rounding of the bin
+                // number: every maximum counted is above lo, and none is counted
+                // again when the bin is cut (one may be left out, which only
+                // lowers the pivot)
+                const uint32_t got = (uint32_t)sm.bin_c, in_bin = (uint32_t)sm.bin_dc;
+                const float step = (hi - lo) * (1.f / kBins);
+                const float eps = 4e-7f * (fabsf(hi) + fabsf(lo) + (hi - lo));
+                const float nhi = hi - (float)bin * step - eps;
+                lo = fmaxf(lo, hi - (float)(bin + 1) * step - eps);
+                __syncthreads();
+                if (!use_k || got <= need + need / 4 + 64 || in_bin < 32 || nhi <= lo) break;
+                above = got - in_bin;
+                hi = nhi;
             }
-            if (lo_ok) pivot = fmaxf(pivot, key_float(lo));
+            if (use_k) pivot_k = lo;
+            if (lo > -INFINITY) pivot = fmaxf(pivot, lo);
             else list = by_m;
+            __syncthreads();  // the counters make way for the list
         }
         // ---- candidates of the slice
         if (list) {
@@ -869,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
                 const int m = o->n_list;
                 if (n + m <= kListMax) {
                     for (int x = tid; x < m; x += kThreads)
-                        sm.list.sorted[n + x] =
+                        sm.list.a[n + x] =
                             (uint64_t)~float_key(o->list.val[x]) << 32 | (uint32_t)o->list.idx[x];
                 }
                 n += m;
@@ -878,15 +975,12 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
         }
         // ---- the exact cut
         if (list) {  // (uniform over the cluster)
-            int np = 2;
-            while (np < n) np <<= 1;
-            for (int x = n + tid; x < np; x += kThreads) sm.list.sorted[x] = ~0ull;
             __syncthreads();
-            bitonic_sort(sm.list.sorted, np);
-            uint64_t *cum = sm.list.sum;
+            uint64_t *keys = sort_list(sm.list.a, sm.list.b, n);
+            uint64_t *cum = keys == sm.list.a ? sm.list.b : sm.list.a;
             for (int x = tid; x < n; x += kThreads) {
                 float wf;
-                cum[x] = weight(key_float(~(uint32_t)(sm.list.sorted[x] >> 32)), rs, sm.tab, wf);
+                cum[x] = weight(key_float(~(uint32_t)(keys[x] >> 32)), rs, sm.tab, wf);
             }
             __syncthreads();
             // (min-p: weights fall with the rank, so the first n_m pass)
@@ -919,11 +1013,11 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
             keep = max(keep, 1);
             if (list) {
                 const uint64_t total = cum[keep - 1];
-                const float inv = (float)((double)(1ull << kUnitLog2) / (double)total);
+                const float inv = inverse(total);
                 if (prow) {
                     // zeros, then the kept ones of this slice
-                    const int lead =
-                        min(row.len, (int)((16 - (reinterpret_cast<uintptr_t>(prow) & 15)) / 4) & 3);
+                    const int off = (int)(reinterpret_cast<uintptr_t>(prow) & 15) / 4;
+                    const int lead = min(row.len, (4 - off) & 3);
                     const int quads = (row.len - lead) / 4;
                     if (tid < lead) prow[tid] = 0.f;
                     for (int x = tid; x < quads; x += kThreads)
@@ -932,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
                     if (tid < row.len - lead - 4 * quads) prow[lead + 4 * quads + tid] = 0.f;
                     __syncthreads();
                     for (int x = tid; x < keep; x += kThreads) {
-                        const uint64_t sv = sm.list.sorted[x];
+                        const uint64_t sv = keys[x];
                         const int e = (int)(uint32_t)sv - e0;
                         if (e < 0 || e >= row.len) continue;
                         float wf;
@@ -941,30 +1035,40 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
                     }
                 }
                 if (a.tokens && rank == 0) {
-                    // the kept ones in index order: index << 32 | rank, their
-                    // weights the differences of the rank order's sums
                     const uint64_t target = draw_target(total);
-                    __syncthreads();
-                    int kp = 2;
-                    while (kp < keep) kp <<= 1;
-                    for (int x = tid; x < kp; x += kThreads)
-                        sm.list.sorted[x] =
-                            x < keep ? sm.list.sorted[x] << 32 | (uint32_t)x : ~0ull;
-                    __syncthreads();
-                    bitonic_sort(sm.list.sorted, kp);
-                    uint64_t w[2];
+                    auto own = [&](int x) { return cum[x] - (x ? cum[x - 1] : 0); };
+                    if (keep <= kThreads) {
+                        // each kept one adds up the weights of indices up to its own
+                        const int parts = list_parts(keep), x = tid / parts, part = tid % parts;
+                        const uint32_t idx = x < keep ? (uint32_t)keys[x] : 0u;
+                        uint64_t c = 0;
+                        if (x < keep)
+                            for (int y = part; y < keep; y += parts)
+                                if ((uint32_t)keys[y] <= idx) c += own(y);
+                        for (int o = parts >> 1; o > 0; o >>= 1)
+                            c += __shfl_xor_sync(kAll, (unsigned long long)c, o);
+                        if (x < keep && part == 0 && c > target && c - own(x) <= target)
+                            a.tokens[rowi] = (int)idx;
+                    } else {
+                        // in index order: index << 32 | rank, sorted and summed
+                        __syncthreads();
+                        for (int x = tid; x < kListMax; x += kThreads)
+                            keys[x] = x < keep ? keys[x] << 32 | (uint32_t)x : ~0ull;
+                        __syncthreads();
+                        bitonic_sort(keys, kListMax);
+                        uint64_t w[2];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int x = 2 * tid + k;
-                        const uint32_t q = x < keep ? (uint32_t)sm.list.sorted[x] : 0u;
-                        w[k] = x < keep ? cum[q] - (q ? cum[q - 1] : 0) : 0;
+                        for (int k = 0; k < 2; ++k) {
+                            const int x = 2 * tid + k;
+                            w[k] = x < keep ? own((int)(uint32_t)keys[x]) : 0;
+                        }
+                        const uint64_t t = block_scan64(w[0] + w[1], sm);
+                        const uint64_t t0 = t - w[1];
+                        if (t0 > target && t0 - w[0] <= target)
+                            a.tokens[rowi] = (int)(keys[2 * tid] >> 32);
+                        if (t > target && t0 <= target)
+                            a.tokens[rowi] = (int)(keys[2 * tid + 1] >> 32);
                     }
-                    const uint64_t t = block_scan64(w[0] + w[1], sm);
-                    const uint64_t t0 = t - w[1];
-                    if (t0 > target && t0 - w[0] <= target)
-                        a.tokens[rowi] = (int)(sm.list.sorted[2 * tid] >> 32);
-                    if (t > target && t0 <= target)
-                        a.tokens[rowi] = (int)(sm.list.sorted[2 * tid + 1] >> 32);
                 }
                 cluster_sync();  // the lists have been read everywhere
                 return;
@@ -977,21 +1081,37 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
     Cut cut{0, ~0ull};       // everything
     uint64_t key_count = 0;  // elements with the cut's key
     if (use_k || use_p) {
-        // the smallest key above -inf's
-        const uint32_t kmax = R::key(rs.lmax), kinf = R::key(-INFINITY);
-        uint32_t kmin = kmax;
-        for (int x = tid; x < row.n; x += kThreads) {
-            const uint32_t k = R::key(row.at(x));
-            if (k > kinf) kmin = min(kmin, k);
+        // The keys the cut can be among: from the pivot of top-k (want_k logits
+        // are at or above it); for top-p alone from the logit whose weight V
+        // times makes the share that may be left out (margins cover the fp32
+        // roundings); else from the smallest logit.
+        const uint32_t kmax = R::key(rs.lmax);
+        uint32_t kmin = 0xffffffffu;
+        if (pivot_k > -INFINITY) {
+            kmin = R::key(pivot_k);
+        } else if (!use_k && all_sum > 0 && top_p < 0.9999f) {
+            const float share = (1.f - fmaxf(top_p, 0.f)) * (float)all_sum / kUnits / (float)a.V;
+            const float l = rs.lmax + (__logf(share) - 0.01f) / (rs.ch * 0.693147181f) -
+                            1e-4f * fabsf(rs.lmax) - 1e-5f;
+            if (l > -INFINITY && share > 0.f) kmin = min(kmax, R::key(l));
         }
-        kmin = __reduce_min_sync(kAll, kmin);
-        if (tid == 0) sm.x_min = kmax;
-        __syncthreads();
-        if (lane == 0) atomicMin(&sm.x_min, kmin);
-        cluster_sync();
-        for (uint32_t c = 0; c < ncta; ++c) kmin = min(kmin, *map_to_rank(&sm.x_min, c));
+        if (kmin == 0xffffffffu) {
+            const uint32_t kinf = R::key(-INFINITY);
+            kmin = kmax;
+            for (int x = tid; x < row.n; x += kThreads) {
+                const uint32_t k = R::key(row.at(x));
+                if (k > kinf) kmin = min(kmin, k);
+            }
+            kmin = __reduce_min_sync(kAll, kmin);
+            if (tid == 0) sm.x_min = kmax;
+            __syncthreads();
+            if (lane == 0) atomicMin(&sm.x_min, kmin);
+            cluster_sync();
+            for (uint32_t c = 0; c < ncta; ++c) kmin = min(kmin, *map_to_rank(&sm.x_min, c));
+        }
         int buf = 0;
-        const Level lv = level_hist(row, sm, buf, kmin, kmax, range_shift(kmin, kmax), rs, ncta);
+        const Level lv =
+            level_hist(row, w0, w1, sm, buf, kmin, kmax, range_shift(kmin, kmax), rs, ncta);
         // totals of the range (the last thread's inclusive prefix)
         if (tid == kThreads - 1) {
             sm.bin_c = lv.c + lv.dc;
@@ -1000,18 +1120,21 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
         __syncthreads();
         const uint64_t all_c = sm.bin_c, all_m = sm.bin_m;
         __syncthreads();
-        uint64_t total = all_m, above = 0;
-        if (use_k && want_k < all_c) {
-            cut = select_cut<false>(row, sm, buf, lv, kmin, kmax, want_k, rs, ncta, above,
+        uint64_t total = !use_k && all_sum > 0 ? all_sum : all_m, above = 0;
+        if (use_k && want_k <= all_c) {
+            cut = select_cut<false>(row, w0, w1, sm, buf, lv, kmin, kmax, want_k, rs, ncta, above,
                                     key_count);
             float wf;
             total = above + cut.ties * weight(R::value(cut.key), rs, sm.tab, wf);
         }
         if (use_p) {
-            const uint64_t target = top_p > 0.f ? max((uint64_t)1, scaled(top_p, total, true)) : 1;
+            // (the range's own weights round one by one, the row's weight at
+            // once: the goal stays within the range)
+            uint64_t target = top_p > 0.f ? max((uint64_t)1, scaled(top_p, total, true)) : 1;
+            target = min(target, all_m);
             uint64_t kc2 = 0;
-            const Cut c2 =
-                select_cut<true>(row, sm, buf, lv, kmin, kmax, target, rs, ncta, above, kc2);
+            const Cut c2 = select_cut<true>(row, w0, w1, sm, buf, lv, kmin, kmax, target, rs, ncta,
+                                            above, kc2);
             if (c2.key > cut.key || (c2.key == cut.key && c2.ties < cut.ties)) {
                 cut = c2;
                 key_count = kc2;
@@ -1054,13 +1177,15 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
     }
 
     // ---- kept weight, the draw, the distribution
+    auto in_cut = [&](float v, int x) {
+        if (!(use_k || use_p)) return true;
+        const uint32_t key = R::key(v);
+        return key > cut.key || (key == cut.key && x < tie_end);
+    };
     auto kept = [&](int x, float &wf) -> uint64_t {
         const float v = row.at(x);
         wf = 0.f;
-        if (use_k || use_p) {
-            const uint32_t key = R::key(v);
-            if (key < cut.key || (key == cut.key && x >= tie_end)) return 0;
-        }
+        if (!in_cut(v, x)) return 0;
         const uint64_t w = weight(v, rs, sm.tab, wf);
         if (w < wmin) {
             wf = 0.f;
@@ -1069,10 +1194,10 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
         return w;
     };
     uint64_t sum = 0;
-    for (int x = w0 + lane; x < w1; x += 32) {
+    for_selected(row, w0, w1, lane, in_cut, [&](int x) {
         float wf;
         sum += kept(x, wf);
-    }
+    });
     sum = warp_sum64(sum);
     if (lane == 0) sm.wsum[warp] = sum;
     __syncthreads();
@@ -1109,12 +1234,16 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
         }
     }
     if (prow) {
-        const float inv = (float)((double)(1ull << kUnitLog2) / (double)total);
-        for (int x = w0 + lane; x < w1; x += 32) {  // (tie_end is the segment's)
+        const float inv = inverse(total);
+        // (tie_end is the segment's)
+        for (int x = w0 + lane; x < w1; x += 32)
+            if (x >= row.pad && x < row.pad + row.len) prow[x - row.pad] = 0.f;
+        __syncwarp();
+        for_selected(row, w0, w1, lane, in_cut, [&](int x) {
             float wf;
             kept(x, wf);
             if (x >= row.pad && x < row.pad + row.len) prow[x - row.pad] = wf * inv;
-        }
+        });
     }
     cluster_sync();  // this CTA's shared memory has been read everywhere
 }
