@@ -262,6 +262,16 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The two halves of a barrier that only keeps a CTA's shared memory alive until
+// the others have read it: arrive after the last read, wait before leaving.
+__device__ __forceinline__ void cluster_reads_done() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_reads() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 template <class T>
 __device__ __forceinline__ const T *map_to_rank(const T *p, uint32_t rank) {
     uint64_t out;
@@ -296,8 +306,7 @@ struct Hist {
 // (key descending, index ascending, as ~key << 32 | index) with their weights'
 // prefix sums.
 struct Lists {
-    float val[kListMax];
-    int idx[kListMax];
+    uint64_t own[kListMax];
     uint64_t a[kListMax], b[kListMax];
 };
 
@@ -314,6 +323,7 @@ struct Shared {
     float red[kWarps];
     float tlow[kWarps];
     int n_list, n_below, n_min;   // candidates; those below top-p's goal; past min-p
+    int last;                     // last thread with weight (draw_in_block)
     // cluster exchange: written by this CTA, read by all, one use each
     uint64_t x_all, x_sum;
     uint32_t x_ties, x_min;
@@ -601,6 +611,50 @@ __device__ __forceinline__ float inverse(uint64_t total) {
     return i0 + __fdividef(fmaf(-i0, lo, fmaf(-i0, hi, kUnits)), hi);
 }
 
+// The warp whose segment of this slice holds the target, or -1; before (the
+// weight in front of the slice) becomes the weight in front of that segment.
+// Uniform over the CTA.
+__device__ __forceinline__ int warp_of_target(const Shared &sm, uint64_t target,
+                                              uint64_t &before) {
+    if (target < before) return -1;
+    for (int w = 0; w < kWarps; ++w) {
+        if (target < before + sm.wsum[w]) return w;
+        before += sm.wsum[w];
+    }
+    return -1;
+}
+
+// One step of the draw by the whole CTA: every thread brings the weights q[4] of
+// four successive indices (their sum s4, the first at index idx) in thread
+// order; before grows by the step's weight.  The thread that reaches the target
+// writes its token; until then each step's last positive weight does.
+__device__ __forceinline__ void draw_in_block(Shared &sm, uint64_t target, uint64_t &before,
+                                              const uint64_t (&q)[4], uint64_t s4, int idx,
+                                              int32_t *token) {
+    if (before > target) return;  // (uniform)
+    const int tid = threadIdx.x;
+    if (tid == 0) sm.last = -1;
+    const uint64_t inc = block_scan64(s4, sm);
+    if (s4) atomicMax(&sm.last, tid);
+    if (tid == kThreads - 1) sm.bin_m = inc;
+    __syncthreads();
+    const uint64_t step = sm.bin_m;
+    const bool hit = before + inc > target && before + inc - s4 <= target;
+    const bool rest = before + step <= target && tid == sm.last;
+    if (hit || rest) {
+        uint64_t c = before + inc - s4;
+        int at = 0;
+        for (int k = 0; k < 4; ++k) {
+            if (q[k]) at = k;
+            c += q[k];
+            if (c > target) break;
+        }
+        *token = idx + at;
+    }
+    before += step;
+    __syncthreads();
+}
+
 template <typename T, bool kResident>
 __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleArgs a) {
     using R = Row<T, kResident>;
@@ -779,43 +833,31 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
             if (c < rank) before += t;
             total += t;
         }
+        cluster_reads_done();
         if (a.tokens) {
-            const uint64_t target = draw_target(total);
-            for (int w = 0; w < warp; ++w) before += sm.wsum[w];
-            if (before <= target && target < before + sum) {
-                // this warp's segment holds the draw: its weights again, from
-                // the input (single weights round to units, so the last
-                // positive one takes a target past their sum)
-                int last = -1;
-                bool found = false;
-                for (int x0 = w0; x0 < w1 && !found; x0 += 128) {
-                    uint64_t w[4], s4 = 0;
+            const int w = warp_of_target(sm, draw_target(total), before);
+            if (w >= 0) {  // the draw is in warp w's segment of this slice
+                // its weights again, from the input, four positions a thread
+                // (single weights round to units, so the last positive one
+                // takes a target past their sum)
+                const int x0 = w * seg, x1 = min(row.n, x0 + seg);
+                for (int base = x0; base < x1; base += 4 * kThreads) {
+                    const int x = base + 4 * tid;
+                    uint64_t q[4], s4 = 0;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int e = x0 + 4 * lane + k - row.pad;
-                        float v = e >= 0 && e < row.len ? clean(L::wide(__ldg(gs + e))) : -INFINITY;
+                        const int e = x + k - row.pad;
+                        float v = x + k < x1 && e >= 0 && e < row.len
+                                      ? clean(L::wide(__ldg(gs + e)))
+                                      : -INFINITY;
                         if (row.inf) v = v == INFINITY ? 0.f : -INFINITY;
                         float wf;
-                        w[k] = weight(v, rs, sm.tab, wf);
-                        s4 += w[k];
+                        q[k] = weight(v, rs, sm.tab, wf);
+                        s4 += q[k];
                     }
-                    const uint64_t inc = warp_scan64(s4, lane);
-                    const unsigned hit = __ballot_sync(kAll, before + inc > target);
-                    const unsigned pos = __ballot_sync(kAll, s4 > 0);
-                    const int src = hit ? __ffs(hit) - 1 : pos ? 31 - __clz(pos) : -1;
-                    if (lane == src) {
-                        uint64_t c = before + inc - s4;
-                        for (int k = 0; k < 4; ++k) {
-                            c += w[k];
-                            if (w[k]) last = x0 + 4 * lane + k;
-                            if (c > target) break;
-                        }
-                    }
-                    if (src >= 0) last = __shfl_sync(kAll, last, src);
-                    found = hit != 0;
-                    before += __shfl_sync(kAll, (unsigned long long)inc, 31);
+                    draw_in_block(sm, draw_target(total), before, q, s4, e0 + x - row.pad,
+                                  a.tokens + rowi);
                 }
-                if (lane == 0) a.tokens[rowi] = e0 + last - row.pad;
             }
         }
         if (prow) {
@@ -840,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
                     if (x >= row.pad && x < row.pad + row.len) out[x] = slice[x] * inv;
             }
         }
-        cluster_sync();  // x_sum has been read everywhere
+        cluster_wait_reads();
         return;
     }
 
@@ -951,28 +993,43 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
                 for (int k = 0; k < 4; ++k) {
                     if (e[k] < pivot || e[k] == -INFINITY) continue;
                     const int at = atomicAdd(&sm.n_list, 1);
-                    if (at < kListMax) {
-                        sm.list.val[at] = e[k];
-                        sm.list.idx[at] = e0 + x + k - row.pad;
-                    }
+                    if (at < kListMax)
+                        sm.list.own[at] = (uint64_t)~float_key(e[k]) << 32 |
+                                          (uint32_t)(e0 + x + k - row.pad);
                 }
             }
         }
         cluster_sync();
         int n = 0;
         if (list) {
-            for (uint32_t c = 0; c < ncta; ++c) {
-                const Shared *o = reinterpret_cast<const Shared *>(map_to_rank(&sm, c));
-                const int m = o->n_list;
-                if (n + m <= kListMax) {
-                    for (int x = tid; x < m; x += kThreads)
-                        sm.list.a[n + x] =
-                            (uint64_t)~float_key(o->list.val[x]) << 32 | (uint32_t)o->list.idx[x];
+            // the CTAs' counts, one a lane, then every entry of every list at once:
+            // a remote read takes most of a microsecond
+            const int m = lane < (int)ncta ? *map_to_rank(&sm.n_list, lane) : 0;
+            int ends = m;
+#pragma unroll
+            for (int o = 1; o < kMaxCluster; o <<= 1) {
+                const int t = __shfl_up_sync(kAll, ends, o);
+                if (lane >= o) ends += t;
+            }
+            n = __shfl_sync(kAll, ends, kMaxCluster - 1);
+            if (n <= kListMax) {
+                for (int x0 = warp * 32; x0 < n; x0 += kThreads) {
+                    const int x = x0 + lane;
+                    int c = 0, from = 0;
+#pragma unroll
+                    for (int q = 0; q < kMaxCluster - 1; ++q) {
+                        const int e = __shfl_sync(kAll, ends, q);
+                        if (x >= e) {
+                            c = q + 1;
+                            from = e;
+                        }
+                    }
+                    if (x < n) sm.list.a[x] = map_to_rank(sm.list.own, c)[x - from];
                 }
-                n += m;
             }
             list = n <= kListMax && n > 0;
         }
+        cluster_reads_done();  // (of the lists)
         // ---- the exact cut
         if (list) {  // (uniform over the cluster)
             __syncthreads();
@@ -1070,11 +1127,12 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
                             a.tokens[rowi] = (int)(keys[2 * tid + 1] >> 32);
                     }
                 }
-                cluster_sync();  // the lists have been read everywhere
+                cluster_wait_reads();
                 return;
             }
         }
-        cluster_sync();  // the lists have been read everywhere: the histograms may follow
+        __syncthreads();
+        cluster_wait_reads();  // the lists have been read everywhere: histograms may follow
     }
 
     // ================================================= any row, by selection
@@ -1177,15 +1235,16 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
     }
 
     // ---- kept weight, the draw, the distribution
-    auto in_cut = [&](float v, int x) {
+    auto in_cut_by = [&](float v, int x, int ends) {
         if (!(use_k || use_p)) return true;
         const uint32_t key = R::key(v);
-        return key > cut.key || (key == cut.key && x < tie_end);
+        return key > cut.key || (key == cut.key && x < ends);
     };
-    auto kept = [&](int x, float &wf) -> uint64_t {
+    auto in_cut = [&](float v, int x) { return in_cut_by(v, x, tie_end); };
+    auto kept = [&](int x, float &wf, int ends) -> uint64_t {
         const float v = row.at(x);
         wf = 0.f;
-        if (!in_cut(v, x)) return 0;
+        if (!in_cut_by(v, x, ends)) return 0;
         const uint64_t w = weight(v, rs, sm.tab, wf);
         if (w < wmin) {
             wf = 0.f;
@@ -1196,7 +1255,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
     uint64_t sum = 0;
     for_selected(row, w0, w1, lane, in_cut, [&](int x) {
         float wf;
-        sum += kept(x, wf);
+        sum += kept(x, wf, tie_end);
     });
     sum = warp_sum64(sum);
     if (lane == 0) sm.wsum[warp] = sum;
@@ -1213,23 +1272,25 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
         if (c < rank) before += t;
         total += t;
     }
+    cluster_reads_done();  // (of x_sum)
     if (a.tokens) {
         const uint64_t target = draw_target(total);
-        for (int w = 0; w < warp; ++w) before += sm.wsum[w];
-        if (before <= target && target < before + sum) {
-            // this warp: lane sums over contiguous runs, the lane, the element
-            const int run = seg / 32, x0 = min(w1, w0 + lane * run), x1 = min(w1, x0 + run);
-            uint64_t ls = 0;
-            float wf;
-            for (int x = x0; x < x1; ++x) ls += kept(x, wf);
-            uint64_t c = before + warp_scan64(ls, lane) - ls;
-            if (c <= target && target < c + ls) {
-                int x = x0;
-                for (;; ++x) {
-                    c += kept(x, wf);
-                    if (c > target || x + 1 >= x1) break;
+        const int w = warp_of_target(sm, target, before);
+        if (w >= 0) {  // the draw is in warp w's segment of this slice
+            // (that warp's ties end where it says)
+            if (warp == w && lane == 0) sm.bin = tie_end;
+            __syncthreads();
+            const int x0 = w * seg, x1 = min(row.n, x0 + seg), ends = sm.bin;
+            for (int base = x0; base < x1; base += 4 * kThreads) {
+                const int x = base + 4 * tid;
+                uint64_t q[4], s4 = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float wf;
+                    q[k] = x + k < x1 ? kept(x + k, wf, ends) : 0;
+                    s4 += q[k];
                 }
-                a.tokens[rowi] = e0 + x - row.pad;
+                draw_in_block(sm, target, before, q, s4, e0 + x - row.pad, a.tokens + rowi);
             }
         }
     }
@@ -1241,11 +1302,11 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
         __syncwarp();
         for_selected(row, w0, w1, lane, in_cut, [&](int x) {
             float wf;
-            kept(x, wf);
+            kept(x, wf, tie_end);
             if (x >= row.pad && x < row.pad + row.len) prow[x - row.pad] = wf * inv;
         });
     }
-    cluster_sync();  // this CTA's shared memory has been read everywhere
+    cluster_wait_reads();
 }
 
 template <typename T>
