@@ -19,27 +19,29 @@
 // their rounding moves one draw in about a thousand to a neighbouring token,
 // against one in 10^5 here.
 //
-// Layout.  One thread-block cluster per row, its CTAs the vocabulary slices,
-// each slice resident in shared memory as fp32: the logits are read from HBM
-// once, every later pass runs on chip.
-//   no filter   one pass for the weights (kept in place of the logits) and their
-//               sum, one that scales and stores them;
-//   filters     a pivot below which nothing can be kept, from the threads' own
-//               maxima (the k-th largest of them is at most the k-th largest
-//               logit, and their weights bound the weight above a pivot from
-//               below); the few logits above it are sorted and cut exactly, the
-//               row is zeros but for the kept ones;
-//   otherwise   (more than kListMax candidates: flat rows, long runs of ties, a
-//               slice that does not fit) radix selection on the logits' ordered
-//               bit patterns: each level is a histogram (count and weight) over
-//               the current key range, summed over the cluster through
-//               distributed shared memory; the bin that holds the cut becomes
-//               the next range, until it is a single key.
+// Layout.  One thread-block cluster per row (of one CTA when there are rows
+// enough), its CTAs the vocabulary slices.  Two kernels:
+//   sample_full    no filter arrays, rows that fit: every slice resident in
+//                  shared memory as fp32, so the logits are read from HBM once;
+//                  one pass for the weights (kept in place of the logits) and
+//                  their sum, one that scales and stores them.
+//   sample_cut     filters: the row is streamed once for the maxima of some
+//                  thousand parts of it (and, with probs, zeros are stored); a
+//                  pivot below which nothing can be kept comes from those maxima
+//                  (the k-th largest of them is at most the k-th largest logit,
+//                  and their weights bound the weight above a pivot from below);
+//                  the few logits above it are sorted and cut exactly.
+//                  Otherwise (more than kListMax candidates: flat rows, long runs
+//                  of ties; no active filter) radix selection on the logits'
+//                  ordered bit patterns: each level is a histogram (count and
+//                  weight) over the current key range, summed over the cluster
+//                  through distributed shared memory; the bin that holds the cut
+//                  becomes the next range, until it is a single key.  These
+//                  passes read the row again, mostly from L2.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
-
-#include <atomic>
+#include <limits.h>
 
 #include "bdsa_device.cuh"
 #include "bdsa_internal.h"
@@ -47,9 +49,12 @@
 namespace bdsa {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;      // sample_cut
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 512;  // one a thread
+constexpr int kFullThreads = 256;  // sample_full: room for its constants as packed pairs
+constexpr int kFullWarps = kFullThreads / 32;
+constexpr int kBins = 512;         // one a thread of sample_cut
+constexpr int kParts = 8;          // parts of a thread's share of a slice, a maximum each
 constexpr int kMaxCluster = 8;
 constexpr int kListMax = 1024;  // candidates the sorted list holds
 constexpr int kUnitLog2 = 41;  // a weight's unit is 2^-41 of the row's largest
@@ -81,10 +86,35 @@ constexpr ExpTable make_exp_table() {
 }
 __device__ const ExpTable g_exp_table = make_exp_table();
 
-// log2(e) / T as two floats, and the row's largest logit.
+// A row's weights are 2^(y - E), y = c l with c = log2(e) / T = ch + cl and E an
+// integer above the largest y (so the largest weight is in [1/2, 1]): a plain
+// product and an exponent, without the subtraction of the largest logit, whose
+// rounding would have to be carried along.  Rows with |c lmax| >= 2^17 (very small
+// temperatures) are `wide`: y = c (l - lmax), E = 0.
 struct RowScale {
     float lmax, ch, cl;
+    float ymin;        // weights with y <= ymin are zero (2^-124 of the scale)
+    uint32_t ebits;    // (127 - E) << 23, modulo 2^32
+    bool wide;
 };
+__device__ __forceinline__ RowScale row_scale(float lmax, float temp) {
+    // log2(e) / T as two floats by a corrected fp32 division (a double one costs
+    // every thread of the CTA some twenty fp64 instructions, which this GPU runs
+    // at 1/64 of the fp32 rate); temperatures below 1e-30 act as 1e-30
+    constexpr float kL2e = 1.44269502162933349609375f, kL2el = 1.925963033500011e-08f;
+    RowScale rs;
+    const float t = fmaxf(temp, 1e-30f);
+    rs.lmax = lmax;
+    rs.ch = __fdiv_rn(kL2e, t);
+    const float rest = fmaf(-rs.ch, t, kL2e) + kL2el;
+    rs.cl = __fdiv_rn(rest, t);
+    const float y = lmax * rs.ch;
+    rs.wide = !(fabsf(y) < 131072.f);
+    const int E = rs.wide ? 0 : (int)floorf(y) + 1;
+    rs.ymin = (float)(E - 124);
+    rs.ebits = (uint32_t)(127 - E) << 23;
+    return rs;
+}
 
 // One lane value, or a packed pair, with the same operations.
 struct V1 {
@@ -106,88 +136,93 @@ __device__ __forceinline__ V1 splat<V1>(float x) { return {x}; }
 template <>
 __device__ __forceinline__ V2 splat<V2>(float x) { return {f2_pack(x, x)}; }
 
-// Table entry and power of two of k sixteenths, from t = k + 1.5 * 2^23 (k <= 0):
-// the float's low bits are k's, and 2^19 of them shift the constant's out.
+// Table entry and power of two of k sixteenths, from t = k + 1.5 * 2^23: the
+// float's low bits are k's, and 19 places up only k's own remain.
 __device__ __forceinline__ float2 table_at(const ExpTable &tab, float t) {
     return tab.v[__float_as_uint(t) & 15u];
 }
-__device__ __forceinline__ float pow2_at(float t) {
-    return __uint_as_float(((__float_as_uint(t) << 19) & 0xff800000u) + 0x3f800000u);
+__device__ __forceinline__ float pow2_at(float t, uint32_t ebits) {
+    return __uint_as_float(((__float_as_uint(t) << 19) & 0xff800000u) + ebits);
 }
-// Weights below 2^-124 (and those of -inf and NaN) are zero.
-constexpr float kMinLog2 = -124.f;
-
-__device__ __forceinline__ void lookup(const ExpTable &tab, V1 t, V1 &th, V1 &tl, V1 &sc) {
+__device__ __forceinline__ void lookup(const ExpTable &tab, uint32_t ebits, V1 t, V1 &th, V1 &tl,
+                                       V1 &sc) {
     const float2 e = table_at(tab, t.a);
     th.a = e.x;
     tl.a = e.y;
-    sc.a = pow2_at(t.a);
+    sc.a = pow2_at(t.a, ebits);
 }
-__device__ __forceinline__ void lookup(const ExpTable &tab, V2 t, V2 &th, V2 &tl, V2 &sc) {
+__device__ __forceinline__ void lookup(const ExpTable &tab, uint32_t ebits, V2 t, V2 &th, V2 &tl,
+                                       V2 &sc) {
     const float2 u = f2_unpack(t.a);
     const float2 e0 = table_at(tab, u.x), e1 = table_at(tab, u.y);
     th.a = f2_pack(e0.x, e1.x);
     tl.a = f2_pack(e0.y, e1.y);
-    sc.a = f2_pack(pow2_at(u.x), pow2_at(u.y));
+    sc.a = f2_pack(pow2_at(u.x, ebits), pow2_at(u.y, ebits));
 }
-__device__ __forceinline__ void keep_normal(V1 yn, V1 &h, V1 &l) {
-    const bool ok = yn.a < -kMinLog2;
+// Zero where y <= ymin (and for -inf and NaN).
+__device__ __forceinline__ void keep_above(V1 y, float ymin, V1 &h, V1 &l) {
+    const bool ok = y.a > ymin;
     h.a = ok ? h.a : 0.f;
     l.a = ok ? l.a : 0.f;
 }
-__device__ __forceinline__ void keep_normal(V2 yn, V2 &h, V2 &l) {
-    const float2 y = f2_unpack(yn.a);
+__device__ __forceinline__ void keep_above(V2 y, float ymin, V2 &h, V2 &l) {
+    const float2 v = f2_unpack(y.a);
     float2 a = f2_unpack(h.a), b = f2_unpack(l.a);
-    if (!(y.x < -kMinLog2)) a.x = b.x = 0.f;
-    if (!(y.y < -kMinLog2)) a.y = b.y = 0.f;
+    if (!(v.x > ymin)) a.x = b.x = 0.f;
+    if (!(v.y > ymin)) a.y = b.y = 0.f;
     h.a = f2_pack(a.x, a.y);
     l.a = f2_pack(b.x, b.y);
 }
 
-// 2^(c (l - lmax)) as wh + wl, |wl| <= ulp(wh) / 2.  The difference is exact
-// (TwoSum: even of 16-bit logits it can need more than 24 bits), its product
-// with c is -yn + yl, y's sixteenths go to the table and the power of two, and
-// the rest r, |r| <= 1/32, with z = r + yl, to
-//   2^z - 1 = r L + (r Ll + yl L + z^2 (c2 + c3 z + c4 z^2 + c5 z^3)).
-template <class V>
+// The weight of l as wh + wl, |wl| <= ulp(wh) / 2.  y = yh + yl (kWide: of the
+// difference to lmax, with its TwoSum error); y's sixteenths go to the table and
+// the power of two, and the rest r of yh, |r| <= 1/32, with z = r + yl, to
+//   2^z - 1 = r L + (yl L + z^2 (c2 + c3 z + c4 z^2 + c5 z^3)),  L = ln 2
+// (as a float: its rounding, 2^-28 of itself, is 2^-33 of the weight).
+template <class V, bool kWide>
 __device__ __forceinline__ void weight_ff(V l, const RowScale &rs, const ExpTable &tab, V &wh,
                                           V &wl) {
-    const V one_n = splat<V>(-1.f), lmax = splat<V>(rs.lmax), ch = splat<V>(rs.ch);
-    const V dh = l + splat<V>(-rs.lmax);
-    const V yn = dh * splat<V>(-rs.ch);  // -y >= 0
-    V yl = vfma(dh, ch, yn);
-    yl = vfma(dh, splat<V>(rs.cl), yl);
-    const V bb = vfma(l, one_n, dh);
-    const V dl = vfma(lmax + bb, one_n, vfma(vfma(bb, one_n, dh), one_n, l));
-    yl = vfma(dl, ch, yl);
-    const V t = vfma(yn, splat<V>(-16.f), splat<V>(12582912.f));  // round to an integer
-    const V rn = vfma(t + splat<V>(-12582912.f), splat<V>(0.0625f), yn);  // -r, exact
-    const V r = rn * one_n;
-    constexpr float kL = 0.693147182464599609375f, kLl = -1.904654323148236017e-09f;
+    const V one_n = splat<V>(-1.f), ch = splat<V>(rs.ch);
+    V yh, yl;
+    if constexpr (kWide) {
+        const V dh = l + splat<V>(-rs.lmax);
+        const V bb = vfma(l, one_n, dh);
+        const V dl =
+            vfma(splat<V>(rs.lmax) + bb, one_n, vfma(vfma(bb, one_n, dh), one_n, l));
+        yh = dh * ch;
+        yl = vfma(dh, ch, yh * one_n);
+        yl = vfma(dl, ch, vfma(dh, splat<V>(rs.cl), yl));
+    } else {
+        yh = l * ch;
+        yl = vfma(l, splat<V>(rs.cl), vfma(l, ch, yh * one_n));
+    }
+    const V t = vfma(yh, splat<V>(16.f), splat<V>(12582912.f));  // round to an integer
+    const V r = vfma(t + splat<V>(-12582912.f), splat<V>(-0.0625f), yh);  // exact
     const V z = r + yl;
+    constexpr float kL = 0.693147182464599609375f;
     V h = vfma(z, splat<V>(1.3333558e-3f), splat<V>(9.6181291e-3f));
     h = vfma(z, h, splat<V>(5.5504109e-2f));
     h = vfma(z, h, splat<V>(2.40226507e-1f));
-    V lo = vfma(r, splat<V>(kLl), yl * splat<V>(kL));
-    lo = vfma(z * z, h, lo);
+    const V lo = vfma(z * z, h, yl * splat<V>(kL));
     const V e = vfma(r, splat<V>(kL), lo);
     V th, tl, sc;
-    lookup(tab, t, th, tl, sc);
+    lookup(tab, rs.ebits, t, th, tl, sc);
     const V b = vfma(th, e, tl);
     const V s = th + b;                                // Fast2Sum: s + (b - (s - th)) exactly
     const V q = vfma(vfma(th, one_n, s), one_n, b);
     wh = s * sc;
     wl = q * sc;
-    keep_normal(yn, wh, wl);
+    keep_above(yh, rs.ymin, wh, wl);
 }
 
 constexpr float kUnits = 2199023255552.f;  // 2^kUnitLog2
 
-// The weight in units of 2^-41 of the largest and, in wf, as a float.
+// The weight in units of 2^-41 of the scale and, in wf, as a float.
 __device__ __forceinline__ uint64_t weight(float l, const RowScale &rs, const ExpTable &tab,
                                            float &wf) {
     V1 wh, wl;
-    weight_ff<V1>(V1{l}, rs, tab, wh, wl);
+    if (rs.wide) weight_ff<V1, true>(V1{l}, rs, tab, wh, wl);
+    else weight_ff<V1, false>(V1{l}, rs, tab, wh, wl);
     wf = wh.a;
     return (uint64_t)(__float2ll_rn(wh.a * kUnits) + (long long)__float2int_rn(wl.a * kUnits));
 }
@@ -295,7 +330,353 @@ __device__ __forceinline__ uint64_t warp_scan64(uint64_t v, int lane) {
     return v;
 }
 
-// ------------------------------------------------------------ shared state
+// ------------------------------------------------------------ one CTA's sums
+// Inclusive prefix sums of v over a CTA of NW warps, in thread order.
+template <int NW>
+__device__ __forceinline__ uint64_t block_scan64(uint64_t v, uint64_t *scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t t = warp_scan64(v, lane);
+    if (lane == 31) scratch[warp] = t;
+    __syncthreads();
+    uint64_t before = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) before += w < warp ? scratch[w] : 0;
+    __syncthreads();
+    return before + t;
+}
+
+// What the draw needs: the weight of each warp's contiguous segment of the slice,
+// and scratch.
+template <int NW>
+struct DrawShared {
+    uint64_t wsum[NW], scan[NW], step, x_sum;  // x_sum: the slice's weight, read by the cluster
+    int last;
+};
+
+// Sets sum (each warp's segment weight, in every lane) up for the draw: total is
+// the cluster's weight, before the weight in front of this slice.
+template <int NW>
+__device__ __forceinline__ void share_sums(DrawShared<NW> &d, uint64_t sum, uint32_t ncta,
+                                           uint32_t rank, uint64_t &total, uint64_t &before) {
+    if ((threadIdx.x & 31) == 0) d.wsum[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint64_t t = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) t += d.wsum[w];
+        d.x_sum = t;
+    }
+    cluster_sync();
+    uint64_t x[kMaxCluster];
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) x[c] = c < ncta ? *map_to_rank(&d.x_sum, c) : 0;
+    total = before = 0;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) {
+        if (c < (int)rank) before += x[c];
+        total += x[c];
+    }
+}
+
+// The warp whose segment of this slice holds the target, or -1; before (the
+// weight in front of the slice) becomes the weight in front of that segment.
+// Uniform over the CTA.
+template <int NW>
+__device__ __forceinline__ int warp_of_target(const DrawShared<NW> &d, uint64_t target,
+                                              uint64_t &before) {
+    if (target < before) return -1;
+    for (int w = 0; w < NW; ++w) {
+        if (target < before + d.wsum[w]) return w;
+        before += d.wsum[w];
+    }
+    return -1;
+}
+
+// One step of the draw by the whole CTA: every thread brings the weights q[4] of
+// four successive indices (their sum s4, the first at index idx) in thread
+// order; before grows by the step's weight.  The thread that reaches the target
+// writes its token; until then each step's last positive weight does.
+template <int NW>
+__device__ __forceinline__ void draw_in_block(DrawShared<NW> &d, uint64_t target,
+                                              uint64_t &before, const uint64_t (&q)[4],
+                                              uint64_t s4, int idx, int32_t *token) {
+    if (before > target) return;  // (uniform)
+    const int tid = threadIdx.x;
+    if (tid == 0) d.last = -1;
+    const uint64_t inc = block_scan64<NW>(s4, d.scan);
+    if (s4) atomicMax(&d.last, tid);
+    if (tid == NW * 32 - 1) d.step = inc;
+    __syncthreads();
+    const uint64_t step = d.step;
+    const bool hit = before + inc > target && before + inc - s4 <= target;
+    const bool rest = before + step <= target && tid == d.last;
+    if (hit || rest) {
+        uint64_t c = before + inc - s4;
+        int at = 0;
+        for (int k = 0; k < 4; ++k) {
+            if (q[k]) at = k;
+            c += q[k];
+            if (c > target) break;
+        }
+        *token = idx + at;
+    }
+    before += step;
+    __syncthreads();
+}
+
+// floor(u * total), below total; u outside [0, 1) is clamped.
+__device__ __forceinline__ uint64_t draw_target(float u, uint64_t total) {
+    return u > 0.f ? (u < 1.f ? scaled(u, total, false) : total - 1) : 0;
+}
+
+// 2^kUnitLog2 / total, rounded once (to within 2^-46).
+__device__ __forceinline__ float inverse(uint64_t total) {
+    const float hi = __ull2float_rz(total);  // hi <= total, both in units
+    const float lo = __ull2float_rn(total - (uint64_t)hi);
+    const float i0 = __fdiv_rn(kUnits, hi);
+    // i0 + (kUnits - i0 (hi + lo)) / hi
+    return i0 + __fdividef(fmaf(-i0, lo, fmaf(-i0, hi, kUnits)), hi);
+}
+
+// The logit as the weights see it when the row's largest is +inf: the +inf ones
+// share the weight.
+__device__ __forceinline__ float if_inf(float v) { return v == INFINITY ? 0.f : -INFINITY; }
+
+// ============================================================ sample_full
+// The weights of positions [x0, x1) of a resident slice (multiples of 256) and
+// their sum, one warp, eight positions a lane and step; kStore: the weights
+// replace the logits.  Returns the lane's sum in units.  A running sum stays below
+// 64 (a slice of at most 48640 positions gives a lane's each at most 24 weights),
+// so one that starts at 64 makes every addition a Fast2Sum, with remainders
+// below 2^-18 whose own sum rounds at 2^-40.
+template <bool kStore, bool kWide>
+__device__ __forceinline__ uint64_t sum_slice(float *s, int x0, int x1, const RowScale &rs,
+                                              const ExpTable &tab, int lane) {
+    constexpr float kBase = 64.f;
+    const V2 neg = splat<V2>(-1.f);
+    V2 acc[4], low[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        acc[k] = splat<V2>(kBase);
+        low[k] = splat<V2>(0.f);
+    }
+    for (int x = x0 + 4 * lane; x < x1; x += 256) {
+        float4 v[2] = {*reinterpret_cast<const float4 *>(s + x),
+                       *reinterpret_cast<const float4 *>(s + x + 128)};
+        float *f = reinterpret_cast<float *>(v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            V2 h, l;
+            weight_ff<V2, kWide>(V2{f2_pack(f[2 * k], f[2 * k + 1])}, rs, tab, h, l);
+            const V2 t = acc[k] + h;
+            const V2 err = vfma(vfma(acc[k], neg, t), neg, h);  // h - (t - acc)
+            acc[k] = t;
+            low[k] = low[k] + (err + l);
+            const float2 w = f2_unpack(h.a);
+            f[2 * k] = w.x;
+            f[2 * k + 1] = w.y;
+        }
+        if (kStore) {
+            *reinterpret_cast<float4 *>(s + x) = v[0];
+            *reinterpret_cast<float4 *>(s + x + 128) = v[1];
+        }
+    }
+    long long sum = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 a = f2_unpack(acc[k].a), b = f2_unpack(low[k].a);
+        sum += __float2ll_rn((a.x - kBase) * kUnits) + __float2ll_rn((a.y - kBase) * kUnits) +
+               __float2ll_rn(b.x * kUnits) + __float2ll_rn(b.y * kUnits);
+    }
+    return (uint64_t)max(sum, 0ll);
+}
+
+struct FullShared {
+    ExpTable tab;
+    DrawShared<kFullWarps> draw;
+    float red[kFullWarps];
+    float x_max;  // read by the cluster
+    int x_first;  // greedy rows: the slice's first largest logit; read by the cluster
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kFullThreads, 2) sample_full_kernel(const SampleArgs a) {
+    using L = Logit<T>;
+    using Raw = typename L::Raw;
+    extern __shared__ __align__(16) uint8_t s_dyn[];
+    __shared__ FullShared sm;
+    float *slice = reinterpret_cast<float *>(s_dyn);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t ncta = (uint32_t)a.ncta, rank = ncta > 1 ? cluster_rank() : 0u;
+    const long rowi = blockIdx.x / ncta;
+    const int r = (int)(rowi / a.B), i = (int)(rowi % a.B);
+    const int e0 = min(a.V, (int)rank * a.slice), len = min(a.V, e0 + a.slice) - e0;
+    const Raw *gs = static_cast<const Raw *>(a.logits) + r * a.lsr + i * a.lsi + e0;
+    constexpr int kVec = 16 / (int)sizeof(Raw);
+    // positions x = index - e0 + pad: the slice keeps its offset from a 16-byte
+    // boundary; -inf in front and behind, up to a multiple of 256
+    const int pad = (int)((reinterpret_cast<uintptr_t>(gs) & 15) / sizeof(Raw));
+    const int n = (len + pad + 255) & ~255;
+    const float temp = a.temperature ? a.temperature[r] : 1.f;
+    const bool bad_temp = !(temp >= 0.f) || temp == INFINITY;
+    float *prow = a.probs ? a.probs + r * a.psr + i * a.psi + e0 : nullptr;
+    if (tid < 16) sm.tab.v[tid] = g_exp_table.v[tid];
+
+    // ---- the slice into shared memory, its largest logit
+    float mx = -INFINITY;
+    {
+        const int head = min(len, pad ? kVec - pad : 0);
+        const int nvec = (len - head) / kVec, tail = head + nvec * kVec;
+        float *dst = slice + pad;
+        if (tid < head) {
+            mx = clean(L::wide(__ldg(gs + tid)));
+            dst[tid] = mx;
+        }
+        if (tid < len - tail) {
+            const float v = clean(L::wide(__ldg(gs + tail + tid)));
+            dst[tail + tid] = v;
+            mx = fmaxf(mx, v);
+        }
+        if (tid < pad) slice[tid] = -INFINITY;
+        if (tid < n - pad - len) dst[len + tid] = -INFINITY;
+        const uint4 *gv = reinterpret_cast<const uint4 *>(gs + head);
+        float *sv = dst + head;
+        auto take = [&](uint4 q, int x) {
+            const Raw *e = reinterpret_cast<const Raw *>(&q);
+#pragma unroll
+            for (int k = 0; k < kVec; k += 4) {
+                float4 v;
+                v.x = clean(L::wide(e[k]));
+                v.y = clean(L::wide(e[k + 1]));
+                v.z = clean(L::wide(e[k + 2]));
+                v.w = clean(L::wide(e[k + 3]));
+                mx = max3f(max3f(mx, v.x, v.y), v.z, v.w);
+                *reinterpret_cast<float4 *>(sv + x * kVec + k) = v;
+            }
+        };
+        constexpr int kU = 8;  // loads in flight a thread
+        int x = tid;
+        for (; x + (kU - 1) * kFullThreads < nvec; x += kU * kFullThreads) {
+            uint4 q[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) q[u] = __ldcs(gv + x + u * kFullThreads);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) take(q[u], x + u * kFullThreads);
+        }
+        for (; x < nvec; x += kFullThreads) take(__ldcs(gv + x), x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+    if (lane == 0) sm.red[warp] = mx;
+    __syncthreads();
+    mx = sm.red[lane % kFullWarps];
+#pragma unroll
+    for (int o = kFullWarps / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+    if (tid == 0) sm.x_max = mx;
+    cluster_sync();
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c)
+        if (c < ncta) mx = fmaxf(mx, *map_to_rank(&sm.x_max, c));
+    if (bad_temp || mx == -INFINITY) {  // no distribution (uniform over the cluster)
+        cluster_reads_done();
+        if (prow)
+            for (int x = tid; x < len; x += kFullThreads) prow[x] = 0.f;
+        if (rank == 0 && tid == 0) {
+            if (a.tokens) a.tokens[rowi] = -1;
+            report_status(a.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
+        }
+        cluster_wait_reads();
+        return;
+    }
+    if (temp == 0.f) {  // greedy: the first largest logit alone
+        if (tid == 0) sm.x_first = INT_MAX;
+        __syncthreads();
+        int first = INT_MAX;
+        for (int x = tid; x < n && first == INT_MAX; x += kFullThreads)
+            if (slice[x] == mx) first = e0 + x - pad;
+        first = __reduce_min_sync(kAll, first);
+        if (lane == 0) atomicMin(&sm.x_first, first);
+        cluster_sync();
+        first = lane < (int)ncta ? *map_to_rank(&sm.x_first, lane) : INT_MAX;
+        first = __reduce_min_sync(kAll, first);
+        cluster_reads_done();
+        if (prow)
+            for (int x = tid; x < len; x += kFullThreads) prow[x] = e0 + x == first ? 1.f : 0.f;
+        if (a.tokens && rank == 0 && tid == 0) a.tokens[rowi] = first;
+        cluster_wait_reads();
+        return;
+    }
+    const bool inf = mx == INFINITY;
+    if (inf) {
+        for (int x = tid; x < n; x += kFullThreads) slice[x] = if_inf(slice[x]);
+        mx = 0.f;
+        __syncthreads();
+    }
+    const RowScale rs = row_scale(mx, temp);
+    const int seg = ((n + kFullWarps - 1) / kFullWarps + 255) & ~255;
+    const int w0 = min(n, warp * seg), w1 = min(n, w0 + seg);
+    uint64_t sum;
+    if (prow)
+        sum = rs.wide ? sum_slice<true, true>(slice, w0, w1, rs, sm.tab, lane)
+                      : sum_slice<true, false>(slice, w0, w1, rs, sm.tab, lane);
+    else
+        sum = rs.wide ? sum_slice<false, true>(slice, w0, w1, rs, sm.tab, lane)
+                      : sum_slice<false, false>(slice, w0, w1, rs, sm.tab, lane);
+    sum = warp_sum64(sum);
+    uint64_t total, before;
+    share_sums(sm.draw, sum, ncta, rank, total, before);
+    cluster_reads_done();
+    if (prow) {
+        const float inv = inverse(total);
+        float *out = prow - pad;
+        if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+#pragma unroll 2
+            for (int x = w0 + 4 * lane; x < w1; x += 128) {
+                const float4 v = *reinterpret_cast<const float4 *>(slice + x);
+                if (x >= pad && x + 4 <= pad + len) {
+                    __stcs(reinterpret_cast<float4 *>(out + x),
+                           make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                } else {
+                    const float e[4] = {v.x, v.y, v.z, v.w};
+                    for (int k = 0; k < 4; ++k)
+                        if (x + k >= pad && x + k < pad + len) out[x + k] = e[k] * inv;
+                }
+            }
+        } else {
+            __syncwarp();
+            for (int x = w0 + lane; x < w1; x += 32)
+                if (x >= pad && x < pad + len) __stcs(out + x, slice[x] * inv);
+        }
+    }
+    if (a.tokens) {
+        const uint64_t target = draw_target(a.u[rowi], total);
+        const int w = warp_of_target(sm.draw, target, before);
+        if (w >= 0) {  // the draw is in warp w's segment of this slice
+            // its weights again, from the input, four positions a thread (single
+            // weights round to units, so the last positive one takes a target
+            // past their sum)
+            const int x0 = w * seg, x1 = min(n, x0 + seg);
+            for (int base = x0; base < x1; base += 4 * kFullThreads) {
+                const int x = base + 4 * tid;
+                uint64_t q[4], s4 = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int e = x + k - pad;
+                    float v = x + k < x1 && e >= 0 && e < len ? clean(L::wide(__ldg(gs + e)))
+                                                              : -INFINITY;
+                    if (inf) v = if_inf(v);
+                    float wf;
+                    q[k] = weight(v, rs, sm.tab, wf);
+                    s4 += q[k];
+                }
+                draw_in_block(sm.draw, target, before, q, s4, e0 + x - pad, a.tokens + rowi);
+            }
+        }
+    }
+    cluster_wait_reads();
+}
+
+// ============================================================ sample_cut
 struct Hist {
     uint32_t cnt[kBins];
     // weight = m0 + m1 2^14 + m2 2^28: a slice has at most 2^18 logits, so no
@@ -310,24 +691,24 @@ struct Lists {
     uint64_t a[kListMax], b[kListMax];
 };
 
-struct Shared {
+struct CutShared {
     ExpTable tab;
     union {
         Hist hist[2];
         Lists list;
     };
-    float tmax[kThreads];         // largest logit of each thread's part of the slice
-    uint64_t scan_c[kWarps], scan_m[kWarps];
-    uint64_t wsum[kWarps];        // weight of each warp's segment
+    uint32_t parts[kBins];        // pivot search: this CTA's part maxima by bin
+    uint64_t scan[kWarps], scan_c[kWarps];
+    DrawShared<kWarps> draw;
     uint32_t wties[kWarps];       // cut-key elements of each warp's segment
-    float red[kWarps];
-    float tlow[kWarps];
-    int n_list, n_below, n_min;   // candidates; those below top-p's goal; past min-p
-    int last;                     // last thread with weight (draw_in_block)
+    float red[2][kWarps];
+    uint32_t hit[kListMax];       // parts that reach the pivot: thread * kParts + part
+    int n_hit, n_list, n_below, n_min;
     // cluster exchange: written by this CTA, read by all, one use each
-    uint64_t x_all, x_sum;
+    float x_max, x_low;
+    uint64_t x_all;
     uint32_t x_ties, x_min;
-    // the bin a select level chose; the list path's cut
+    // the bin a select level (or the pivot search) chose
     int bin;
     uint64_t bin_c, bin_m, bin_dc, bin_dm;
 };
@@ -344,20 +725,16 @@ struct Level {
     uint64_t c, m, dc, dm;
 };
 
-// This CTA's slice.  Positions x run over [0, n) = vocabulary indices e0 + x -
-// pad; resident slices hold them in shared memory as fp32, with -inf in the pad
-// positions in front and behind (n is a multiple of 128 then).
-template <typename T, bool kResident>
+// This CTA's slice, read from global memory (mostly L2: it has been streamed).
+template <typename T>
 struct Row {
     using L = Logit<T>;
-    const float *s;
     const typename L::Raw *g;
-    int n, pad, len;   // len: the slice's logits
-    bool inf;          // the row's maximum is +inf: +inf counts as 0, the rest as -inf
+    int n;
+    bool inf;  // the row's maximum is +inf
     __device__ __forceinline__ float at(int x) const {
-        if (kResident) return s[x];
         const float v = clean(L::wide(__ldg(g + x)));
-        return inf ? (v == INFINITY ? 0.f : -INFINITY) : v;
+        return inf ? if_inf(v) : v;
     }
     static __device__ __forceinline__ uint32_t key(float v) { return float_key(v) >> L::kKeyShift; }
     // a float of the type with this key
@@ -394,7 +771,7 @@ __device__ __forceinline__ void for_selected(const R &row, int x0, int x1, int l
 // One histogram level over the keys in [klo, khi], bin 0 the highest keys.  Every
 // thread of every CTA of the cluster ends with its bin's totals over the cluster.
 template <class R>
-__device__ Level level_hist(const R &row, int w0, int w1, Shared &sm, int buf, uint32_t klo,
+__device__ Level level_hist(const R &row, int w0, int w1, CutShared &sm, int buf, uint32_t klo,
                             uint32_t khi, int shift, const RowScale &rs, uint32_t ncta) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Hist &h = sm.hist[buf];
@@ -428,16 +805,16 @@ __device__ Level level_hist(const R &row, int w0, int w1, Shared &sm, int buf, u
     uint64_t ic = warp_scan64(lv.dc, lane), im = warp_scan64(lv.dm, lane);
     if (lane == 31) {
         sm.scan_c[warp] = ic;
-        sm.scan_m[warp] = im;
+        sm.scan[warp] = im;
     }
     __syncthreads();
     for (int w = 0; w < warp; ++w) {
         ic += sm.scan_c[w];
-        im += sm.scan_m[w];
+        im += sm.scan[w];
     }
     lv.c = ic - lv.dc;
     lv.m = im - lv.dm;
-    __syncthreads();  // scan_c / scan_m may be written again
+    __syncthreads();  // scan_c / scan may be written again
     return lv;
 }
 
@@ -452,7 +829,7 @@ __device__ __forceinline__ int range_shift(uint32_t klo, uint32_t khi) {
 // weight).  `lv` is the level over [klo, khi].  above_m: the weight of the keys
 // above the cut's; key_count: the elements with the cut's key.
 template <bool kMass, class R>
-__device__ Cut select_cut(const R &row, int w0, int w1, Shared &sm, int &buf, Level lv,
+__device__ Cut select_cut(const R &row, int w0, int w1, CutShared &sm, int &buf, Level lv,
                           uint32_t klo, uint32_t khi, uint64_t target, const RowScale &rs,
                           uint32_t ncta, uint64_t &above_m, uint64_t &key_count) {
     int shift = range_shift(klo, khi);
@@ -549,52 +926,70 @@ __device__ __forceinline__ uint64_t *sort_list(uint64_t *a, uint64_t *b, int n) 
     return a;
 }
 
-// Inclusive prefix sums of v over the CTA's threads (0 elsewhere), in thread order.
-__device__ __forceinline__ uint64_t block_scan64(uint64_t v, Shared &sm) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint64_t t = warp_scan64(v, lane);
-    if (lane == 31) sm.scan_m[warp] = t;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) t += sm.scan_m[w];
-    __syncthreads();
-    return t;
-}
 // Prefix sums of a[0, n), n <= kListMax, in place (two entries a thread).
-__device__ __forceinline__ void scan_list(uint64_t *a, int n, Shared &sm) {
+__device__ __forceinline__ void scan_list(uint64_t *a, int n, uint64_t *scratch) {
     static_assert(kListMax == 2 * kThreads, "two entries a thread");
     const int i = 2 * threadIdx.x;
     const uint64_t x = i < n ? a[i] : 0, y = i + 1 < n ? a[i + 1] : 0;
-    const uint64_t t = block_scan64(x + y, sm);
+    const uint64_t t = block_scan64<kWarps>(x + y, scratch);
     if (i < n) a[i] = t - y;
     if (i + 1 < n) a[i + 1] = t;
     __syncthreads();
 }
 
-// The weight of positions [x0, x1) of a resident slice (multiples of 128), summed
-// by one warp, four positions a lane and step.  kStore: the weights replace the
-// logits.  Returns the lane's sum in units.
-template <bool kStore>
-__device__ __forceinline__ uint64_t sum_weights(float *s, int x0, int x1, const RowScale &rs,
-                                                const ExpTable &tab, int lane) {
+// How a slice splits into 16-byte vectors: element counts of the ragged ends.
+struct Span {
+    int head, nvec, tail;  // tail: the first element behind the vectors
+};
+template <typename Raw>
+__device__ __forceinline__ Span span_of(const Raw *p, int len) {
+    constexpr int kVec = 16 / (int)sizeof(Raw);
+    const int mis = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(Raw));
+    Span s;
+    s.head = min(len, mis ? kVec - mis : 0);
+    s.nvec = (len - s.head) / kVec;
+    s.tail = s.head + s.nvec * kVec;
+    return s;
+}
+
+// The weight of the slice in units, this thread's share (every thread of the CTA).
+template <typename T, bool kWide>
+__device__ __forceinline__ uint64_t sum_stream(const Row<T> &row, const Span &sp,
+                                               const RowScale &rs, const ExpTable &tab) {
+    using L = Logit<T>;
+    using Raw = typename L::Raw;
+    constexpr int kVec = 16 / (int)sizeof(Raw);
+    const int tid = threadIdx.x;
     const V2 neg = splat<V2>(-1.f);
     V2 acc = splat<V2>(0.f), low = splat<V2>(0.f);
-    auto add = [&](V2 h, V2 l) {  // TwoSum
-        const V2 t = acc + h;
+    auto add = [&](float v0, float v1) {
+        if (row.inf) {
+            v0 = if_inf(v0);
+            v1 = if_inf(v1);
+        }
+        V2 h, l;
+        weight_ff<V2, kWide>(V2{f2_pack(v0, v1)}, rs, tab, h, l);
+        const V2 t = acc + h;  // TwoSum
         const V2 hh = vfma(acc, neg, t);
         const V2 err = vfma(vfma(hh, neg, t), neg, acc) + vfma(hh, neg, h);
         acc = t;
         low = low + (err + l);
     };
-    for (int x = x0 + 4 * lane; x < x1; x += 128) {
-        const float4 v = *reinterpret_cast<const float4 *>(s + x);
-        V2 h0, l0, h1, l1;
-        weight_ff<V2>(V2{f2_pack(v.x, v.y)}, rs, tab, h0, l0);
-        weight_ff<V2>(V2{f2_pack(v.z, v.w)}, rs, tab, h1, l1);
-        add(h0, l0);
-        add(h1, l1);
-        if (kStore) {
-            const float2 a = f2_unpack(h0.a), b = f2_unpack(h1.a);
-            *reinterpret_cast<float4 *>(s + x) = make_float4(a.x, a.y, b.x, b.y);
+    if (tid < sp.head) add(clean(L::wide(__ldg(row.g + tid))), -INFINITY);
+    if (tid < row.n - sp.tail) add(clean(L::wide(__ldg(row.g + sp.tail + tid))), -INFINITY);
+    const uint4 *gv = reinterpret_cast<const uint4 *>(row.g + sp.head);
+    constexpr int kU = 4;
+    for (int x = tid; x < sp.nvec; x += kU * kThreads) {
+        uint4 q[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            if (x + u * kThreads < sp.nvec) q[u] = __ldg(gv + x + u * kThreads);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            if (x + u * kThreads >= sp.nvec) break;
+            const Raw *e = reinterpret_cast<const Raw *>(&q[u]);
+#pragma unroll
+            for (int k = 0; k < kVec; k += 2) add(clean(L::wide(e[k])), clean(L::wide(e[k + 1])));
         }
     }
     const float2 a = f2_unpack(acc.a), b = f2_unpack(low.a);
@@ -602,85 +997,24 @@ __device__ __forceinline__ uint64_t sum_weights(float *s, int x0, int x1, const 
                       __float2ll_rn(b.x * kUnits) + __float2ll_rn(b.y * kUnits));
 }
 
-// 2^kUnitLog2 / total, rounded once (to within 2^-46).
-__device__ __forceinline__ float inverse(uint64_t total) {
-    const float hi = __ull2float_rz(total);  // hi <= total, both in units
-    const float lo = __ull2float_rn(total - (uint64_t)hi);
-    const float i0 = __fdiv_rn(kUnits, hi);
-    // i0 + (kUnits - i0 (hi + lo)) / hi
-    return i0 + __fdividef(fmaf(-i0, lo, fmaf(-i0, hi, kUnits)), hi);
-}
-
-// The warp whose segment of this slice holds the target, or -1; before (the
-// weight in front of the slice) becomes the weight in front of that segment.
-// Uniform over the CTA.
-__device__ __forceinline__ int warp_of_target(const Shared &sm, uint64_t target,
-                                              uint64_t &before) {
-    if (target < before) return -1;
-    for (int w = 0; w < kWarps; ++w) {
-        if (target < before + sm.wsum[w]) return w;
-        before += sm.wsum[w];
-    }
-    return -1;
-}
-
-// One step of the draw by the whole CTA: every thread brings the weights q[4] of
-// four successive indices (their sum s4, the first at index idx) in thread
-// order; before grows by the step's weight.  The thread that reaches the target
-// writes its token; until then each step's last positive weight does.
-__device__ __forceinline__ void draw_in_block(Shared &sm, uint64_t target, uint64_t &before,
-                                              const uint64_t (&q)[4], uint64_t s4, int idx,
-                                              int32_t *token) {
-    if (before > target) return;  // (uniform)
-    const int tid = threadIdx.x;
-    if (tid == 0) sm.last = -1;
-    const uint64_t inc = block_scan64(s4, sm);
-    if (s4) atomicMax(&sm.last, tid);
-    if (tid == kThreads - 1) sm.bin_m = inc;
-    __syncthreads();
-    const uint64_t step = sm.bin_m;
-    const bool hit = before + inc > target && before + inc - s4 <= target;
-    const bool rest = before + step <= target && tid == sm.last;
-    if (hit || rest) {
-        uint64_t c = before + inc - s4;
-        int at = 0;
-        for (int k = 0; k < 4; ++k) {
-            if (q[k]) at = k;
-            c += q[k];
-            if (c > target) break;
-        }
-        *token = idx + at;
-    }
-    before += step;
-    __syncthreads();
-}
-
-template <typename T, bool kResident>
-__global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleArgs a) {
-    using R = Row<T, kResident>;
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArgs a) {
+    using R = Row<T>;
     using L = Logit<T>;
     using Raw = typename L::Raw;
-    extern __shared__ __align__(16) uint8_t s_dyn[];
-    __shared__ Shared sm;
-    float *slice = reinterpret_cast<float *>(s_dyn);
+    constexpr int kVec = 16 / (int)sizeof(Raw);
+    __shared__ CutShared sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ncta = (uint32_t)a.ncta, rank = ncta > 1 ? cluster_rank() : 0u;
     const long rowi = blockIdx.x / ncta;
     const int r = (int)(rowi / a.B), i = (int)(rowi % a.B);
-    const Raw *grow = static_cast<const Raw *>(a.logits) + r * a.lsr + i * a.lsi;
-    const int e0 = min(a.V, (int)rank * a.slice), e1 = min(a.V, e0 + a.slice);
-    constexpr int kVec = 16 / (int)sizeof(Raw);
-    const Raw *gs = grow + e0;  // the slice
+    const int e0 = min(a.V, (int)rank * a.slice);
     R row;
-    row.g = gs;
-    row.s = slice;
-    row.len = e1 - e0;
-    // logits from the 16-byte boundary at or before the slice; a resident slice
-    // keeps that offset
-    const int mis = (int)((reinterpret_cast<uintptr_t>(gs) & 15) / sizeof(Raw));
-    row.pad = kResident ? mis : 0;
-    row.n = kResident ? (row.len + row.pad + 127) & ~127 : row.len;
+    row.n = min(a.V, e0 + a.slice) - e0;
+    row.g = static_cast<const Raw *>(a.logits) + r * a.lsr + i * a.lsi + e0;
     row.inf = false;
+    const Span sp = span_of(row.g, row.n);
+    const uint4 *gv = reinterpret_cast<const uint4 *>(row.g + sp.head);
 
     // ---- this row's parameters
     const float temp = a.temperature ? a.temperature[r] : 1.f;
@@ -688,224 +1022,138 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
     const float top_p = a.top_p ? a.top_p[r] : 1.f;
     const float min_p = a.min_p ? a.min_p[r] : 0.f;
     const bool bad_temp = !(temp >= 0.f) || temp == INFINITY;
-    const bool greedy = temp == 0.f;
-    const bool one = greedy || min_p > 1.f;  // only the first of the order is kept
+    const bool one = temp == 0.f || min_p > 1.f;  // only the first of the order is kept
     const bool use_k = one || (top_k > 0 && top_k < a.V);
     const bool use_p = !one && top_p < 1.f;
     const bool use_m = !one && min_p > 0.f;
-    const bool filtered = use_k || use_p || use_m;
     float *prow = a.probs ? a.probs + r * a.psr + i * a.psi + e0 : nullptr;
     if (tid < 16) sm.tab.v[tid] = g_exp_table.v[tid];
-    if (tid == 0) sm.n_list = sm.n_below = sm.n_min = 0;
+    if (tid == 0) sm.n_hit = sm.n_list = sm.n_below = sm.n_min = 0;
 
-    // ---- the slice into shared memory, the largest logit of each thread's part
-    float mx = -INFINITY;
+    // ---- one pass: the largest logit of each of the thread's kParts parts (vector
+    // tid + kThreads (part + kParts j), the ragged ends to part 0); zeros to probs
+    float tm[kParts];
+#pragma unroll
+    for (int u = 0; u < kParts; ++u) tm[u] = -INFINITY;
     {
-        const int head = min(row.len, mis ? kVec - mis : 0);
-        const int nvec = (row.len - head) / kVec, tail = head + nvec * kVec;
-        float *dst = slice + row.pad;
-        if (tid < head) {
-            mx = clean(L::wide(__ldg(gs + tid)));
-            if (kResident) dst[tid] = mx;
-        }
-        if (tid < row.len - tail) {
-            const float v = clean(L::wide(__ldg(gs + tail + tid)));
-            if (kResident) dst[tail + tid] = v;
-            mx = fmaxf(mx, v);
-        }
-        if (kResident) {
-            if (tid < row.pad) slice[tid] = -INFINITY;
-            if (tid < row.n - row.pad - row.len) dst[row.len + tid] = -INFINITY;
-        }
-        const uint4 *gv = reinterpret_cast<const uint4 *>(gs + head);
-        float *sv = dst + head;
-        auto take = [&](uint4 q, int x) {
-            const Raw *e = reinterpret_cast<const Raw *>(&q);
+        const Span op = prow ? span_of(reinterpret_cast<const uint32_t *>(prow), row.n)
+                             : Span{0, 0, 0};
+        const int zeros = prow ? op.nvec : 0;
+        float4 *zv = reinterpret_cast<float4 *>(prow + op.head);
+        constexpr int kZ = kVec / 4;  // 16-byte stores to each 16-byte load
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x0 = 0; x0 < sp.nvec; x0 += kParts * kThreads) {
+            const int x = x0 + tid;
+            uint4 q[kParts];
 #pragma unroll
-            for (int k = 0; k < kVec; k += 4) {
-                float4 v;
-                v.x = clean(L::wide(e[k]));
-                v.y = clean(L::wide(e[k + 1]));
-                v.z = clean(L::wide(e[k + 2]));
-                v.w = clean(L::wide(e[k + 3]));
-                mx = max3f(max3f(mx, v.x, v.y), v.z, v.w);
-                if (kResident) *reinterpret_cast<float4 *>(sv + x * kVec + k) = v;
+            for (int u = 0; u < kParts; ++u)
+                if (x + u * kThreads < sp.nvec) q[u] = __ldg(gv + x + u * kThreads);
+#pragma unroll
+            for (int u = 0; u < kParts * kZ; ++u) {
+                const int z = x0 * kZ + tid + u * kThreads;
+                if (z < zeros) __stcs(zv + z, zero);
             }
-        };
-        constexpr int kU = 4;  // loads in flight a thread
-        int x = tid;
-        for (; x + (kU - 1) * kThreads < nvec; x += kU * kThreads) {
-            uint4 q[kU];
 #pragma unroll
-            for (int u = 0; u < kU; ++u) q[u] = __ldcs(gv + x + u * kThreads);
+            for (int u = 0; u < kParts; ++u) {
+                if (x + u * kThreads >= sp.nvec) break;
+                const Raw *e = reinterpret_cast<const Raw *>(&q[u]);
 #pragma unroll
-            for (int u = 0; u < kU; ++u) take(q[u], x + u * kThreads);
+                for (int k = 0; k < kVec; k += 2)  // (max.f32 passes over NaN)
+                    tm[u] = max3f(tm[u], L::wide(e[k]), L::wide(e[k + 1]));
+            }
         }
-        for (; x < nvec; x += kThreads) take(__ldcs(gv + x), x);
+        if (tid < sp.head) tm[0] = fmaxf(tm[0], L::wide(__ldg(row.g + tid)));
+        if (tid < row.n - sp.tail) tm[0] = fmaxf(tm[0], L::wide(__ldg(row.g + sp.tail + tid)));
+        if (prow) {  // what the loop above did not reach
+            const int steps = (sp.nvec + kParts * kThreads - 1) / (kParts * kThreads);
+            for (int z = steps * kParts * kThreads * kZ + tid; z < zeros; z += kThreads)
+                __stcs(zv + z, zero);
+            if (tid < op.head) prow[tid] = 0.f;
+            if (tid < row.n - op.tail) prow[op.tail + tid] = 0.f;
+        }
     }
-    sm.tmax[tid] = mx;
-    cluster_sync();
-    // every CTA takes the row's thread maxima: ncta a thread
-    float tm[kMaxCluster], lowest = INFINITY;
-    mx = -INFINITY;
+    // the row's largest logit and its smallest part maximum
+    float mx = -INFINITY, lowest = INFINITY;
 #pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c) {
-        tm[c] = c < ncta ? map_to_rank(sm.tmax, c)[tid] : -INFINITY;
-        mx = fmaxf(mx, tm[c]);
-        if (tm[c] > -INFINITY) lowest = fminf(lowest, tm[c]);
+    for (int u = 0; u < kParts; ++u) {
+        mx = fmaxf(mx, tm[u]);
+        if (tm[u] > -INFINITY) lowest = fminf(lowest, tm[u]);
     }
+    auto reduce = [&](float &hi, float &lo, int from) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
-        lowest = fminf(lowest, __shfl_xor_sync(kAll, lowest, o));
-    }
+        for (int o = from; o > 0; o >>= 1) {
+            hi = fmaxf(hi, __shfl_xor_sync(kAll, hi, o));
+            lo = fminf(lo, __shfl_xor_sync(kAll, lo, o));
+        }
+    };
+    reduce(mx, lowest, 16);
     if (lane == 0) {
-        sm.red[warp] = mx;
-        sm.tlow[warp] = lowest;
+        sm.red[0][warp] = mx;
+        sm.red[1][warp] = lowest;
     }
     __syncthreads();
-    mx = sm.red[lane % kWarps];
-    lowest = sm.tlow[lane % kWarps];
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) {
-        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
-        lowest = fminf(lowest, __shfl_xor_sync(kAll, lowest, o));
+    mx = sm.red[0][lane % kWarps];
+    lowest = sm.red[1][lane % kWarps];
+    reduce(mx, lowest, kWarps / 2);
+    if (ncta > 1) {
+        if (tid == 0) {
+            sm.x_max = mx;
+            sm.x_low = lowest;
+        }
+        cluster_sync();
+        if (lane < (int)ncta) {
+            mx = *map_to_rank(&sm.x_max, lane);
+            lowest = *map_to_rank(&sm.x_low, lane);
+        }
+        reduce(mx, lowest, 16);
     }
     if (bad_temp || mx == -INFINITY) {  // no distribution (uniform over the cluster)
-        if (prow)
-            for (int x = tid; x < row.len; x += kThreads) prow[x] = 0.f;
+        cluster_reads_done();
         if (rank == 0 && tid == 0) {
             if (a.tokens) a.tokens[rowi] = -1;
             report_status(a.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
         }
-        cluster_sync();  // tmax has been read everywhere
-        return;
-    }
-    RowScale rs;
-    rs.lmax = mx;
-    if (mx == INFINITY) {  // the +inf logits share the weight
-        row.inf = true;
-        rs.lmax = 0.f;
-        if (kResident)
-            for (int x = tid; x < row.n; x += kThreads)
-                slice[x] = slice[x] == INFINITY ? 0.f : -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) tm[c] = tm[c] == INFINITY ? 0.f : -INFINITY;
-        lowest = 0.f;
-        __syncthreads();
-    }
-    {
-        // temperatures below 1e-30 act as 1e-30 (greedy rows weigh every kept
-        // logit alike: only one is kept)
-        // log2(e) / T as two floats by a corrected fp32 division (a double one
-        // costs every thread of the CTA some twenty fp64 instructions, which
-        // this GPU runs at 1/64 of the fp32 rate)
-        constexpr float kL2e = 1.44269502162933349609375f, kL2el = 1.925963033500011e-08f;
-        const float t = fmaxf(greedy ? 1.f : temp, 1e-30f);
-        rs.ch = __fdiv_rn(kL2e, t);
-        const float rest = fmaf(-rs.ch, t, kL2e) + kL2el;
-        rs.cl = __fdiv_rn(rest, t);
-    }
-    const float u = a.tokens ? a.u[rowi] : 0.f;
-    // floor(u * total), below total; u outside [0, 1) is clamped
-    auto draw_target = [&](uint64_t total) -> uint64_t {
-        return u > 0.f ? (u < 1.f ? scaled(u, total, false) : total - 1) : 0;
-    };
-    const int seg = ((row.n + kWarps - 1) / kWarps + 127) & ~127;
-    const int w0 = min(row.n, warp * seg), w1 = min(row.n, w0 + seg);
-
-    // ================================================= no filter
-    if (kResident && !filtered) {
-        uint64_t sum = prow ? sum_weights<true>(slice, w0, w1, rs, sm.tab, lane)
-                            : sum_weights<false>(slice, w0, w1, rs, sm.tab, lane);
-        sum = warp_sum64(sum);
-        if (lane == 0) sm.wsum[warp] = sum;
-        __syncthreads();
-        if (tid == 0) {
-            uint64_t t = 0;
-            for (int w = 0; w < kWarps; ++w) t += sm.wsum[w];
-            sm.x_sum = t;
-        }
-        cluster_sync();
-        uint64_t total = 0, before = 0;
-        for (uint32_t c = 0; c < ncta; ++c) {
-            const uint64_t t = *map_to_rank(&sm.x_sum, c);
-            if (c < rank) before += t;
-            total += t;
-        }
-        cluster_reads_done();
-        if (a.tokens) {
-            const int w = warp_of_target(sm, draw_target(total), before);
-            if (w >= 0) {  // the draw is in warp w's segment of this slice
-                // its weights again, from the input, four positions a thread
-                // (single weights round to units, so the last positive one
-                // takes a target past their sum)
-                const int x0 = w * seg, x1 = min(row.n, x0 + seg);
-                for (int base = x0; base < x1; base += 4 * kThreads) {
-                    const int x = base + 4 * tid;
-                    uint64_t q[4], s4 = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int e = x + k - row.pad;
-                        float v = x + k < x1 && e >= 0 && e < row.len
-                                      ? clean(L::wide(__ldg(gs + e)))
-                                      : -INFINITY;
-                        if (row.inf) v = v == INFINITY ? 0.f : -INFINITY;
-                        float wf;
-                        q[k] = weight(v, rs, sm.tab, wf);
-                        s4 += q[k];
-                    }
-                    draw_in_block(sm, draw_target(total), before, q, s4, e0 + x - row.pad,
-                                  a.tokens + rowi);
-                }
-            }
-        }
-        if (prow) {
-            const float inv = inverse(total);
-            float *out = prow - row.pad;
-            if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
-                for (int x = w0 + 4 * lane; x < w1; x += 128) {
-                    const float4 v = *reinterpret_cast<const float4 *>(slice + x);
-                    if (x >= row.pad && x + 4 <= row.pad + row.len) {
-                        __stcs(reinterpret_cast<float4 *>(out + x),
-                               make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-                    } else {
-                        const float e[4] = {v.x, v.y, v.z, v.w};
-                        for (int k = 0; k < 4; ++k)
-                            if (x + k >= row.pad && x + k < row.pad + row.len)
-                                out[x + k] = e[k] * inv;
-                    }
-                }
-            } else {
-                __syncwarp();
-                for (int x = w0 + lane; x < w1; x += 32)
-                    if (x >= row.pad && x < row.pad + row.len) out[x] = slice[x] * inv;
-            }
-        }
         cluster_wait_reads();
         return;
     }
+    if (mx == INFINITY) {
+        row.inf = true;
+        mx = lowest = 0.f;
+#pragma unroll
+        for (int u = 0; u < kParts; ++u) tm[u] = if_inf(tm[u]);
+    }
+    const RowScale rs = row_scale(mx, temp == 0.f ? 1.f : temp);
+    float wmax_f;
+    const uint64_t wmax = weight(mx, rs, sm.tab, wmax_f);
+    const float u01 = a.tokens ? a.u[rowi] : 0.f;
+    const uint64_t wmin = use_m ? (min_p >= 1.f ? wmax : scaled(min_p, wmax, true)) : 0;
+    const uint64_t want_k = one ? 1u : (uint64_t)top_k;
+
+    // ================================================= the row's weight
+    uint64_t all_sum = 0;  // (top-p without top-k)
+    if (use_p && !use_k) {
+        const uint64_t mine = rs.wide ? sum_stream<T, true>(row, sp, rs, sm.tab)
+                                      : sum_stream<T, false>(row, sp, rs, sm.tab);
+        const uint64_t t = warp_sum64(mine);
+        if (lane == 0) sm.scan[warp] = t;
+        __syncthreads();
+        if (tid == 0) {
+            uint64_t v = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += sm.scan[w];
+            sm.x_all = v;
+        }
+        cluster_sync();
+        uint64_t x[kMaxCluster];
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) x[c] = c < ncta ? *map_to_rank(&sm.x_all, c) : 0;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) all_sum += x[c];
+    }
 
     // ================================================= filters, by a sorted list
-    const uint64_t wmin =
-        use_m ? (min_p >= 1.f ? 1ull << kUnitLog2 : scaled(min_p, 1ull << kUnitLog2, true)) : 0;
-    const uint64_t want_k = one ? 1u : (uint64_t)top_k;
-    uint64_t all_sum = 0;        // the row's weight (top-p without top-k)
-    float pivot_k = -INFINITY;   // at least want_k logits are at or above it
-    if (kResident && filtered) {
-        if (use_p && !use_k) {
-            uint64_t sum = warp_sum64(
-                sum_weights<false>(slice, w0, w1, rs, sm.tab, lane));
-            if (lane == 0) sm.wsum[warp] = sum;
-            __syncthreads();
-            if (tid == 0) {
-                uint64_t t = 0;
-                for (int w = 0; w < kWarps; ++w) t += sm.wsum[w];
-                sm.x_all = t;
-            }
-            cluster_sync();
-            for (uint32_t c = 0; c < ncta; ++c) all_sum += *map_to_rank(&sm.x_all, c);
-        }
+    float pivot_k = -INFINITY;  // at least want_k logits are at or above it
+    if (use_k || use_p || use_m) {
         // ---- pivot: nothing below it is kept
         float pivot = -INFINITY;
         bool list = true;
@@ -917,48 +1165,60 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
             pivot = rs.lmax + t * (t < 0.f ? 1.0001f : 1.f) - 1e-4f * fabsf(rs.lmax) - 1e-5f;
         }
         if ((use_k || use_p) && a.V > kListMax) {
-            // A histogram of the threads' maxima over equal parts of [lowest,
-            // lmax], from the top: the pivot is the lower end of the first bin
-            // where want_k maxima are reached (want_k logits at least are then
-            // at or above it), or where their weights -- taken at the bin's
-            // middle, an estimate the exact cut checks -- reach top-p's goal.
-            // A bin that goes far past want_k is cut again.
-            uint32_t *cnt = sm.hist[0].cnt;
+            // A histogram of the part maxima over equal bins of [lowest, lmax],
+            // from the top: the pivot is the lower end of the first bin where
+            // want_k maxima are reached (want_k logits at least are then at or
+            // above it), or where their weights -- taken at the bin's middle, an
+            // estimate the exact cut checks -- reach top-p's goal.  A bin that
+            // goes far past want_k is cut again.
             float lo = lowest, hi = rs.lmax;
             uint32_t above = 0;  // maxima above hi
             const uint32_t need = (uint32_t)min(want_k, (uint64_t)1 << 20);
-            const float goal = 1.002f * fminf(top_p, 1.f) * (float)all_sum;
+            const float goal =
+                1.002f * fminf(top_p, 1.f) * (float)all_sum * (524288.f / kUnits);
             for (int level = 0; level < 3; ++level) {
                 const float scale = hi > lo ? (float)kBins / (hi - lo) : 0.f;
-                cnt[tid] = 0;
+                sm.parts[tid] = 0;
                 if (tid == 0) sm.bin = -1;
                 __syncthreads();
 #pragma unroll
-                for (int c = 0; c < kMaxCluster; ++c)
-                    if (tm[c] >= lo && tm[c] <= hi)
-                        atomicAdd(cnt + min(kBins - 1, (int)((hi - tm[c]) * scale)), 1u);
-                __syncthreads();
-                const uint32_t n = cnt[tid];
-                // counts in the low half, weights (units of 2^-19 of the largest
-                // and maximum, 2^31 at most together) in the high half
+                for (int u = 0; u < kParts; ++u)
+                    if (tm[u] >= lo && tm[u] <= hi)
+                        atomicAdd(sm.parts + min(kBins - 1, (int)((hi - tm[u]) * scale)), 1u);
+                uint32_t n = 0;
+                if (ncta > 1) {
+                    cluster_sync();
+                    uint32_t x[kMaxCluster];
+#pragma unroll
+                    for (int c = 0; c < kMaxCluster; ++c)
+                        x[c] = c < ncta ? map_to_rank(sm.parts, c)[tid] : 0;
+#pragma unroll
+                    for (int c = 0; c < kMaxCluster; ++c) n += x[c];
+                } else {
+                    __syncthreads();
+                    n = sm.parts[tid];
+                }
+                // counts in the low half, weights (units of 2^-19 of the scale,
+                // 2^15 part maxima at most) in the high half
                 uint64_t v = n;
                 if (!use_k && n) {
                     float wf;
                     weight(hi - ((float)tid + 0.5f) * (hi - lo) * (1.f / kBins), rs, sm.tab, wf);
-                    v += (uint64_t)((float)n * wf * 524288.f) << 32;
+                    v += (uint64_t)((float)n * wf * 65536.f) << 32;
                 }
-                const uint64_t inc = block_scan64(v, sm);
+                const uint64_t inc = block_scan64<kWarps>(v, sm.scan);
                 const uint32_t upto = above + (uint32_t)inc;
+                const float g16 = goal * 0.125f;
                 const bool in = use_k ? upto >= need && upto - n < need
-                                      : (float)(inc >> 32) >= goal * (524288.f / kUnits) &&
-                                            (float)((inc - v) >> 32) <
-                                                goal * (524288.f / kUnits);
+                                      : (float)(inc >> 32) >= g16 &&
+                                            (float)((inc - v) >> 32) < g16;
                 if (in) {
                     sm.bin = tid;
                     sm.bin_c = upto;
                     sm.bin_dc = n;
                 }
-                __syncthreads();
+                if (ncta > 1) cluster_sync();  // (parts have been read everywhere)
+                else __syncthreads();
                 const int bin = sm.bin;
                 if (bin < 0) {  // too few maxima (a later level: the last pivot stands)
                     if (level == 0) lo = -INFINITY;
@@ -981,22 +1241,47 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
             if (use_k) pivot_k = lo;
             if (lo > -INFINITY) pivot = fmaxf(pivot, lo);
             else list = by_m;
-            __syncthreads();  // the counters make way for the list
         }
-        // ---- candidates of the slice
+        // ---- candidates of the slice: the parts that reach the pivot, then their
+        // logits, a warp a part
         if (list) {
-            for (int x = 4 * tid; x < row.n; x += 4 * kThreads) {
-                const float4 v = *reinterpret_cast<const float4 *>(slice + x);
-                if (max3f(fmaxf(v.x, v.y), v.z, v.w) < pivot) continue;
-                const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (e[k] < pivot || e[k] == -INFINITY) continue;
-                    const int at = atomicAdd(&sm.n_list, 1);
-                    if (at < kListMax)
-                        sm.list.own[at] = (uint64_t)~float_key(e[k]) << 32 |
-                                          (uint32_t)(e0 + x + k - row.pad);
+            for (int u = 0; u < kParts; ++u) {
+                if (tm[u] < pivot || tm[u] == -INFINITY) continue;
+                const int at = atomicAdd(&sm.n_hit, 1);
+                if (at < kListMax) sm.hit[at] = (uint32_t)(tid * kParts + u);
+            }
+            __syncthreads();
+            const int hits = sm.n_hit;
+            auto offer = [&](float v, int x) {
+                if (row.inf) v = if_inf(v);
+                if (v < pivot || v == -INFINITY) return;
+                const int at = atomicAdd(&sm.n_list, 1);
+                if (at < kListMax)
+                    sm.list.own[at] = (uint64_t)~float_key(v) << 32 | (uint32_t)(e0 + x);
+            };
+            if (hits <= kListMax) {
+                for (int h = warp; h < hits; h += kWarps) {
+                    const int owner = (int)(sm.hit[h] / kParts), part = (int)(sm.hit[h] % kParts);
+                    // element e of the part: vector owner + kThreads (part + kParts j)
+                    for (int e = lane;; e += 32) {
+                        const int j = e / kVec, x = owner + kThreads * (part + kParts * j);
+                        if (x < sp.nvec) {
+                            const int at = sp.head + x * kVec + e % kVec;
+                            offer(clean(L::wide(__ldg(row.g + at))), at);
+                        }
+                        if (owner + kThreads * (part + kParts * ((e - lane + 32) / kVec)) >=
+                            sp.nvec)
+                            break;
+                    }
+                    if (part == 0 && lane == 0) {
+                        if (owner < sp.head) offer(clean(L::wide(__ldg(row.g + owner))), owner);
+                        if (owner < row.n - sp.tail)
+                            offer(clean(L::wide(__ldg(row.g + sp.tail + owner))), sp.tail + owner);
+                    }
                 }
+            } else if (tid == 0) {
+                sm.n_list = kListMax + 1;
             }
         }
         cluster_sync();
@@ -1005,7 +1290,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
             // the CTAs' counts, one a lane, then every entry of every list at once:
             // a remote read takes most of a microsecond
             const int m = lane < (int)ncta ? *map_to_rank(&sm.n_list, lane) : 0;
-            int ends = m;
+            int ends = min(m, kListMax + 1);
 #pragma unroll
             for (int o = 1; o < kMaxCluster; o <<= 1) {
                 const int t = __shfl_up_sync(kAll, ends, o);
@@ -1035,15 +1320,16 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
             __syncthreads();
             uint64_t *keys = sort_list(sm.list.a, sm.list.b, n);
             uint64_t *cum = keys == sm.list.a ? sm.list.b : sm.list.a;
-            for (int x = tid; x < n; x += kThreads) {
-                float wf;
-                cum[x] = weight(key_float(~(uint32_t)(keys[x] >> 32)), rs, sm.tab, wf);
-            }
-            __syncthreads();
             // (min-p: weights fall with the rank, so the first n_m pass)
             int nm = 0;
-            for (int x = tid; x < n; x += kThreads) nm += cum[x] >= wmin;
-            scan_list(cum, n, sm);
+            for (int x = tid; x < n; x += kThreads) {
+                float wf;
+                const uint64_t w = weight(key_float(~(uint32_t)(keys[x] >> 32)), rs, sm.tab, wf);
+                cum[x] = w;
+                nm += w >= wmin;
+            }
+            __syncthreads();
+            scan_list(cum, n, sm.scan);
             int nk = n;
             if (use_k) nk = (int)min((uint64_t)n, want_k);
             int keep = nk;
@@ -1056,43 +1342,35 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
                 int below = 0;
                 for (int x = tid; x < nk; x += kThreads) below += cum[x] < goal;
                 below = __reduce_add_sync(kAll, below);
-                if (lane == 0) atomicAdd(&sm.n_below, below);
-                __syncthreads();
-                keep = min(keep, sm.n_below + 1);
-                if (!use_k && !use_m && sm.n_below == n) list = false;  // short of the goal
+                if (lane == 0 && below) atomicAdd(&sm.n_below, below);
             }
             if (use_m) {
                 nm = __reduce_add_sync(kAll, nm);
-                if (lane == 0) atomicAdd(&sm.n_min, nm);
+                if (lane == 0 && nm) atomicAdd(&sm.n_min, nm);
+            }
+            if (use_p || use_m) {
                 __syncthreads();
-                keep = min(keep, sm.n_min);
+                if (use_p) keep = min(keep, sm.n_below + 1);
+                if (use_m) keep = min(keep, sm.n_min);
+                if (use_p && !use_k && !use_m && sm.n_below == n) list = false;  // short
             }
             keep = max(keep, 1);
             if (list) {
                 const uint64_t total = cum[keep - 1];
-                const float inv = inverse(total);
                 if (prow) {
-                    // zeros, then the kept ones of this slice
-                    const int off = (int)(reinterpret_cast<uintptr_t>(prow) & 15) / 4;
-                    const int lead = min(row.len, (4 - off) & 3);
-                    const int quads = (row.len - lead) / 4;
-                    if (tid < lead) prow[tid] = 0.f;
-                    for (int x = tid; x < quads; x += kThreads)
-                        __stcs(reinterpret_cast<float4 *>(prow + lead) + x,
-                               make_float4(0.f, 0.f, 0.f, 0.f));
-                    if (tid < row.len - lead - 4 * quads) prow[lead + 4 * quads + tid] = 0.f;
-                    __syncthreads();
+                    // the kept ones of this slice (over the zeros of the first pass)
+                    const float inv = inverse(total);
                     for (int x = tid; x < keep; x += kThreads) {
                         const uint64_t sv = keys[x];
                         const int e = (int)(uint32_t)sv - e0;
-                        if (e < 0 || e >= row.len) continue;
+                        if (e < 0 || e >= row.n) continue;
                         float wf;
                         weight(key_float(~(uint32_t)(sv >> 32)), rs, sm.tab, wf);
                         prow[e] = wf * inv;
                     }
                 }
                 if (a.tokens && rank == 0) {
-                    const uint64_t target = draw_target(total);
+                    const uint64_t target = draw_target(u01, total);
                     auto own = [&](int x) { return cum[x] - (x ? cum[x - 1] : 0); };
                     if (keep <= kThreads) {
                         // each kept one adds up the weights of indices up to its own
@@ -1119,7 +1397,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
                             const int x = 2 * tid + k;
                             w[k] = x < keep ? own((int)(uint32_t)keys[x]) : 0;
                         }
-                        const uint64_t t = block_scan64(w[0] + w[1], sm);
+                        const uint64_t t = block_scan64<kWarps>(w[0] + w[1], sm.scan);
                         const uint64_t t0 = t - w[1];
                         if (t0 > target && t0 - w[0] <= target)
                             a.tokens[rowi] = (int)(keys[2 * tid] >> 32);
@@ -1136,6 +1414,8 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
     }
 
     // ================================================= any row, by selection
+    const int seg = ((row.n + kWarps - 1) / kWarps + 31) & ~31;
+    const int w0 = min(row.n, warp * seg), w1 = min(row.n, w0 + seg);
     Cut cut{0, ~0ull};       // everything
     uint64_t key_count = 0;  // elements with the cut's key
     if (use_k || use_p) {
@@ -1148,7 +1428,8 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
         if (pivot_k > -INFINITY) {
             kmin = R::key(pivot_k);
         } else if (!use_k && all_sum > 0 && top_p < 0.9999f) {
-            const float share = (1.f - fmaxf(top_p, 0.f)) * (float)all_sum / kUnits / (float)a.V;
+            const float share = (1.f - fmaxf(top_p, 0.f)) * (float)all_sum /
+                                (kUnits * (float)a.V * wmax_f);
             const float l = rs.lmax + (__logf(share) - 0.01f) / (rs.ch * 0.693147181f) -
                             1e-4f * fabsf(rs.lmax) - 1e-5f;
             if (l > -INFINITY && share > 0.f) kmin = min(kmax, R::key(l));
@@ -1258,24 +1539,12 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
         sum += kept(x, wf, tie_end);
     });
     sum = warp_sum64(sum);
-    if (lane == 0) sm.wsum[warp] = sum;
-    __syncthreads();
-    if (tid == 0) {
-        uint64_t t = 0;
-        for (int w = 0; w < kWarps; ++w) t += sm.wsum[w];
-        sm.x_sum = t;
-    }
-    cluster_sync();
-    uint64_t total = 0, before = 0;
-    for (uint32_t c = 0; c < ncta; ++c) {
-        const uint64_t t = *map_to_rank(&sm.x_sum, c);
-        if (c < rank) before += t;
-        total += t;
-    }
-    cluster_reads_done();  // (of x_sum)
+    uint64_t total, before;
+    share_sums(sm.draw, sum, ncta, rank, total, before);
+    cluster_reads_done();
     if (a.tokens) {
-        const uint64_t target = draw_target(total);
-        const int w = warp_of_target(sm, target, before);
+        const uint64_t target = draw_target(u01, total);
+        const int w = warp_of_target(sm.draw, target, before);
         if (w >= 0) {  // the draw is in warp w's segment of this slice
             // (that warp's ties end where it says)
             if (warp == w && lane == 0) sm.bin = tie_end;
@@ -1290,59 +1559,73 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const SampleA
                     q[k] = x + k < x1 ? kept(x + k, wf, ends) : 0;
                     s4 += q[k];
                 }
-                draw_in_block(sm, target, before, q, s4, e0 + x - row.pad, a.tokens + rowi);
+                draw_in_block(sm.draw, target, before, q, s4, e0 + x, a.tokens + rowi);
             }
         }
     }
-    if (prow) {
+    if (prow) {  // over the zeros of the first pass (tie_end is the segment's)
         const float inv = inverse(total);
-        // (tie_end is the segment's)
-        for (int x = w0 + lane; x < w1; x += 32)
-            if (x >= row.pad && x < row.pad + row.len) prow[x - row.pad] = 0.f;
-        __syncwarp();
         for_selected(row, w0, w1, lane, in_cut, [&](int x) {
             float wf;
             kept(x, wf, tie_end);
-            if (x >= row.pad && x < row.pad + row.len) prow[x - row.pad] = wf * inv;
+            prow[x] = wf * inv;
         });
     }
     cluster_wait_reads();
 }
 
-template <typename T>
-int launch_typed(const SampleArgs &in, int num_sms, cudaStream_t stream) {
-    SampleArgs a = in;
-    constexpr long kMaxSlice = 80 * 1024;  // bytes: two CTAs an SM
-    const long bytes = (long)a.V * 4;      // as fp32
-    // CTAs a row: enough that two slices fit an SM, and more while they still
-    // spread the rows over the GPU (a slice of at least 4096 logits)
-    const long rows = (long)a.bs * a.B;
-    int ncta = 1;
-    while (ncta < kMaxCluster &&
-           (bytes > kMaxSlice * ncta || (rows * ncta <= num_sms && a.V / (2 * ncta) >= 4096)))
-        ncta *= 2;
-    a.ncta = ncta;
-    a.slice = (int)((((long)a.V + ncta - 1) / ncta + 31) & ~31L);
-    // pad in front (up to 7 logits) and up to a multiple of 128 behind
-    const size_t smem = ((size_t)a.slice + 7 + 127) / 128 * 512;
-    const bool resident = smem <= 190 * 1024;
-    auto kernel = resident ? token_sample_kernel<T, true> : token_sample_kernel<T, false>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             resident ? (int)smem : 0) != cudaSuccess)
+template <typename K>
+int launch_cluster(K *kernel, const SampleArgs &a, int threads, size_t smem, cudaStream_t stream) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+        cudaSuccess)
         return BDSA_CUDA_ERROR;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * ncta));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = resident ? smem : 0;
+    cfg.gridDim = dim3((unsigned)((long)a.bs * a.B * a.ncta));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ncta;
+    attr[0].val.clusterDim.x = (unsigned)a.ncta;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? BDSA_OK : BDSA_CUDA_ERROR;
+}
+
+template <typename T>
+int launch_typed(const SampleArgs &in, int num_sms, cudaStream_t stream) {
+    SampleArgs a = in;
+    const long rows = (long)a.bs * a.B;
+    auto set_slices = [&](int ncta) {
+        a.ncta = ncta;
+        a.slice = (int)((((long)a.V + ncta - 1) / ncta + 31) & ~31L);
+    };
+    if (!a.top_k && !a.top_p && !a.min_p) {
+        // CTAs a row: enough that two slices (as fp32) fit an SM, and more while
+        // they still spread the rows over the GPU (a slice of at least 4096)
+        constexpr long kMaxSlice = 104 * 1024;
+        const long bytes = (long)a.V * 4;
+        int ncta = 1;
+        while (ncta < kMaxCluster &&
+               (bytes > kMaxSlice * ncta || (rows * ncta <= num_sms && a.V / (2 * ncta) >= 4096)))
+            ncta *= 2;
+        set_slices(ncta);
+        // pad in front (up to 7 logits) and up to a multiple of 256 behind
+        const size_t smem = ((size_t)a.slice + 7 + 255) / 256 * 1024;
+        if (smem <= 190 * 1024)
+            return launch_cluster(sample_full_kernel<T>, a, kFullThreads, smem, stream);
+    }
+    // one CTA a row when the rows alone fill the GPU twice over; else slices of at
+    // least 4096
+    int ncta = 1;
+    while (ncta < kMaxCluster &&
+           ((rows * ncta * 2 <= 2 * num_sms && a.V / (2 * ncta) >= 4096) ||
+            a.V > ncta * (1 << 18)))
+        ncta *= 2;
+    set_slices(ncta);
+    return launch_cluster(sample_cut_kernel<T>, a, kThreads, 0, stream);
 }
 
 }  // namespace
