@@ -443,47 +443,44 @@ __device__ __forceinline__ float inverse(uint64_t total) {
 __device__ __forceinline__ float if_inf(float v) { return v == INFINITY ? 0.f : -INFINITY; }
 
 // ============================================================ sample_full
-// The weights of positions [x0, x1) of a resident slice (multiples of 256) and
-// their sum, one warp, eight positions a lane and step; kStore: the weights
+// The weights of positions [x0, x1) of a resident slice (multiples of 128) and
+// their sum, one warp, four positions a lane and step; kStore: the weights
 // replace the logits.  Returns the lane's sum in units.  A running sum stays below
-// 64 (a slice of at most 48640 positions gives a lane's each at most 24 weights),
-// so one that starts at 64 makes every addition a Fast2Sum, with remainders
-// below 2^-18 whose own sum rounds at 2^-40.
+// 64 (a slice of at most 48640 positions gives each of a lane's four at most 48
+// weights), so one that starts at 64 makes every addition a Fast2Sum, with
+// remainders below 2^-18 whose own sum rounds at 2^-40.
 template <bool kStore, bool kWide>
 __device__ __forceinline__ uint64_t sum_slice(float *s, int x0, int x1, const RowScale &rs,
                                               const ExpTable &tab, int lane) {
     constexpr float kBase = 64.f;
     const V2 neg = splat<V2>(-1.f);
-    V2 acc[4], low[4];
+    V2 acc[2], low[2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
         acc[k] = splat<V2>(kBase);
         low[k] = splat<V2>(0.f);
     }
-    for (int x = x0 + 4 * lane; x < x1; x += 256) {
-        float4 v[2] = {*reinterpret_cast<const float4 *>(s + x),
-                       *reinterpret_cast<const float4 *>(s + x + 128)};
-        float *f = reinterpret_cast<float *>(v);
+#pragma unroll 2
+    for (int x = x0 + 4 * lane; x < x1; x += 128) {
+        const float4 v = *reinterpret_cast<const float4 *>(s + x);
+        V2 h[2], l[2];
+        weight_ff<V2, kWide>(V2{f2_pack(v.x, v.y)}, rs, tab, h[0], l[0]);
+        weight_ff<V2, kWide>(V2{f2_pack(v.z, v.w)}, rs, tab, h[1], l[1]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            V2 h, l;
-            weight_ff<V2, kWide>(V2{f2_pack(f[2 * k], f[2 * k + 1])}, rs, tab, h, l);
-            const V2 t = acc[k] + h;
-            const V2 err = vfma(vfma(acc[k], neg, t), neg, h);  // h - (t - acc)
+        for (int k = 0; k < 2; ++k) {
+            const V2 t = acc[k] + h[k];
+            const V2 err = vfma(vfma(acc[k], neg, t), neg, h[k]);  // h - (t - acc)
             acc[k] = t;
-            low[k] = low[k] + (err + l);
-            const float2 w = f2_unpack(h.a);
-            f[2 * k] = w.x;
-            f[2 * k + 1] = w.y;
+            low[k] = low[k] + (err + l[k]);
         }
         if (kStore) {
-            *reinterpret_cast<float4 *>(s + x) = v[0];
-            *reinterpret_cast<float4 *>(s + x + 128) = v[1];
+            const float2 a = f2_unpack(h[0].a), b = f2_unpack(h[1].a);
+            *reinterpret_cast<float4 *>(s + x) = make_float4(a.x, a.y, b.x, b.y);
         }
     }
     long long sum = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
         const float2 a = f2_unpack(acc[k].a), b = f2_unpack(low[k].a);
         sum += __float2ll_rn((a.x - kBase) * kUnits) + __float2ll_rn((a.y - kBase) * kUnits) +
                __float2ll_rn(b.x * kUnits) + __float2ll_rn(b.y * kUnits);
@@ -514,9 +511,9 @@ __global__ void __launch_bounds__(kFullThreads, 2) sample_full_kernel(const Samp
     const Raw *gs = static_cast<const Raw *>(a.logits) + r * a.lsr + i * a.lsi + e0;
     constexpr int kVec = 16 / (int)sizeof(Raw);
     // positions x = index - e0 + pad: the slice keeps its offset from a 16-byte
-    // boundary; -inf in front and behind, up to a multiple of 256
+    // boundary; -inf in front and behind, up to a multiple of 128
     const int pad = (int)((reinterpret_cast<uintptr_t>(gs) & 15) / sizeof(Raw));
-    const int n = (len + pad + 255) & ~255;
+    const int n = (len + pad + 127) & ~127;
     const float temp = a.temperature ? a.temperature[r] : 1.f;
     const bool bad_temp = !(temp >= 0.f) || temp == INFINITY;
     float *prow = a.probs ? a.probs + r * a.psr + i * a.psi + e0 : nullptr;
@@ -569,9 +566,9 @@ __global__ void __launch_bounds__(kFullThreads, 2) sample_full_kernel(const Samp
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
     if (lane == 0) sm.red[warp] = mx;
     __syncthreads();
-    mx = sm.red[lane % kFullWarps];
+    mx = lane < kFullWarps ? sm.red[lane] : -INFINITY;
 #pragma unroll
-    for (int o = kFullWarps / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
     if (tid == 0) sm.x_max = mx;
     cluster_sync();
 #pragma unroll
@@ -613,7 +610,7 @@ __global__ void __launch_bounds__(kFullThreads, 2) sample_full_kernel(const Samp
         __syncthreads();
     }
     const RowScale rs = row_scale(mx, temp);
-    const int seg = ((n + kFullWarps - 1) / kFullWarps + 255) & ~255;
+    const int seg = ((n + kFullWarps - 1) / kFullWarps + 127) & ~127;
     const int w0 = min(n, warp * seg), w1 = min(n, w0 + seg);
     uint64_t sum;
     if (prow)
@@ -725,15 +722,19 @@ struct Level {
     uint64_t c, m, dc, dm;
 };
 
-// This CTA's slice, read from global memory (mostly L2: it has been streamed).
-template <typename T>
+// This CTA's slice: in shared memory (kRes), or read from global memory again
+// (mostly L2: it has been streamed).
+template <typename T, bool kRes>
 struct Row {
     using L = Logit<T>;
-    const typename L::Raw *g;
+    const typename L::Raw *g;  // in global memory
+    const typename L::Raw *s;  // kRes: the copy, as far from a 16-byte boundary
     int n;
     bool inf;  // the row's maximum is +inf
+    __device__ __forceinline__ typename L::Raw raw(int x) const { return kRes ? s[x] : __ldg(g + x); }
+    __device__ __forceinline__ uint4 vec(const uint4 *p) const { return kRes ? *p : __ldg(p); }
     __device__ __forceinline__ float at(int x) const {
-        const float v = clean(L::wide(__ldg(g + x)));
+        const float v = clean(L::wide(raw(x)));
         return inf ? if_inf(v) : v;
     }
     static __device__ __forceinline__ uint32_t key(float v) { return float_key(v) >> L::kKeyShift; }
@@ -755,6 +756,7 @@ __device__ __forceinline__ void for_selected(const R &row, int x0, int x1, int l
     for (int base = x0; base < x1; base += 1024) {
         uint32_t mask = 0;
         const int steps = min(32, (x1 - base + 31) / 32);
+#pragma unroll 8
         for (int j = 0; j < steps; ++j) {
             const int x = base + 32 * j + lane;
             if (x < x1 && pred(row.at(x), x)) mask |= 1u << j;
@@ -953,8 +955,8 @@ __device__ __forceinline__ Span span_of(const Raw *p, int len) {
 }
 
 // The weight of the slice in units, this thread's share (every thread of the CTA).
-template <typename T, bool kWide>
-__device__ __forceinline__ uint64_t sum_stream(const Row<T> &row, const Span &sp,
+template <typename T, bool kRes, bool kWide>
+__device__ __forceinline__ uint64_t sum_stream(const Row<T, kRes> &row, const Span &sp,
                                                const RowScale &rs, const ExpTable &tab) {
     using L = Logit<T>;
     using Raw = typename L::Raw;
@@ -975,15 +977,15 @@ __device__ __forceinline__ uint64_t sum_stream(const Row<T> &row, const Span &sp
         acc = t;
         low = low + (err + l);
     };
-    if (tid < sp.head) add(clean(L::wide(__ldg(row.g + tid))), -INFINITY);
-    if (tid < row.n - sp.tail) add(clean(L::wide(__ldg(row.g + sp.tail + tid))), -INFINITY);
-    const uint4 *gv = reinterpret_cast<const uint4 *>(row.g + sp.head);
-    constexpr int kU = 4;
+    if (tid < sp.head) add(clean(L::wide(row.raw(tid))), -INFINITY);
+    if (tid < row.n - sp.tail) add(clean(L::wide(row.raw(sp.tail + tid))), -INFINITY);
+    const uint4 *gv = reinterpret_cast<const uint4 *>((kRes ? row.s : row.g) + sp.head);
+    constexpr int kU = kRes ? 2 : 4;
     for (int x = tid; x < sp.nvec; x += kU * kThreads) {
         uint4 q[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u)
-            if (x + u * kThreads < sp.nvec) q[u] = __ldg(gv + x + u * kThreads);
+            if (x + u * kThreads < sp.nvec) q[u] = row.vec(gv + x + u * kThreads);
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             if (x + u * kThreads >= sp.nvec) break;
@@ -997,12 +999,13 @@ __device__ __forceinline__ uint64_t sum_stream(const Row<T> &row, const Span &sp
                       __float2ll_rn(b.x * kUnits) + __float2ll_rn(b.y * kUnits));
 }
 
-template <typename T>
+template <typename T, bool kRes>
 __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArgs a) {
-    using R = Row<T>;
+    using R = Row<T, kRes>;
     using L = Logit<T>;
     using Raw = typename L::Raw;
     constexpr int kVec = 16 / (int)sizeof(Raw);
+    extern __shared__ __align__(16) uint8_t s_dyn[];
     __shared__ CutShared sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ncta = (uint32_t)a.ncta, rank = ncta > 1 ? cluster_rank() : 0u;
@@ -1014,6 +1017,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
     row.g = static_cast<const Raw *>(a.logits) + r * a.lsr + i * a.lsi + e0;
     row.inf = false;
     const Span sp = span_of(row.g, row.n);
+    Raw *copy = reinterpret_cast<Raw *>(s_dyn) +
+                (reinterpret_cast<uintptr_t>(row.g) & 15) / sizeof(Raw);
+    row.s = copy;
     const uint4 *gv = reinterpret_cast<const uint4 *>(row.g + sp.head);
 
     // ---- this row's parameters
@@ -1056,14 +1062,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
 #pragma unroll
             for (int u = 0; u < kParts; ++u) {
                 if (x + u * kThreads >= sp.nvec) break;
+                if (kRes) reinterpret_cast<uint4 *>(copy + sp.head)[x + u * kThreads] = q[u];
                 const Raw *e = reinterpret_cast<const Raw *>(&q[u]);
 #pragma unroll
                 for (int k = 0; k < kVec; k += 2)  // (max.f32 passes over NaN)
                     tm[u] = max3f(tm[u], L::wide(e[k]), L::wide(e[k + 1]));
             }
         }
-        if (tid < sp.head) tm[0] = fmaxf(tm[0], L::wide(__ldg(row.g + tid)));
-        if (tid < row.n - sp.tail) tm[0] = fmaxf(tm[0], L::wide(__ldg(row.g + sp.tail + tid)));
+        auto ragged = [&](int x) {
+            const Raw v = __ldg(row.g + x);
+            if (kRes) copy[x] = v;
+            tm[0] = fmaxf(tm[0], L::wide(v));
+        };
+        if (tid < sp.head) ragged(tid);
+        if (tid < row.n - sp.tail) ragged(sp.tail + tid);
         if (prow) {  // what the loop above did not reach
             const int steps = (sp.nvec + kParts * kThreads - 1) / (kParts * kThreads);
             for (int z = steps * kParts * kThreads * kZ + tid; z < zeros; z += kThreads)
@@ -1132,8 +1144,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
     // ================================================= the row's weight
     uint64_t all_sum = 0;  // (top-p without top-k)
     if (use_p && !use_k) {
-        const uint64_t mine = rs.wide ? sum_stream<T, true>(row, sp, rs, sm.tab)
-                                      : sum_stream<T, false>(row, sp, rs, sm.tab);
+        const uint64_t mine = rs.wide ? sum_stream<T, kRes, true>(row, sp, rs, sm.tab)
+                                      : sum_stream<T, kRes, false>(row, sp, rs, sm.tab);
         const uint64_t t = warp_sum64(mine);
         if (lane == 0) sm.scan[warp] = t;
         __syncthreads();
@@ -1164,7 +1176,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
             const float t = __logf(fminf(min_p, 1.f)) / (rs.ch * 0.693147181f);
             pivot = rs.lmax + t * (t < 0.f ? 1.0001f : 1.f) - 1e-4f * fabsf(rs.lmax) - 1e-5f;
         }
-        if ((use_k || use_p) && a.V > kListMax) {
+        if ((use_k || use_p) && a.V > kListMax / 4) {
             // A histogram of the part maxima over equal bins of [lowest, lmax],
             // from the top: the pivot is the lower end of the first bin where
             // want_k maxima are reached (want_k logits at least are then at or
@@ -1240,7 +1252,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
             }
             if (use_k) pivot_k = lo;
             if (lo > -INFINITY) pivot = fmaxf(pivot, lo);
-            else list = by_m;
+            else list = by_m || a.V <= kListMax;
+            // (every maximum at or above the pivot brings a candidate at least)
+            if (lo > -INFINITY && (uint32_t)sm.bin_c > kListMax && !by_m) list = false;
         }
         // ---- candidates of the slice: the parts that reach the pivot, then their
         // logits, a warp a part
@@ -1268,16 +1282,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
                         const int j = e / kVec, x = owner + kThreads * (part + kParts * j);
                         if (x < sp.nvec) {
                             const int at = sp.head + x * kVec + e % kVec;
-                            offer(clean(L::wide(__ldg(row.g + at))), at);
+                            offer(clean(L::wide(row.raw(at))), at);
                         }
                         if (owner + kThreads * (part + kParts * ((e - lane + 32) / kVec)) >=
                             sp.nvec)
                             break;
                     }
                     if (part == 0 && lane == 0) {
-                        if (owner < sp.head) offer(clean(L::wide(__ldg(row.g + owner))), owner);
+                        if (owner < sp.head) offer(clean(L::wide(row.raw(owner))), owner);
                         if (owner < row.n - sp.tail)
-                            offer(clean(L::wide(__ldg(row.g + sp.tail + owner))), sp.tail + owner);
+                            offer(clean(L::wide(row.raw(sp.tail + owner))), sp.tail + owner);
                     }
                 }
             } else if (tid == 0) {
@@ -1612,8 +1626,8 @@ int launch_typed(const SampleArgs &in, int num_sms, cudaStream_t stream) {
                (bytes > kMaxSlice * ncta || (rows * ncta <= num_sms && a.V / (2 * ncta) >= 4096)))
             ncta *= 2;
         set_slices(ncta);
-        // pad in front (up to 7 logits) and up to a multiple of 256 behind
-        const size_t smem = ((size_t)a.slice + 7 + 255) / 256 * 1024;
+        // pad in front (up to 7 logits) and up to a multiple of 128 behind
+        const size_t smem = ((size_t)a.slice + 7 + 127) / 128 * 512;
         if (smem <= 190 * 1024)
             return launch_cluster(sample_full_kernel<T>, a, kFullThreads, smem, stream);
     }
@@ -1621,11 +1635,14 @@ int launch_typed(const SampleArgs &in, int num_sms, cudaStream_t stream) {
     // least 4096
     int ncta = 1;
     while (ncta < kMaxCluster &&
-           ((rows * ncta * 2 <= 2 * num_sms && a.V / (2 * ncta) >= 4096) ||
-            a.V > ncta * (1 << 18)))
+           ((rows * ncta <= num_sms && a.V / (2 * ncta) >= 4096) || a.V > ncta * (1 << 18)))
         ncta *= 2;
     set_slices(ncta);
-    return launch_cluster(sample_cut_kernel<T>, a, kThreads, 0, stream);
+    // slices two of which fit an SM stay there for the later passes
+    const size_t smem = (size_t)a.slice * sizeof(T) + 16;
+    if (smem <= 72 * 1024)
+        return launch_cluster(sample_cut_kernel<T, true>, a, kThreads, smem, stream);
+    return launch_cluster(sample_cut_kernel<T, false>, a, kThreads, 0, stream);
 }
 
 }  // namespace
