@@ -21,10 +21,10 @@
 //
 // Layout.  One thread-block cluster per row (of one CTA when there are rows
 // enough), its CTAs the vocabulary slices.  Two kernels:
-//   sample_full    no filter arrays, rows that fit: every slice resident in
-//                  shared memory as fp32, so the logits are read from HBM once;
-//                  one pass for the weights (kept in place of the logits) and
-//                  their sum, one that scales and stores them.
+//   sample_full    no filter arrays: one pass for the row's weight, each thread
+//                  against the largest logit it has met so far (a new one moves
+//                  its scale by a power of two, exactly), a second one, from L2,
+//                  for the distribution.
 //   sample_cut     filters: the row is streamed once for the maxima of some
 //                  thousand parts of it (and, with probs, zeros are stored); a
 //                  pivot below which nothing can be kept comes from those maxima
@@ -49,15 +49,12 @@
 namespace bdsa {
 namespace {
 
-constexpr int kThreads = 512;      // sample_cut
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kFullThreads = 256;  // sample_full: room for its constants as packed pairs
-constexpr int kFullWarps = kFullThreads / 32;
 constexpr int kBins = 512;         // one a thread of sample_cut
 constexpr int kParts = 8;          // parts of a thread's share of a slice, a maximum each
 constexpr int kMaxCluster = 8;
 constexpr int kListMax = 1024;  // candidates the sorted list holds
-constexpr int kUnitLog2 = 41;  // a weight's unit is 2^-41 of the row's largest
 constexpr uint32_t kAll = 0xffffffffu;
 
 // ------------------------------------------------------------ 2^(j / 16)
@@ -94,8 +91,14 @@ __device__ const ExpTable g_exp_table = make_exp_table();
 struct RowScale {
     float lmax, ch, cl;
     float ymin;        // weights with y <= ymin are zero (2^-124 of the scale)
+    int E;
     uint32_t ebits;    // (127 - E) << 23, modulo 2^32
     bool wide;
+    __device__ __forceinline__ void set_scale(int e) {
+        E = e;
+        ymin = (float)(e - 124);
+        ebits = (uint32_t)(127 - e) << 23;
+    }
 };
 __device__ __forceinline__ RowScale row_scale(float lmax, float temp) {
     // log2(e) / T as two floats by a corrected fp32 division (a double one costs
@@ -110,9 +113,7 @@ __device__ __forceinline__ RowScale row_scale(float lmax, float temp) {
     rs.cl = __fdiv_rn(rest, t);
     const float y = lmax * rs.ch;
     rs.wide = !(fabsf(y) < 131072.f);
-    const int E = rs.wide ? 0 : (int)floorf(y) + 1;
-    rs.ymin = (float)(E - 124);
-    rs.ebits = (uint32_t)(127 - E) << 23;
+    rs.set_scale(rs.wide ? 0 : (int)floorf(y) + 1);
     return rs;
 }
 
@@ -215,7 +216,8 @@ __device__ __forceinline__ void weight_ff(V l, const RowScale &rs, const ExpTabl
     keep_above(yh, rs.ymin, wh, wl);
 }
 
-constexpr float kUnits = 2199023255552.f;  // 2^kUnitLog2
+// A weight's unit is 2^-41 of the row's scale.
+constexpr float kUnits = 2199023255552.f;
 
 // The weight in units of 2^-41 of the scale and, in wf, as a float.
 __device__ __forceinline__ uint64_t weight(float l, const RowScale &rs, const ExpTable &tab,
@@ -331,8 +333,7 @@ __device__ __forceinline__ uint64_t warp_scan64(uint64_t v, int lane) {
 }
 
 // ------------------------------------------------------------ one CTA's sums
-// Inclusive prefix sums of v over a CTA of NW warps, in thread order.
-template <int NW>
+// Inclusive prefix sums of v over the CTA, in thread order.
 __device__ __forceinline__ uint64_t block_scan64(uint64_t v, uint64_t *scratch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t t = warp_scan64(v, lane);
@@ -340,30 +341,29 @@ __device__ __forceinline__ uint64_t block_scan64(uint64_t v, uint64_t *scratch) 
     __syncthreads();
     uint64_t before = 0;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) before += w < warp ? scratch[w] : 0;
+    for (int w = 0; w < kWarps; ++w) before += w < warp ? scratch[w] : 0;
     __syncthreads();
     return before + t;
 }
 
 // What the draw needs: the weight of each warp's contiguous segment of the slice,
 // and scratch.
-template <int NW>
 struct DrawShared {
-    uint64_t wsum[NW], scan[NW], step, x_sum;  // x_sum: the slice's weight, read by the cluster
+    uint64_t wsum[kWarps], scan[kWarps], step;
+    uint64_t x_sum;  // the slice's weight, read by the cluster
     int last;
 };
 
 // Sets sum (each warp's segment weight, in every lane) up for the draw: total is
 // the cluster's weight, before the weight in front of this slice.
-template <int NW>
-__device__ __forceinline__ void share_sums(DrawShared<NW> &d, uint64_t sum, uint32_t ncta,
+__device__ __forceinline__ void share_sums(DrawShared &d, uint64_t sum, uint32_t ncta,
                                            uint32_t rank, uint64_t &total, uint64_t &before) {
     if ((threadIdx.x & 31) == 0) d.wsum[threadIdx.x >> 5] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
         uint64_t t = 0;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) t += d.wsum[w];
+        for (int w = 0; w < kWarps; ++w) t += d.wsum[w];
         d.x_sum = t;
     }
     cluster_sync();
@@ -381,11 +381,10 @@ __device__ __forceinline__ void share_sums(DrawShared<NW> &d, uint64_t sum, uint
 // The warp whose segment of this slice holds the target, or -1; before (the
 // weight in front of the slice) becomes the weight in front of that segment.
 // Uniform over the CTA.
-template <int NW>
-__device__ __forceinline__ int warp_of_target(const DrawShared<NW> &d, uint64_t target,
+__device__ __forceinline__ int warp_of_target(const DrawShared &d, uint64_t target,
                                               uint64_t &before) {
     if (target < before) return -1;
-    for (int w = 0; w < NW; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         if (target < before + d.wsum[w]) return w;
         before += d.wsum[w];
     }
@@ -396,16 +395,15 @@ __device__ __forceinline__ int warp_of_target(const DrawShared<NW> &d, uint64_t 
 // four successive indices (their sum s4, the first at index idx) in thread
 // order; before grows by the step's weight.  The thread that reaches the target
 // writes its token; until then each step's last positive weight does.
-template <int NW>
-__device__ __forceinline__ void draw_in_block(DrawShared<NW> &d, uint64_t target,
+__device__ __forceinline__ void draw_in_block(DrawShared &d, uint64_t target,
                                               uint64_t &before, const uint64_t (&q)[4],
                                               uint64_t s4, int idx, int32_t *token) {
     if (before > target) return;  // (uniform)
     const int tid = threadIdx.x;
     if (tid == 0) d.last = -1;
-    const uint64_t inc = block_scan64<NW>(s4, d.scan);
+    const uint64_t inc = block_scan64(s4, d.scan);
     if (s4) atomicMax(&d.last, tid);
-    if (tid == NW * 32 - 1) d.step = inc;
+    if (tid == kThreads - 1) d.step = inc;
     __syncthreads();
     const uint64_t step = d.step;
     const bool hit = before + inc > target && before + inc - s4 <= target;
@@ -429,7 +427,7 @@ __device__ __forceinline__ uint64_t draw_target(float u, uint64_t total) {
     return u > 0.f ? (u < 1.f ? scaled(u, total, false) : total - 1) : 0;
 }
 
-// 2^kUnitLog2 / total, rounded once (to within 2^-46).
+// 2^41 / total, rounded once (to within 2^-46).
 __device__ __forceinline__ float inverse(uint64_t total) {
     const float hi = __ull2float_rz(total);  // hi <= total, both in units
     const float lo = __ull2float_rn(total - (uint64_t)hi);
@@ -442,142 +440,199 @@ __device__ __forceinline__ float inverse(uint64_t total) {
 // share the weight.
 __device__ __forceinline__ float if_inf(float v) { return v == INFINITY ? 0.f : -INFINITY; }
 
-// ============================================================ sample_full
-// The weights of positions [x0, x1) of a resident slice (multiples of 128) and
-// their sum, one warp, four positions a lane and step; kStore: the weights
-// replace the logits.  Returns the lane's sum in units.  A running sum stays below
-// 64 (a slice of at most 48640 positions gives each of a lane's four at most 48
-// weights), so one that starts at 64 makes every addition a Fast2Sum, with
-// remainders below 2^-18 whose own sum rounds at 2^-40.
-template <bool kStore, bool kWide>
-__device__ __forceinline__ uint64_t sum_slice(float *s, int x0, int x1, const RowScale &rs,
-                                              const ExpTable &tab, int lane) {
-    constexpr float kBase = 64.f;
-    const V2 neg = splat<V2>(-1.f);
-    V2 acc[2], low[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        acc[k] = splat<V2>(kBase);
-        low[k] = splat<V2>(0.f);
+// The running sum of one thread: weights of two packed lanes as 2^(y - E), floats
+// with their remainders, for the row scale `rs` (E in rs.ebits and rs.ymin).
+struct Running {
+    V2 acc, low;
+    __device__ __forceinline__ void clear() { acc = low = splat<V2>(0.f); }
+    __device__ __forceinline__ void add(V2 h, V2 l) {  // TwoSum
+        const V2 neg = splat<V2>(-1.f);
+        const V2 t = acc + h;
+        const V2 hh = vfma(acc, neg, t);
+        const V2 err = vfma(vfma(hh, neg, t), neg, acc) + vfma(hh, neg, h);
+        acc = t;
+        low = low + (err + l);
     }
-#pragma unroll 2
-    for (int x = x0 + 4 * lane; x < x1; x += 128) {
-        const float4 v = *reinterpret_cast<const float4 *>(s + x);
-        V2 h[2], l[2];
-        weight_ff<V2, kWide>(V2{f2_pack(v.x, v.y)}, rs, tab, h[0], l[0]);
-        weight_ff<V2, kWide>(V2{f2_pack(v.z, v.w)}, rs, tab, h[1], l[1]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const V2 t = acc[k] + h[k];
-            const V2 err = vfma(vfma(acc[k], neg, t), neg, h[k]);  // h - (t - acc)
-            acc[k] = t;
-            low[k] = low[k] + (err + l[k]);
-        }
-        if (kStore) {
-            const float2 a = f2_unpack(h[0].a), b = f2_unpack(h[1].a);
-            *reinterpret_cast<float4 *>(s + x) = make_float4(a.x, a.y, b.x, b.y);
-        }
+    // in units, of a scale 2^(to - from) as large
+    __device__ __forceinline__ uint64_t units(int from, int to) const {
+        const float2 a = f2_unpack(acc.a), b = f2_unpack(low.a);
+        if (to - from > 64) return 0;
+        const float f = kUnits * __int_as_float((127 + from - to) << 23);
+        const long long v = __float2ll_rn(a.x * f) + __float2ll_rn(a.y * f) +
+                            __float2ll_rn(b.x * f) + __float2ll_rn(b.y * f);
+        return (uint64_t)max(v, 0ll);
     }
-    long long sum = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const float2 a = f2_unpack(acc[k].a), b = f2_unpack(low[k].a);
-        sum += __float2ll_rn((a.x - kBase) * kUnits) + __float2ll_rn((a.y - kBase) * kUnits) +
-               __float2ll_rn(b.x * kUnits) + __float2ll_rn(b.y * kUnits);
-    }
-    return (uint64_t)max(sum, 0ll);
+};
+
+// How a slice splits into 16-byte vectors: element counts of the ragged ends.
+struct Span {
+    int head, nvec, tail;  // tail: the first element behind the vectors
+};
+template <typename Raw>
+__device__ __forceinline__ Span span_of(const Raw *p, int len) {
+    constexpr int kVec = 16 / (int)sizeof(Raw);
+    const int mis = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(Raw));
+    Span s;
+    s.head = min(len, mis ? kVec - mis : 0);
+    s.nvec = (len - s.head) / kVec;
+    s.tail = s.head + s.nvec * kVec;
+    return s;
 }
 
+// A warp's segment of a slice: vectors [v0, v1) of the slice's Span, and the
+// ragged ends (the head with the first warp, the tail with the last).  Segments
+// are in index order.
+struct Segment {
+    int v0, v1, head0, head1, tail0, tail1;  // elements [head0, head1), [tail0, tail1)
+};
+__device__ __forceinline__ Segment segment_of(const Span &sp, int len, int w) {
+    const int per = (sp.nvec + kWarps - 1) / kWarps;
+    Segment g;
+    g.v0 = min(sp.nvec, w * per);
+    g.v1 = min(sp.nvec, g.v0 + per);
+    g.head0 = 0;
+    g.head1 = w == 0 ? sp.head : 0;
+    g.tail0 = sp.tail;
+    g.tail1 = w == kWarps - 1 ? len : sp.tail;
+    return g;
+}
+
+// ============================================================ sample_full
 struct FullShared {
     ExpTable tab;
-    DrawShared<kFullWarps> draw;
-    float red[kFullWarps];
+    DrawShared draw;
+    float red[kWarps];
     float x_max;  // read by the cluster
     int x_first;  // greedy rows: the slice's first largest logit; read by the cluster
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kFullThreads, 2) sample_full_kernel(const SampleArgs a) {
+struct FullRow {
     using L = Logit<T>;
     using Raw = typename L::Raw;
-    extern __shared__ __align__(16) uint8_t s_dyn[];
+    static constexpr int kVec = 16 / (int)sizeof(Raw);
+    const Raw *g;
+    int len;
+    bool inf;
+    __device__ __forceinline__ float value(Raw r) const {
+        const float v = clean(L::wide(r));
+        return inf ? if_inf(v) : v;
+    }
+};
+
+// Weights and sum of a segment at a known scale, this lane's share in units (rows
+// of very small temperatures, and rows with +inf logits).
+template <typename T>
+__device__ __noinline__ uint64_t sum_segment(const FullRow<T> &row, const Span &sp,
+                                             const Segment &sg, const RowScale &rs,
+                                             const ExpTable &tab, int lane) {
+    uint64_t sum = 0;
+    float wf;
+    for (int x = sg.head0 + lane; x < sg.head1; x += 32)
+        sum += weight(row.value(__ldg(row.g + x)), rs, tab, wf);
+    for (int x = sp.head + sg.v0 * row.kVec + lane; x < sp.head + sg.v1 * row.kVec; x += 32)
+        sum += weight(row.value(__ldg(row.g + x)), rs, tab, wf);
+    for (int x = sg.tail0 + lane; x < sg.tail1; x += 32)
+        sum += weight(row.value(__ldg(row.g + x)), rs, tab, wf);
+    return sum;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) sample_full_kernel(const SampleArgs a) {
+    using L = Logit<T>;
+    using Raw = typename L::Raw;
+    constexpr int kVec = 16 / (int)sizeof(Raw);
     __shared__ FullShared sm;
-    float *slice = reinterpret_cast<float *>(s_dyn);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ncta = (uint32_t)a.ncta, rank = ncta > 1 ? cluster_rank() : 0u;
     const long rowi = blockIdx.x / ncta;
     const int r = (int)(rowi / a.B), i = (int)(rowi % a.B);
-    const int e0 = min(a.V, (int)rank * a.slice), len = min(a.V, e0 + a.slice) - e0;
-    const Raw *gs = static_cast<const Raw *>(a.logits) + r * a.lsr + i * a.lsi + e0;
-    constexpr int kVec = 16 / (int)sizeof(Raw);
-    // positions x = index - e0 + pad: the slice keeps its offset from a 16-byte
-    // boundary; -inf in front and behind, up to a multiple of 128
-    const int pad = (int)((reinterpret_cast<uintptr_t>(gs) & 15) / sizeof(Raw));
-    const int n = (len + pad + 127) & ~127;
+    const int e0 = min(a.V, (int)rank * a.slice);
+    FullRow<T> row;
+    row.len = min(a.V, e0 + a.slice) - e0;
+    row.g = static_cast<const Raw *>(a.logits) + r * a.lsr + i * a.lsi + e0;
+    row.inf = false;
+    const Span sp = span_of(row.g, row.len);
+    const Segment sg = segment_of(sp, row.len, warp);
+    const uint4 *gv = reinterpret_cast<const uint4 *>(row.g + sp.head);
     const float temp = a.temperature ? a.temperature[r] : 1.f;
-    const bool bad_temp = !(temp >= 0.f) || temp == INFINITY;
+    const bool bad_temp = !(temp >= 0.f) || temp == INFINITY, greedy = temp == 0.f;
     float *prow = a.probs ? a.probs + r * a.psr + i * a.psi + e0 : nullptr;
     if (tid < 16) sm.tab.v[tid] = g_exp_table.v[tid];
+    __syncthreads();
 
-    // ---- the slice into shared memory, its largest logit
+    // ---- the largest logit and, against each thread's largest so far, the weight
     float mx = -INFINITY;
+    Running run;
+    run.clear();
+    RowScale rs = row_scale(0.f, bad_temp || greedy ? 1.f : temp);
+    rs.set_scale(-(1 << 20));  // (the thread's scale so far)
+    auto grow = [&](float m) {  // m: the largest of the next logits
+        if (!(m > mx)) return;
+        mx = m;
+        const int e = (int)fminf(fmaxf(floorf(m * rs.ch), -524288.f), 524288.f) + 1;
+        if (e <= rs.E) return;
+        const int d = min(e - rs.E, 126);
+        const V2 f = splat<V2>(__int_as_float((127 - d) << 23));
+        run.acc = run.acc * f;
+        run.low = run.low * f;
+        rs.set_scale(e);
+    };
+    auto pair = [&](float v0, float v1) {
+        V2 h, l;
+        weight_ff<V2, false>(V2{f2_pack(v0, v1)}, rs, sm.tab, h, l);
+        run.add(h, l);
+    };
+    auto ragged = [&](int x0, int x1) {
+        for (int x = x0 + lane; x < x1; x += 32) {
+            const float v = clean(L::wide(__ldg(row.g + x)));
+            grow(v);
+            pair(v, -INFINITY);
+        }
+    };
+    ragged(sg.head0, sg.head1);
     {
-        const int head = min(len, pad ? kVec - pad : 0);
-        const int nvec = (len - head) / kVec, tail = head + nvec * kVec;
-        float *dst = slice + pad;
-        if (tid < head) {
-            mx = clean(L::wide(__ldg(gs + tid)));
-            dst[tid] = mx;
-        }
-        if (tid < len - tail) {
-            const float v = clean(L::wide(__ldg(gs + tail + tid)));
-            dst[tail + tid] = v;
-            mx = fmaxf(mx, v);
-        }
-        if (tid < pad) slice[tid] = -INFINITY;
-        if (tid < n - pad - len) dst[len + tid] = -INFINITY;
-        const uint4 *gv = reinterpret_cast<const uint4 *>(gs + head);
-        float *sv = dst + head;
-        auto take = [&](uint4 q, int x) {
-            const Raw *e = reinterpret_cast<const Raw *>(&q);
-#pragma unroll
-            for (int k = 0; k < kVec; k += 4) {
-                float4 v;
-                v.x = clean(L::wide(e[k]));
-                v.y = clean(L::wide(e[k + 1]));
-                v.z = clean(L::wide(e[k + 2]));
-                v.w = clean(L::wide(e[k + 3]));
-                mx = max3f(max3f(mx, v.x, v.y), v.z, v.w);
-                *reinterpret_cast<float4 *>(sv + x * kVec + k) = v;
-            }
-        };
-        constexpr int kU = 8;  // loads in flight a thread
-        int x = tid;
-        for (; x + (kU - 1) * kFullThreads < nvec; x += kU * kFullThreads) {
+        constexpr int kU = 32 / kVec;  // 4 or 8 loads in flight a thread
+        for (int x = sg.v0 + lane; x < sg.v1; x += 32 * kU) {
             uint4 q[kU];
 #pragma unroll
-            for (int u = 0; u < kU; ++u) q[u] = __ldcs(gv + x + u * kFullThreads);
+            for (int u = 0; u < kU; ++u)
+                if (x + 32 * u < sg.v1) q[u] = __ldg(gv + x + 32 * u);
 #pragma unroll
-            for (int u = 0; u < kU; ++u) take(q[u], x + u * kFullThreads);
+            for (int u = 0; u < kU; ++u) {
+                if (x + 32 * u >= sg.v1) break;
+                const Raw *e = reinterpret_cast<const Raw *>(&q[u]);
+                float m = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < kVec; k += 2) m = max3f(m, L::wide(e[k]), L::wide(e[k + 1]));
+                grow(m);
+#pragma unroll
+                for (int k = 0; k < kVec; k += 2) pair(L::wide(e[k]), L::wide(e[k + 1]));
+            }
         }
-        for (; x < nvec; x += kFullThreads) take(__ldcs(gv + x), x);
     }
+    ragged(sg.tail0, sg.tail1);
+
+    // ---- the row's largest logit
+    float rmx = mx;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
-    if (lane == 0) sm.red[warp] = mx;
+    for (int o = 16; o > 0; o >>= 1) rmx = fmaxf(rmx, __shfl_xor_sync(kAll, rmx, o));
+    if (lane == 0) sm.red[warp] = rmx;
     __syncthreads();
-    mx = lane < kFullWarps ? sm.red[lane] : -INFINITY;
+    rmx = sm.red[lane % kWarps];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
-    if (tid == 0) sm.x_max = mx;
-    cluster_sync();
+    for (int o = kWarps / 2; o > 0; o >>= 1) rmx = fmaxf(rmx, __shfl_xor_sync(kAll, rmx, o));
+    if (ncta > 1) {
+        if (tid == 0) sm.x_max = rmx;
+        cluster_sync();
+        if (lane < (int)ncta) rmx = *map_to_rank(&sm.x_max, lane);
 #pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c)
-        if (c < ncta) mx = fmaxf(mx, *map_to_rank(&sm.x_max, c));
-    if (bad_temp || mx == -INFINITY) {  // no distribution (uniform over the cluster)
+        for (int o = 16; o > 0; o >>= 1) rmx = fmaxf(rmx, __shfl_xor_sync(kAll, rmx, o));
+    }
+    if (bad_temp || rmx == -INFINITY) {  // no distribution (uniform over the cluster)
         cluster_reads_done();
         if (prow)
-            for (int x = tid; x < len; x += kFullThreads) prow[x] = 0.f;
+            for (int x = tid; x < row.len; x += kThreads) prow[x] = 0.f;
         if (rank == 0 && tid == 0) {
             if (a.tokens) a.tokens[rowi] = -1;
             report_status(a.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
@@ -585,12 +640,12 @@ __global__ void __launch_bounds__(kFullThreads, 2) sample_full_kernel(const Samp
         cluster_wait_reads();
         return;
     }
-    if (temp == 0.f) {  // greedy: the first largest logit alone
+    if (greedy) {  // the first largest logit alone
         if (tid == 0) sm.x_first = INT_MAX;
         __syncthreads();
         int first = INT_MAX;
-        for (int x = tid; x < n && first == INT_MAX; x += kFullThreads)
-            if (slice[x] == mx) first = e0 + x - pad;
+        for (int x = tid; x < row.len && first == INT_MAX; x += kThreads)
+            if (clean(L::wide(__ldg(row.g + x))) == rmx) first = e0 + x;
         first = __reduce_min_sync(kAll, first);
         if (lane == 0) atomicMin(&sm.x_first, first);
         cluster_sync();
@@ -598,75 +653,90 @@ __global__ void __launch_bounds__(kFullThreads, 2) sample_full_kernel(const Samp
         first = __reduce_min_sync(kAll, first);
         cluster_reads_done();
         if (prow)
-            for (int x = tid; x < len; x += kFullThreads) prow[x] = e0 + x == first ? 1.f : 0.f;
+            for (int x = tid; x < row.len; x += kThreads) prow[x] = e0 + x == first ? 1.f : 0.f;
         if (a.tokens && rank == 0 && tid == 0) a.tokens[rowi] = first;
         cluster_wait_reads();
         return;
     }
-    const bool inf = mx == INFINITY;
-    if (inf) {
-        for (int x = tid; x < n; x += kFullThreads) slice[x] = if_inf(slice[x]);
-        mx = 0.f;
-        __syncthreads();
-    }
-    const RowScale rs = row_scale(mx, temp);
-    const int seg = ((n + kFullWarps - 1) / kFullWarps + 127) & ~127;
-    const int w0 = min(n, warp * seg), w1 = min(n, w0 + seg);
+    row.inf = rmx == INFINITY;
+    const int met = rs.E;
+    rs = row_scale(row.inf ? 0.f : rmx, temp);
     uint64_t sum;
-    if (prow)
-        sum = rs.wide ? sum_slice<true, true>(slice, w0, w1, rs, sm.tab, lane)
-                      : sum_slice<true, false>(slice, w0, w1, rs, sm.tab, lane);
-    else
-        sum = rs.wide ? sum_slice<false, true>(slice, w0, w1, rs, sm.tab, lane)
-                      : sum_slice<false, false>(slice, w0, w1, rs, sm.tab, lane);
+    if (rs.wide || row.inf) {
+        sum = sum_segment<T>(row, sp, sg, rs, sm.tab, lane);
+    } else {
+        sum = run.units(met, rs.E);
+    }
     sum = warp_sum64(sum);
     uint64_t total, before;
     share_sums(sm.draw, sum, ncta, rank, total, before);
     cluster_reads_done();
+
+    // ---- the distribution
     if (prow) {
         const float inv = inverse(total);
-        float *out = prow - pad;
-        if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
-#pragma unroll 2
-            for (int x = w0 + 4 * lane; x < w1; x += 128) {
-                const float4 v = *reinterpret_cast<const float4 *>(slice + x);
-                if (x >= pad && x + 4 <= pad + len) {
-                    __stcs(reinterpret_cast<float4 *>(out + x),
-                           make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-                } else {
-                    const float e[4] = {v.x, v.y, v.z, v.w};
-                    for (int k = 0; k < 4; ++k)
-                        if (x + k >= pad && x + k < pad + len) out[x + k] = e[k] * inv;
+        const V2 inv2 = splat<V2>(inv);
+        const bool vec = ((reinterpret_cast<uintptr_t>(prow + sp.head)) & 15) == 0;
+        auto one = [&](int x) {
+            float wf;
+            weight(row.value(__ldg(row.g + x)), rs, sm.tab, wf);
+            prow[x] = wf * inv;
+        };
+        for (int x = sg.head0 + lane; x < sg.head1; x += 32) one(x);
+        if (vec && !rs.wide && !row.inf) {
+            constexpr int kU = 16 / kVec;
+            for (int x = sg.v0 + lane; x < sg.v1; x += 32 * kU) {
+                uint4 q[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    if (x + 32 * u < sg.v1) q[u] = __ldcs(gv + x + 32 * u);
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    if (x + 32 * u >= sg.v1) break;
+                    const Raw *e = reinterpret_cast<const Raw *>(&q[u]);
+                    float *out = prow + sp.head + (long)(x + 32 * u) * kVec;
+#pragma unroll
+                    for (int k = 0; k < kVec; k += 4) {
+                        V2 h[2], l;
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            weight_ff<V2, false>(
+                                V2{f2_pack(L::wide(e[k + 2 * p]), L::wide(e[k + 2 * p + 1]))}, rs,
+                                sm.tab, h[p], l);
+                            h[p] = h[p] * inv2;
+                        }
+                        const float2 x0 = f2_unpack(h[0].a), x1 = f2_unpack(h[1].a);
+                        __stcs(reinterpret_cast<float4 *>(out + k),
+                               make_float4(x0.x, x0.y, x1.x, x1.y));
+                    }
                 }
             }
         } else {
-            __syncwarp();
-            for (int x = w0 + lane; x < w1; x += 32)
-                if (x >= pad && x < pad + len) __stcs(out + x, slice[x] * inv);
+            for (int x = sp.head + sg.v0 * kVec + lane; x < sp.head + sg.v1 * kVec; x += 32) one(x);
         }
+        for (int x = sg.tail0 + lane; x < sg.tail1; x += 32) one(x);
     }
+    // ---- the draw
     if (a.tokens) {
         const uint64_t target = draw_target(a.u[rowi], total);
         const int w = warp_of_target(sm.draw, target, before);
-        if (w >= 0) {  // the draw is in warp w's segment of this slice
-            // its weights again, from the input, four positions a thread (single
-            // weights round to units, so the last positive one takes a target
-            // past their sum)
-            const int x0 = w * seg, x1 = min(n, x0 + seg);
-            for (int base = x0; base < x1; base += 4 * kFullThreads) {
+        if (w >= 0) {
+            // in warp w's segment of this slice: its weights again, four positions a
+            // thread (single weights round to units, so the last positive one takes
+            // a target past their sum)
+            const Segment d = segment_of(sp, row.len, w);
+            const int x0 = d.head1 > d.head0 ? 0 : sp.head + d.v0 * kVec;
+            const int x1 = d.tail1 > d.tail0 ? row.len : sp.head + d.v1 * kVec;
+            for (int base = x0; base < x1; base += 4 * kThreads) {
                 const int x = base + 4 * tid;
                 uint64_t q[4], s4 = 0;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int e = x + k - pad;
-                    float v = x + k < x1 && e >= 0 && e < len ? clean(L::wide(__ldg(gs + e)))
-                                                              : -INFINITY;
-                    if (inf) v = if_inf(v);
                     float wf;
-                    q[k] = weight(v, rs, sm.tab, wf);
+                    q[k] = x + k < x1 ? weight(row.value(__ldg(row.g + x + k)), rs, sm.tab, wf) : 0;
                     s4 += q[k];
                 }
-                draw_in_block(sm.draw, target, before, q, s4, e0 + x - pad, a.tokens + rowi);
+                draw_in_block(sm.draw, target, before, q, s4, e0 + x, a.tokens + rowi);
             }
         }
     }
@@ -696,7 +766,7 @@ struct CutShared {
     };
     uint32_t parts[kBins];        // pivot search: this CTA's part maxima by bin
     uint64_t scan[kWarps], scan_c[kWarps];
-    DrawShared<kWarps> draw;
+    DrawShared draw;
     uint32_t wties[kWarps];       // cut-key elements of each warp's segment
     float red[2][kWarps];
     uint32_t hit[kListMax];       // parts that reach the pivot: thread * kParts + part
@@ -731,7 +801,9 @@ struct Row {
     const typename L::Raw *s;  // kRes: the copy, as far from a 16-byte boundary
     int n;
     bool inf;  // the row's maximum is +inf
-    __device__ __forceinline__ typename L::Raw raw(int x) const { return kRes ? s[x] : __ldg(g + x); }
+    __device__ __forceinline__ typename L::Raw raw(int x) const {
+        return kRes ? s[x] : __ldg(g + x);
+    }
     __device__ __forceinline__ uint4 vec(const uint4 *p) const { return kRes ? *p : __ldg(p); }
     __device__ __forceinline__ float at(int x) const {
         const float v = clean(L::wide(raw(x)));
@@ -933,25 +1005,10 @@ __device__ __forceinline__ void scan_list(uint64_t *a, int n, uint64_t *scratch)
     static_assert(kListMax == 2 * kThreads, "two entries a thread");
     const int i = 2 * threadIdx.x;
     const uint64_t x = i < n ? a[i] : 0, y = i + 1 < n ? a[i + 1] : 0;
-    const uint64_t t = block_scan64<kWarps>(x + y, scratch);
+    const uint64_t t = block_scan64(x + y, scratch);
     if (i < n) a[i] = t - y;
     if (i + 1 < n) a[i + 1] = t;
     __syncthreads();
-}
-
-// How a slice splits into 16-byte vectors: element counts of the ragged ends.
-struct Span {
-    int head, nvec, tail;  // tail: the first element behind the vectors
-};
-template <typename Raw>
-__device__ __forceinline__ Span span_of(const Raw *p, int len) {
-    constexpr int kVec = 16 / (int)sizeof(Raw);
-    const int mis = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(Raw));
-    Span s;
-    s.head = min(len, mis ? kVec - mis : 0);
-    s.nvec = (len - s.head) / kVec;
-    s.tail = s.head + s.nvec * kVec;
-    return s;
 }
 
 // The weight of the slice in units, this thread's share (every thread of the CTA).
@@ -962,8 +1019,8 @@ __device__ __forceinline__ uint64_t sum_stream(const Row<T, kRes> &row, const Sp
     using Raw = typename L::Raw;
     constexpr int kVec = 16 / (int)sizeof(Raw);
     const int tid = threadIdx.x;
-    const V2 neg = splat<V2>(-1.f);
-    V2 acc = splat<V2>(0.f), low = splat<V2>(0.f);
+    Running run;
+    run.clear();
     auto add = [&](float v0, float v1) {
         if (row.inf) {
             v0 = if_inf(v0);
@@ -971,11 +1028,7 @@ __device__ __forceinline__ uint64_t sum_stream(const Row<T, kRes> &row, const Sp
         }
         V2 h, l;
         weight_ff<V2, kWide>(V2{f2_pack(v0, v1)}, rs, tab, h, l);
-        const V2 t = acc + h;  // TwoSum
-        const V2 hh = vfma(acc, neg, t);
-        const V2 err = vfma(vfma(hh, neg, t), neg, acc) + vfma(hh, neg, h);
-        acc = t;
-        low = low + (err + l);
+        run.add(h, l);
     };
     if (tid < sp.head) add(clean(L::wide(row.raw(tid))), -INFINITY);
     if (tid < row.n - sp.tail) add(clean(L::wide(row.raw(sp.tail + tid))), -INFINITY);
@@ -994,9 +1047,7 @@ __device__ __forceinline__ uint64_t sum_stream(const Row<T, kRes> &row, const Sp
             for (int k = 0; k < kVec; k += 2) add(clean(L::wide(e[k])), clean(L::wide(e[k + 1])));
         }
     }
-    const float2 a = f2_unpack(acc.a), b = f2_unpack(low.a);
-    return (uint64_t)(__float2ll_rn(a.x * kUnits) + __float2ll_rn(a.y * kUnits) +
-                      __float2ll_rn(b.x * kUnits) + __float2ll_rn(b.y * kUnits));
+    return run.units(0, 0);
 }
 
 template <typename T, bool kRes>
@@ -1218,7 +1269,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
                     weight(hi - ((float)tid + 0.5f) * (hi - lo) * (1.f / kBins), rs, sm.tab, wf);
                     v += (uint64_t)((float)n * wf * 65536.f) << 32;
                 }
-                const uint64_t inc = block_scan64<kWarps>(v, sm.scan);
+                const uint64_t inc = block_scan64(v, sm.scan);
                 const uint32_t upto = above + (uint32_t)inc;
                 const float g16 = goal * 0.125f;
                 const bool in = use_k ? upto >= need && upto - n < need
@@ -1411,7 +1462,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
                             const int x = 2 * tid + k;
                             w[k] = x < keep ? own((int)(uint32_t)keys[x]) : 0;
                         }
-                        const uint64_t t = block_scan64<kWarps>(w[0] + w[1], sm.scan);
+                        const uint64_t t = block_scan64(w[0] + w[1], sm.scan);
                         const uint64_t t0 = t - w[1];
                         if (t0 > target && t0 - w[0] <= target)
                             a.tokens[rowi] = (int)(keys[2 * tid] >> 32);
@@ -1616,21 +1667,6 @@ int launch_typed(const SampleArgs &in, int num_sms, cudaStream_t stream) {
         a.ncta = ncta;
         a.slice = (int)((((long)a.V + ncta - 1) / ncta + 31) & ~31L);
     };
-    if (!a.top_k && !a.top_p && !a.min_p) {
-        // CTAs a row: enough that two slices (as fp32) fit an SM, and more while
-        // they still spread the rows over the GPU (a slice of at least 4096)
-        constexpr long kMaxSlice = 104 * 1024;
-        const long bytes = (long)a.V * 4;
-        int ncta = 1;
-        while (ncta < kMaxCluster &&
-               (bytes > kMaxSlice * ncta || (rows * ncta <= num_sms && a.V / (2 * ncta) >= 4096)))
-            ncta *= 2;
-        set_slices(ncta);
-        // pad in front (up to 7 logits) and up to a multiple of 128 behind
-        const size_t smem = ((size_t)a.slice + 7 + 127) / 128 * 512;
-        if (smem <= 190 * 1024)
-            return launch_cluster(sample_full_kernel<T>, a, kFullThreads, smem, stream);
-    }
     // one CTA a row when the rows alone fill the GPU twice over; else slices of at
     // least 4096
     int ncta = 1;
@@ -1638,6 +1674,8 @@ int launch_typed(const SampleArgs &in, int num_sms, cudaStream_t stream) {
            ((rows * ncta <= num_sms && a.V / (2 * ncta) >= 4096) || a.V > ncta * (1 << 18)))
         ncta *= 2;
     set_slices(ncta);
+    if (!a.top_k && !a.top_p && !a.min_p)
+        return launch_cluster(sample_full_kernel<T>, a, kThreads, 0, stream);
     // slices two of which fit an SM stay there for the later passes
     const size_t smem = (size_t)a.slice * sizeof(T) + 16;
     if (smem <= 72 * 1024)
