@@ -21,10 +21,10 @@
 //
 // Layout.  One thread-block cluster per row (of one CTA when there are rows
 // enough), its CTAs the vocabulary slices.  Two kernels:
-//   sample_full    no filter arrays: one pass for the row's weight, each thread
-//                  against the largest logit it has met so far (a new one moves
-//                  its scale by a power of two, exactly), a second one, from L2,
-//                  for the distribution.
+//   sample_full    no filter arrays: one pass for the weights (stored to probs as
+//                  they are) and their sum, against a scale taken from the row's
+//                  first logits; a second one, on lines still in L2, that divides
+//                  by the sum.  Two CTAs a row keep the rows in flight within L2.
 //   sample_cut     filters: the row is streamed once for the maxima of some
 //                  thousand parts of it (and, with probs, zeros are stored); a
 //                  pivot below which nothing can be kept comes from those maxima
@@ -58,10 +58,10 @@ constexpr int kListMax = 1024;  // candidates the sorted list holds
 constexpr uint32_t kAll = 0xffffffffu;
 
 // ------------------------------------------------------------ 2^(j / 16)
-// The factor as hi + lo.  Sixteen 8-byte entries fill the 32 banks of shared
-// memory once, so a warp's lookups never conflict.
+// The factor as hi + lo.  Sixteen words of either lie in banks of their own, so a
+// warp's lookups never conflict.
 struct ExpTable {
-    float2 v[16];
+    float hi[16], lo[16];
 };
 constexpr double exp2_series(double x) {  // 2^x for 0 <= x < 1 (Taylor series of e^(x ln 2))
     const double y = x * 0.69314718055994530942;
@@ -76,8 +76,8 @@ constexpr ExpTable make_exp_table() {
     ExpTable t{};
     for (int j = 0; j < 16; ++j) {
         const double v = exp2_series(j / 16.0);
-        t.v[j].x = (float)v;
-        t.v[j].y = (float)(v - (double)(float)v);
+        t.hi[j] = (float)v;
+        t.lo[j] = (float)(v - (double)(float)v);
     }
     return t;
 }
@@ -139,25 +139,22 @@ __device__ __forceinline__ V2 splat<V2>(float x) { return {f2_pack(x, x)}; }
 
 // Table entry and power of two of k sixteenths, from t = k + 1.5 * 2^23: the
 // float's low bits are k's, and 19 places up only k's own remain.
-__device__ __forceinline__ float2 table_at(const ExpTable &tab, float t) {
-    return tab.v[__float_as_uint(t) & 15u];
-}
+__device__ __forceinline__ uint32_t table_at(float t) { return __float_as_uint(t) & 15u; }
 __device__ __forceinline__ float pow2_at(float t, uint32_t ebits) {
     return __uint_as_float(((__float_as_uint(t) << 19) & 0xff800000u) + ebits);
 }
 __device__ __forceinline__ void lookup(const ExpTable &tab, uint32_t ebits, V1 t, V1 &th, V1 &tl,
                                        V1 &sc) {
-    const float2 e = table_at(tab, t.a);
-    th.a = e.x;
-    tl.a = e.y;
+    th.a = tab.hi[table_at(t.a)];
+    tl.a = tab.lo[table_at(t.a)];
     sc.a = pow2_at(t.a, ebits);
 }
 __device__ __forceinline__ void lookup(const ExpTable &tab, uint32_t ebits, V2 t, V2 &th, V2 &tl,
                                        V2 &sc) {
     const float2 u = f2_unpack(t.a);
-    const float2 e0 = table_at(tab, u.x), e1 = table_at(tab, u.y);
-    th.a = f2_pack(e0.x, e1.x);
-    tl.a = f2_pack(e0.y, e1.y);
+    const uint32_t i0 = table_at(u.x), i1 = table_at(u.y);
+    th.a = f2_pack(tab.hi[i0], tab.hi[i1]);
+    tl.a = f2_pack(tab.lo[i0], tab.lo[i1]);
     sc.a = f2_pack(pow2_at(u.x, ebits), pow2_at(u.y, ebits));
 }
 // Zero where y <= ymin (and for -inf and NaN).
@@ -456,7 +453,7 @@ struct Running {
     // in units, of a scale 2^(to - from) as large
     __device__ __forceinline__ uint64_t units(int from, int to) const {
         const float2 a = f2_unpack(acc.a), b = f2_unpack(low.a);
-        if (to - from > 64) return 0;
+        if (to - from > 126) return 0;
         const float f = kUnits * __int_as_float((127 + from - to) << 23);
         const long long v = __float2ll_rn(a.x * f) + __float2ll_rn(a.y * f) +
                             __float2ll_rn(b.x * f) + __float2ll_rn(b.y * f);
@@ -558,36 +555,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_full_kernel(const SampleAr
     const float temp = a.temperature ? a.temperature[r] : 1.f;
     const bool bad_temp = !(temp >= 0.f) || temp == INFINITY, greedy = temp == 0.f;
     float *prow = a.probs ? a.probs + r * a.psr + i * a.psi + e0 : nullptr;
-    if (tid < 16) sm.tab.v[tid] = g_exp_table.v[tid];
+    if (tid < 16) {
+        sm.tab.hi[tid] = g_exp_table.hi[tid];
+        sm.tab.lo[tid] = g_exp_table.lo[tid];
+    }
     __syncthreads();
 
-    // ---- the largest logit and, against each thread's largest so far, the weight
+    // ---- the scale of the first pass: that of the row's first logits, so at most
+    // the row's own (a row whose first logits are masked takes 0)
+    const Raw *row0 = row.g - e0;
+    float first = -INFINITY;
+    for (int x = 0; x < min(a.V, 4); ++x) first = fmaxf(first, L::wide(__ldg(row0 + x)));
+    RowScale rs = row_scale(0.f, bad_temp || greedy ? 1.f : temp);
+    const float y0 = first * rs.ch;
+    const int E0 = fabsf(y0) < 131072.f ? (int)floorf(y0) + 1 : 0;
+    rs.set_scale(E0);
+
+    // ---- weights, their sum, the largest logit
     float mx = -INFINITY;
     Running run;
     run.clear();
-    RowScale rs = row_scale(0.f, bad_temp || greedy ? 1.f : temp);
-    rs.set_scale(-(1 << 20));  // (the thread's scale so far)
-    auto grow = [&](float m) {  // m: the largest of the next logits
-        if (!(m > mx)) return;
-        mx = m;
-        const int e = (int)fminf(fmaxf(floorf(m * rs.ch), -524288.f), 524288.f) + 1;
-        if (e <= rs.E) return;
-        const int d = min(e - rs.E, 126);
-        const V2 f = splat<V2>(__int_as_float((127 - d) << 23));
-        run.acc = run.acc * f;
-        run.low = run.low * f;
-        rs.set_scale(e);
-    };
-    auto pair = [&](float v0, float v1) {
-        V2 h, l;
-        weight_ff<V2, false>(V2{f2_pack(v0, v1)}, rs, sm.tab, h, l);
-        run.add(h, l);
-    };
+    const bool vec = (reinterpret_cast<uintptr_t>(prow + sp.head) & 15) == 0;
     auto ragged = [&](int x0, int x1) {
         for (int x = x0 + lane; x < x1; x += 32) {
-            const float v = clean(L::wide(__ldg(row.g + x)));
-            grow(v);
-            pair(v, -INFINITY);
+            const float v = L::wide(__ldg(row.g + x));
+            mx = fmaxf(mx, v);
+            V2 h, l;
+            weight_ff<V2, false>(V2{f2_pack(v, -INFINITY)}, rs, sm.tab, h, l);
+            run.add(h, l);
+            if (prow) prow[x] = f2_unpack(h.a).x;
         }
     };
     ragged(sg.head0, sg.head1);
@@ -602,12 +598,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_full_kernel(const SampleAr
             for (int u = 0; u < kU; ++u) {
                 if (x + 32 * u >= sg.v1) break;
                 const Raw *e = reinterpret_cast<const Raw *>(&q[u]);
-                float m = -INFINITY;
+                float *out = prow + sp.head + (long)(x + 32 * u) * kVec;
 #pragma unroll
-                for (int k = 0; k < kVec; k += 2) m = max3f(m, L::wide(e[k]), L::wide(e[k + 1]));
-                grow(m);
+                for (int k = 0; k < kVec; k += 4) {
+                    V2 h[2], l[2];
 #pragma unroll
-                for (int k = 0; k < kVec; k += 2) pair(L::wide(e[k]), L::wide(e[k + 1]));
+                    for (int p = 0; p < 2; ++p) {
+                        const float v0 = L::wide(e[k + 2 * p]), v1 = L::wide(e[k + 2 * p + 1]);
+                        mx = max3f(mx, v0, v1);
+                        weight_ff<V2, false>(V2{f2_pack(v0, v1)}, rs, sm.tab, h[p], l[p]);
+                        run.add(h[p], l[p]);
+                    }
+                    if (prow) {
+                        const float2 x0 = f2_unpack(h[0].a), x1 = f2_unpack(h[1].a);
+                        if (vec) {
+                            *reinterpret_cast<float4 *>(out + k) =
+                                make_float4(x0.x, x0.y, x1.x, x1.y);
+                        } else {
+                            out[k] = x0.x;
+                            out[k + 1] = x0.y;
+                            out[k + 2] = x1.x;
+                            out[k + 3] = x1.y;
+                        }
+                    }
+                }
             }
         }
     }
@@ -659,62 +673,69 @@ __global__ void __launch_bounds__(kThreads, 2) sample_full_kernel(const SampleAr
         return;
     }
     row.inf = rmx == INFINITY;
-    const int met = rs.E;
     rs = row_scale(row.inf ? 0.f : rmx, temp);
-    uint64_t sum;
-    if (rs.wide || row.inf) {
-        sum = sum_segment<T>(row, sp, sg, rs, sm.tab, lane);
-    } else {
-        sum = run.units(met, rs.E);
-    }
+    // the first pass holds unless its scale was far below the row's (its weights
+    // may have left fp32's range) or above it, or the row needs the wide form
+    const bool again = rs.wide || row.inf || rs.E < E0 || rs.E > E0 + 100;
+    uint64_t sum = again ? sum_segment<T>(row, sp, sg, rs, sm.tab, lane) : run.units(E0, rs.E);
     sum = warp_sum64(sum);
     uint64_t total, before;
     share_sums(sm.draw, sum, ncta, rank, total, before);
     cluster_reads_done();
 
-    // ---- the distribution
+    // ---- the distribution (each lane has its own stores before it)
     if (prow) {
         const float inv = inverse(total);
-        const V2 inv2 = splat<V2>(inv);
-        const bool vec = ((reinterpret_cast<uintptr_t>(prow + sp.head)) & 15) == 0;
-        auto one = [&](int x) {
-            float wf;
-            weight(row.value(__ldg(row.g + x)), rs, sm.tab, wf);
-            prow[x] = wf * inv;
-        };
-        for (int x = sg.head0 + lane; x < sg.head1; x += 32) one(x);
-        if (vec && !rs.wide && !row.inf) {
-            constexpr int kU = 16 / kVec;
-            for (int x = sg.v0 + lane; x < sg.v1; x += 32 * kU) {
-                uint4 q[kU];
+        if (again) {
+            auto one = [&](int x) {
+                float wf;
+                weight(row.value(__ldg(row.g + x)), rs, sm.tab, wf);
+                prow[x] = wf * inv;
+            };
+            for (int x = sg.head0 + lane; x < sg.head1; x += 32) one(x);
+            __syncwarp();
+            for (int x = sp.head + sg.v0 * kVec + lane; x < sp.head + sg.v1 * kVec; x += 32) one(x);
+            for (int x = sg.tail0 + lane; x < sg.tail1; x += 32) one(x);
+        } else {
+            // the stored weights are relative to E0
+            const float f = __int_as_float((127 + E0 - rs.E) << 23);
+            const V2 f2 = splat<V2>(f), i2 = splat<V2>(inv);
+            for (int x = sg.head0 + lane; x < sg.head1; x += 32) prow[x] = prow[x] * f * inv;
+            for (int x = sg.tail0 + lane; x < sg.tail1; x += 32) prow[x] = prow[x] * f * inv;
+            if (vec) {
+                constexpr int kU = 4;
+                const int q0 = sg.v0 * (kVec / 4), q1 = sg.v1 * (kVec / 4);
+                float4 *out = reinterpret_cast<float4 *>(prow + sp.head);
+                // (a lane's quads: kVec / 4 neighbours of each of its vectors)
+                auto quad = [&](int j) {
+                    const int v = j / (kVec / 4), k = j % (kVec / 4);
+                    return (sg.v0 + v * 32 + lane) * (kVec / 4) + k;
+                };
+                const int n = ((sg.v1 - sg.v0 + 31) / 32) * (kVec / 4);
+                for (int j = 0; j < n; j += kU) {
+                    float4 w[kU];
 #pragma unroll
-                for (int u = 0; u < kU; ++u)
-                    if (x + 32 * u < sg.v1) q[u] = __ldcs(gv + x + 32 * u);
+                    for (int u = 0; u < kU; ++u) {
+                        const int x = quad(j + u);
+                        if (j + u < n && x >= q0 && x < q1) w[u] = out[x];
+                    }
 #pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    if (x + 32 * u >= sg.v1) break;
-                    const Raw *e = reinterpret_cast<const Raw *>(&q[u]);
-                    float *out = prow + sp.head + (long)(x + 32 * u) * kVec;
-#pragma unroll
-                    for (int k = 0; k < kVec; k += 4) {
-                        V2 h[2], l;
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            weight_ff<V2, false>(
-                                V2{f2_pack(L::wide(e[k + 2 * p]), L::wide(e[k + 2 * p + 1]))}, rs,
-                                sm.tab, h[p], l);
-                            h[p] = h[p] * inv2;
-                        }
-                        const float2 x0 = f2_unpack(h[0].a), x1 = f2_unpack(h[1].a);
-                        __stcs(reinterpret_cast<float4 *>(out + k),
-                               make_float4(x0.x, x0.y, x1.x, x1.y));
+                    for (int u = 0; u < kU; ++u) {
+                        const int x = quad(j + u);
+                        if (!(j + u < n && x >= q0 && x < q1)) continue;
+                        const float2 x0 = f2_unpack((V2{f2_pack(w[u].x, w[u].y)} * f2 * i2).a);
+                        const float2 x1 = f2_unpack((V2{f2_pack(w[u].z, w[u].w)} * f2 * i2).a);
+                        __stcs(out + x, make_float4(x0.x, x0.y, x1.x, x1.y));
                     }
                 }
+            } else {
+                for (int v = sg.v0 + lane; v < sg.v1; v += 32)
+                    for (int k = 0; k < kVec; ++k) {
+                        float *o = prow + sp.head + (long)v * kVec + k;
+                        *o = *o * f * inv;
+                    }
             }
-        } else {
-            for (int x = sp.head + sg.v0 * kVec + lane; x < sp.head + sg.v1 * kVec; x += 32) one(x);
         }
-        for (int x = sg.tail0 + lane; x < sg.tail1; x += 32) one(x);
     }
     // ---- the draw
     if (a.tokens) {
@@ -1084,7 +1105,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
     const bool use_p = !one && top_p < 1.f;
     const bool use_m = !one && min_p > 0.f;
     float *prow = a.probs ? a.probs + r * a.psr + i * a.psi + e0 : nullptr;
-    if (tid < 16) sm.tab.v[tid] = g_exp_table.v[tid];
+    if (tid < 16) {
+        sm.tab.hi[tid] = g_exp_table.hi[tid];
+        sm.tab.lo[tid] = g_exp_table.lo[tid];
+    }
     if (tid == 0) sm.n_hit = sm.n_list = sm.n_below = sm.n_min = 0;
 
     // ---- one pass: the largest logit of each of the thread's kParts parts (vector
@@ -1673,9 +1697,14 @@ int launch_typed(const SampleArgs &in, int num_sms, cudaStream_t stream) {
     while (ncta < kMaxCluster &&
            ((rows * ncta <= num_sms && a.V / (2 * ncta) >= 4096) || a.V > ncta * (1 << 18)))
         ncta *= 2;
-    set_slices(ncta);
-    if (!a.top_k && !a.top_p && !a.min_p)
+    if (!a.top_k && !a.top_p && !a.min_p) {
+        // (two CTAs a row, four to an SM pair: the rows in flight, as stored
+        // weights, fit L2 up to V = 200 k)
+        if (ncta < 2 && a.probs && a.V >= 16384) ncta = 2;
+        set_slices(ncta);
         return launch_cluster(sample_full_kernel<T>, a, kThreads, 0, stream);
+    }
+    set_slices(ncta);
     // slices two of which fit an SM stay there for the later passes
     const size_t smem = (size_t)a.slice * sizeof(T) + 16;
     if (smem <= 72 * 1024)
