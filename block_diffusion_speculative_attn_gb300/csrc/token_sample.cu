@@ -494,6 +494,46 @@ __device__ __forceinline__ Segment segment_of(const Span &sp, int len, int w) {
     return g;
 }
 
+// kV = 4 or 8 floats, a 16- or 32-byte line piece a lane when aligned; kLast: not
+// read again, so the first to leave L2.
+template <int kV, bool kLast>
+__device__ __forceinline__ void store_vec(float *p, const float (&w)[kV], bool aligned) {
+    if (!aligned) {
+#pragma unroll
+        for (int k = 0; k < kV; ++k) p[k] = w[k];
+    } else if constexpr (kV == 8 && kLast) {
+        asm volatile(
+            "st.global.L2::evict_first.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+            "f"(w[0]), "f"(w[1]), "f"(w[2]), "f"(w[3]), "f"(w[4]), "f"(w[5]), "f"(w[6]), "f"(w[7])
+            : "memory");
+    } else if constexpr (kV == 8) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+                     "f"(w[0]), "f"(w[1]), "f"(w[2]), "f"(w[3]), "f"(w[4]), "f"(w[5]), "f"(w[6]),
+                     "f"(w[7])
+                     : "memory");
+    } else if constexpr (kLast) {
+        __stcs(reinterpret_cast<float4 *>(p), make_float4(w[0], w[1], w[2], w[3]));
+    } else {
+        *reinterpret_cast<float4 *>(p) = make_float4(w[0], w[1], w[2], w[3]);
+    }
+}
+template <int kV>
+__device__ __forceinline__ void load_vec(const float *p, float (&w)[kV]) {
+    if constexpr (kV == 8) {
+        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]), "=f"(w[4]), "=f"(w[5]),
+                       "=f"(w[6]), "=f"(w[7])
+                     : "l"(p)
+                     : "memory");
+    } else {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    }
+}
+
 // ============================================================ sample_full
 struct FullShared {
     ExpTable tab;
@@ -575,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_full_kernel(const SampleAr
     float mx = -INFINITY;
     Running run;
     run.clear();
-    const bool vec = (reinterpret_cast<uintptr_t>(prow + sp.head) & 15) == 0;
+    const bool vec = (reinterpret_cast<uintptr_t>(prow + sp.head) % (4 * kVec)) == 0;
     auto ragged = [&](int x0, int x1) {
         for (int x = x0 + lane; x < x1; x += 32) {
             const float v = L::wide(__ldg(row.g + x));
@@ -588,41 +628,37 @@ __global__ void __launch_bounds__(kThreads, 2) sample_full_kernel(const SampleAr
     };
     ragged(sg.head0, sg.head1);
     {
-        constexpr int kU = 32 / kVec;  // 4 or 8 loads in flight a thread
-        for (int x = sg.v0 + lane; x < sg.v1; x += 32 * kU) {
-            uint4 q[kU];
+        // two vectors a step, the next step's on their way meanwhile
+        uint4 q[2], next[2];
+        auto fetch = [&](int x, uint4 (&v)[2]) {
 #pragma unroll
-            for (int u = 0; u < kU; ++u)
-                if (x + 32 * u < sg.v1) q[u] = __ldg(gv + x + 32 * u);
+            for (int u = 0; u < 2; ++u)
+                if (x + 32 * u < sg.v1) v[u] = __ldcs(gv + x + 32 * u);
+        };
+        fetch(sg.v0 + lane, q);
+        for (int x = sg.v0 + lane; x < sg.v1; x += 64) {
+            fetch(x + 64, next);
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
+            for (int u = 0; u < 2; ++u) {
                 if (x + 32 * u >= sg.v1) break;
                 const Raw *e = reinterpret_cast<const Raw *>(&q[u]);
                 float *out = prow + sp.head + (long)(x + 32 * u) * kVec;
+                float w[kVec];
 #pragma unroll
-                for (int k = 0; k < kVec; k += 4) {
-                    V2 h[2], l[2];
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const float v0 = L::wide(e[k + 2 * p]), v1 = L::wide(e[k + 2 * p + 1]);
-                        mx = max3f(mx, v0, v1);
-                        weight_ff<V2, false>(V2{f2_pack(v0, v1)}, rs, sm.tab, h[p], l[p]);
-                        run.add(h[p], l[p]);
-                    }
-                    if (prow) {
-                        const float2 x0 = f2_unpack(h[0].a), x1 = f2_unpack(h[1].a);
-                        if (vec) {
-                            *reinterpret_cast<float4 *>(out + k) =
-                                make_float4(x0.x, x0.y, x1.x, x1.y);
-                        } else {
-                            out[k] = x0.x;
-                            out[k + 1] = x0.y;
-                            out[k + 2] = x1.x;
-                            out[k + 3] = x1.y;
-                        }
-                    }
+                for (int k = 0; k < kVec; k += 2) {
+                    const float v0 = L::wide(e[k]), v1 = L::wide(e[k + 1]);
+                    mx = max3f(mx, v0, v1);
+                    V2 h, l;
+                    weight_ff<V2, false>(V2{f2_pack(v0, v1)}, rs, sm.tab, h, l);
+                    run.add(h, l);
+                    const float2 f = f2_unpack(h.a);
+                    w[k] = f.x;
+                    w[k + 1] = f.y;
                 }
+                if (prow) store_vec<kVec, false>(out, w, vec);
             }
+            q[0] = next[0];
+            q[1] = next[1];
         }
     }
     ragged(sg.tail0, sg.tail1);
@@ -703,29 +739,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_full_kernel(const SampleAr
             for (int x = sg.head0 + lane; x < sg.head1; x += 32) prow[x] = prow[x] * f * inv;
             for (int x = sg.tail0 + lane; x < sg.tail1; x += 32) prow[x] = prow[x] * f * inv;
             if (vec) {
-                constexpr int kU = 4;
-                const int q0 = sg.v0 * (kVec / 4), q1 = sg.v1 * (kVec / 4);
-                float4 *out = reinterpret_cast<float4 *>(prow + sp.head);
-                // (a lane's quads: kVec / 4 neighbours of each of its vectors)
-                auto quad = [&](int j) {
-                    const int v = j / (kVec / 4), k = j % (kVec / 4);
-                    return (sg.v0 + v * 32 + lane) * (kVec / 4) + k;
-                };
-                const int n = ((sg.v1 - sg.v0 + 31) / 32) * (kVec / 4);
-                for (int j = 0; j < n; j += kU) {
-                    float4 w[kU];
+                constexpr int kU = 16 / kVec;
+                for (int x = sg.v0 + lane; x < sg.v1; x += 32 * kU) {
+                    float w[kU][kVec];
+#pragma unroll
+                    for (int u = 0; u < kU; ++u)
+                        if (x + 32 * u < sg.v1)
+                            load_vec<kVec>(prow + sp.head + (long)(x + 32 * u) * kVec, w[u]);
 #pragma unroll
                     for (int u = 0; u < kU; ++u) {
-                        const int x = quad(j + u);
-                        if (j + u < n && x >= q0 && x < q1) w[u] = out[x];
-                    }
+                        if (x + 32 * u >= sg.v1) break;
 #pragma unroll
-                    for (int u = 0; u < kU; ++u) {
-                        const int x = quad(j + u);
-                        if (!(j + u < n && x >= q0 && x < q1)) continue;
-                        const float2 x0 = f2_unpack((V2{f2_pack(w[u].x, w[u].y)} * f2 * i2).a);
-                        const float2 x1 = f2_unpack((V2{f2_pack(w[u].z, w[u].w)} * f2 * i2).a);
-                        __stcs(out + x, make_float4(x0.x, x0.y, x1.x, x1.y));
+                        for (int k = 0; k < kVec; k += 2) {
+                            const float2 y =
+                                f2_unpack((V2{f2_pack(w[u][k], w[u][k + 1])} * f2 * i2).a);
+                            w[u][k] = y.x;
+                            w[u][k + 1] = y.y;
+                        }
+                        store_vec<kVec, true>(prow + sp.head + (long)(x + 32 * u) * kVec, w[u], true);
                     }
                 }
             } else {
