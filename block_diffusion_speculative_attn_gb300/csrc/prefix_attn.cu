@@ -152,6 +152,17 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
         : "memory");
 }
 
+// One lane of the (converged) warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // 16 consecutive 32-bit columns of the thread's lane.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
@@ -371,78 +382,110 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
             }
         } else if (warp == C::kMma) {
             // ------------------------------------------------ MMA issuer
-            if (lane == 0) {
+            // The whole warp walks the schedule and one elected lane issues: an
+            // MMA takes its descriptors from uniform registers, which only code
+            // that the warp runs together keeps them in (a single lane's loop
+            // spent 125 cycles an MMA on moving them, twice what the MMA takes).
+            {
+                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+                const bool leader = elect_one();
                 constexpr uint32_t idesc_qk = idesc_bf16_f32(kPrefixRows, kBN, 0, 0);
                 constexpr uint32_t idesc_pv = idesc_bf16_f32(kPrefixRows, D, 0, 1);
-                long g = 0;             // key tiles
-                long gt[2] = {0, 0};    // S tiles of each row tile
-                int kt[2] = {0, 0};     // pieces of each row tile
+                uint32_t gt[2] = {0, 0};  // S tiles of each row tile
+                uint32_t kt[2] = {0, 0};  // pieces of each row tile
                 bool ok = true;
                 auto wait = [&](int i, uint32_t parity) {
                     ok = ok && mbar_wait(bar(i), parity & 1, abort_flag, prm.dev_status);
+                    ok = __all_sync(0xffffffffu, ok);
                 };
-                auto issue_s = [&](int t, long gk) {
-                    const int ks = (int)(gk % C::NK);
+                // descriptors of the first operand tiles; another tile, or K step, is an
+                // addition to the address field (an MMA takes the tensor cores 64
+                // cycles, so its issue has to stay well below that)
+                const uint64_t dq = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
+                const uint64_t dk = smem_desc_sw128(sbase + C::kOffK, 16, 1024);
+                const uint64_t dv = smem_desc_sw128(sbase + C::kOffV, C::kSlab, 1024);
+                auto issue_s = [&](int t, int ks) {
+                    const uint64_t q = dq + (uint32_t)(t * (C::kTile >> 4));
+                    const uint64_t k = dk + (uint32_t)(ks * (C::kTile >> 4));
+                    const uint32_t d = tm + kS + t * 128;
+                    if (!leader) return;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        umma_bf16(tmem + kS + t * 128,
-                                  smem_desc_sw128(sbase + C::kOffQ + t * C::kTile +
-                                                      (kk >> 2) * C::kSlab + (kk & 3) * 32,
-                                                  16, 1024),
-                                  smem_desc_sw128(sbase + C::kOffK + ks * C::kTile +
-                                                      (kk >> 2) * C::kSlab + (kk & 3) * 32,
-                                                  16, 1024),
-                                  idesc_qk, kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * C::kSlab + (kk & 3) * 32) >> 4;
+                        umma_bf16(d, q + off, k + off, idesc_qk, kk > 0 ? 1u : 0u);
+                    }
                     umma_commit(bar(C::SF + t));
                 };
-                auto issue_pv = [&](int t, long gv, bool first) {
-                    const int vs = (int)(gv % C::NV);
+                auto issue_pv = [&](int t, int vs, bool first) {
+                    const uint64_t v = dv + (uint32_t)(vs * (C::kTile >> 4));
+                    const uint32_t d = tm + kO + t * 128;
+                    if (!leader) return;
 #pragma unroll
                     for (int kk = 0; kk < kBN / 16; ++kk)
-                        umma_bf16_ts(tmem + kO + t * 128, tmem + kS + t * 128 + kk * 8,
-                                     smem_desc_sw128(sbase + C::kOffV + vs * C::kTile +
-                                                         kk * 16 * 128,
-                                                     C::kSlab, 1024),
+                        umma_bf16_ts(d, tm + kS + t * 128 + kk * 8, v + (uint32_t)(kk * 128),
                                      idesc_pv, (first && kk == 0) ? 0u : 1u);
                 };
+                // ring positions and their phases
+                int ks = 0, vs = 0;
+                uint32_t kph = 0, vph = 0;
                 while (ok && walk.next(prm, c1, pc)) {
                     const int nact = prm.x.npt < pc.ntok ? 2 : 1;
                     const int n = pc.e - pc.a;
                     // first S of each row tile
-                    wait(C::KF + (int)(g % C::NK), (uint32_t)(g / C::NK));
-                    for (int t = 0; ok && t < nact; ++t) {
+                    wait(C::KF + ks, kph);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (!ok || t >= nact) break;
                         wait(C::QF + t, kt[t]);
                         tc_fence_after();
-                        if (ok) issue_s(t, g);
-                        if (ok && n == 1) umma_commit(bar(C::QE + t));
+                        if (ok) issue_s(t, ks);
+                        if (ok && n == 1 && leader) umma_commit(bar(C::QE + t));
                     }
                     if (!ok) break;
-                    umma_commit(bar(C::KE + (int)(g % C::NK)));
-                    for (int j = 0; ok && j < n; ++j, ++g) {
-                        const long gn = g + 1;  // the next tile's K
-                        if (j + 1 < n) wait(C::KF + (int)(gn % C::NK), (uint32_t)(gn / C::NK));
-                        wait(C::VF + (int)(g % C::NV), (uint32_t)(g / C::NV));
-                        for (int t = 0; ok && t < nact; ++t) {
+                    if (leader) umma_commit(bar(C::KE + ks));
+                    if (++ks == C::NK) {
+                        ks = 0;
+                        kph ^= 1;
+                    }
+                    for (int j = 0; ok && j < n; ++j) {
+                        const bool more = j + 1 < n;
+                        wait(C::VF + vs, vph);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (!ok || t >= nact) break;
                             if (j == 0 && kt[t] > 0) wait(C::OE + t, kt[t] - 1);
-                            wait(C::PF + t, (uint32_t)gt[t]);
+                            wait(C::PF + t, gt[t]);
                             if (!ok) break;
                             ++gt[t];
                             tc_fence_after();
-                            issue_pv(t, g, j == 0);
-                            if (j + 1 < n) {
-                                issue_s(t, g + 1);
-                                if (j + 2 == n) umma_commit(bar(C::QE + t));
-                            } else {
+                            issue_pv(t, vs, j == 0);
+                            if (more) {
+                                if (t == 0) wait(C::KF + ks, kph);
+                                if (!ok) break;
+                                issue_s(t, ks);
+                                if (j + 2 == n && leader) umma_commit(bar(C::QE + t));
+                            } else if (leader) {
                                 umma_commit(bar(C::OF + t));
                             }
                         }
                         if (!ok) break;
-                        umma_commit(bar(C::VE + (int)(g % C::NV)));
-                        if (j + 1 < n) umma_commit(bar(C::KE + (int)((g + 1) % C::NK)));
+                        if (leader) umma_commit(bar(C::VE + vs));
+                        if (++vs == C::NV) {
+                            vs = 0;
+                            vph ^= 1;
+                        }
+                        if (more) {
+                            if (leader) umma_commit(bar(C::KE + ks));
+                            if (++ks == C::NK) {
+                                ks = 0;
+                                kph ^= 1;
+                            }
+                        }
                     }
-                    for (int t = 0; t < nact; ++t) ++kt[t];
+                    ++kt[0];
+                    if (nact == 2) ++kt[1];
                 }
-                umma_commit(bar(C::DR));
+                if (leader) umma_commit(bar(C::DR));
                 mbar_wait_drain(bar(C::DR), 0);
             }
         }

@@ -756,7 +756,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_full_kernel(const SampleAr
                             w[u][k] = y.x;
                             w[u][k + 1] = y.y;
                         }
-                        store_vec<kVec, true>(prow + sp.head + (long)(x + 32 * u) * kVec, w[u], true);
+                        store_vec<kVec, true>(prow + sp.head + (long)(x + 32 * u) * kVec, w[u],
+                                              true);
                     }
                 }
             } else {
