@@ -17,9 +17,10 @@
 // and persistent CTAs take equal cost ranges.  A piece leaves its rows' o / l
 // and log2-sum-exp in fp32.
 //
-// Inside a CTA (12 warps, one idle): warps 0-3 and 4-7 are the softmax of the two row
-// tiles, one thread a row; then a K producer (also Q), an MMA issuer and a V
-// producer.  A row tile's S (128 columns of TMEM) is read by its softmax, which
+// Inside a CTA (12 warps): warps 0-3 and 4-7 are the softmax of the two row
+// tiles, one thread a row; then a K producer (also Q), a V producer and an MMA
+// issuer for each row tile (one issuer for both spent more time on its waits,
+// commits and descriptors than the tensor cores on the MMAs).  A row tile's S (128 columns of TMEM) is read by its softmax, which
 // writes P as bf16 over it; PV takes P from TMEM.  The two tiles alternate on
 // the tensor cores -- while one tile's PV and next S run (1024 cycles at D =
 // 128), the other's softmax runs on the ALUs -- and share every K and V tile in
@@ -58,15 +59,15 @@ struct PCfg {
     static constexpr int VF = KE + NK;
     static constexpr int VE = VF + NV;
     static constexpr int SF = VE + NV;   // 2: S of a row tile written (PV before it done)
-    static constexpr int PF = SF + 2;    // 2: P written, O rescaled
-    static constexpr int OF = PF + 2;    // 2: last PV of the piece done
+    static constexpr int PF = SF + 2;    // 2 x 2: half of P written (and O rescaled)
+    static constexpr int OF = PF + 4;    // 2: last PV of the piece done
     static constexpr int OE = OF + 2;    // 2: O read by the epilogue
-    static constexpr int DR = OE + 2;    // drain
-    static constexpr int kNumBars = DR + 1;
+    static constexpr int DR = OE + 2;    // 2: drain
+    static constexpr int kNumBars = DR + 2;
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
     static constexpr int kSmem = kOffMisc + 256 + 1024;
-    static constexpr int kProdK = 8, kMma = 9, kProdV = 10;
-    // (a twelfth, idle warp completes the third warpgroup)
+    // a K producer (also Q), an MMA issuer for each row tile, a V producer
+    static constexpr int kProdK = 8, kMma0 = 9, kProdV = 10, kMma1 = 11;
     static constexpr int kThreads = 12 * 32;
     // Registers a thread: 168 at launch (12 warps of 65536 / 384), moved from
     // the producers' warpgroup to the softmax ones, whose 128 scores a thread
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     // TMEM columns: S of row tile t at 128 t (P over its first 64), O at 256 + 128 t
     constexpr uint32_t kS = 0, kO = 256;
 
-    if (warp == C::kMma) {
+    if (warp == C::kMma0) {
         tmem_alloc(smem_u32(&sch->tmem), 512);
         tmem_relinquish();
     }
@@ -200,19 +201,21 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
             mbar_init(bar(C::QF + t), 1);
             mbar_init(bar(C::QE + t), 1);
             mbar_init(bar(C::SF + t), 1);
-            mbar_init(bar(C::PF + t), 4);
+            mbar_init(bar(C::PF + 2 * t), 4);
+            mbar_init(bar(C::PF + 2 * t + 1), 4);
             mbar_init(bar(C::OF + t), 1);
             mbar_init(bar(C::OE + t), 4);
         }
         for (int k = 0; k < C::NK; ++k) {
             mbar_init(bar(C::KF + k), 1);
-            mbar_init(bar(C::KE + k), 1);
+            mbar_init(bar(C::KE + k), 2);
         }
         for (int k = 0; k < C::NV; ++k) {
             mbar_init(bar(C::VF + k), 1);
-            mbar_init(bar(C::VE + k), 1);
+            mbar_init(bar(C::VE + k), 2);
         }
         mbar_init(bar(C::DR), 1);
+        mbar_init(bar(C::DR + 1), 1);
         *abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -329,8 +332,9 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                 bool ok = true;
                 while (ok && walk.next(prm, c1, pc)) {
                     if (is_k) {
-                        for (int t = 0; ok && t < 2; ++t) {
-                            if (t * prm.x.npt >= pc.ntok) continue;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (!ok || t * prm.x.npt >= pc.ntok) break;
                             if (kq[t] > 0)
                                 ok = mbar_wait(bar(C::QE + t), (kq[t] - 1) & 1, abort_flag,
                                                prm.dev_status);
@@ -375,118 +379,122 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                 }
                 // Drain: the last load issued into each buffer has landed.
                 if (is_k)
+#pragma unroll
                     for (int t = 0; t < 2; ++t)
                         if (kq[t] > 0) mbar_wait_drain(bar(C::QF + t), (kq[t] - 1) & 1);
                 for (long i = max(0L, g - NR); i < g; ++i)
                     mbar_wait_drain(bar(FULL + (int)(i % NR)), (uint32_t)((i / NR) & 1));
             }
-        } else if (warp == C::kMma) {
-            // ------------------------------------------------ MMA issuer
+        } else {
+            // ------------------------------------------------ MMA issuers, one a row tile
             // The whole warp walks the schedule and one elected lane issues: an
             // MMA takes its descriptors from uniform registers, which only code
-            // that the warp runs together keeps them in (a single lane's loop
-            // spent 125 cycles an MMA on moving them, twice what the MMA takes).
+            // that the warp runs together keeps them in.
             {
-                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+                const int t = warp == C::kMma0 ? 0 : 1;
+                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + t * 128;
                 const bool leader = elect_one();
                 constexpr uint32_t idesc_qk = idesc_bf16_f32(kPrefixRows, kBN, 0, 0);
                 constexpr uint32_t idesc_pv = idesc_bf16_f32(kPrefixRows, D, 0, 1);
-                uint32_t gt[2] = {0, 0};  // S tiles of each row tile
-                uint32_t kt[2] = {0, 0};  // pieces of each row tile
+                uint32_t gt = 0, kt = 0;  // S tiles and pieces of this row tile
                 bool ok = true;
                 auto wait = [&](int i, uint32_t parity) {
                     ok = ok && mbar_wait(bar(i), parity & 1, abort_flag, prm.dev_status);
                     ok = __all_sync(0xffffffffu, ok);
                 };
+                auto commit = [&](int i) {
+                    if (leader) umma_commit(bar(i));
+                };
                 // descriptors of the first operand tiles; another tile, or K step, is an
-                // addition to the address field (an MMA takes the tensor cores 64
-                // cycles, so its issue has to stay well below that)
-                const uint64_t dq = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
+                // addition to the address field
+                const uint64_t dq = smem_desc_sw128(sbase + C::kOffQ + t * C::kTile, 16, 1024);
                 const uint64_t dk = smem_desc_sw128(sbase + C::kOffK, 16, 1024);
                 const uint64_t dv = smem_desc_sw128(sbase + C::kOffV, C::kSlab, 1024);
-                auto issue_s = [&](int t, int ks) {
-                    const uint64_t q = dq + (uint32_t)(t * (C::kTile >> 4));
+                auto issue_s = [&](int ks) {
                     const uint64_t k = dk + (uint32_t)(ks * (C::kTile >> 4));
-                    const uint32_t d = tm + kS + t * 128;
                     if (!leader) return;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = ((kk >> 2) * C::kSlab + (kk & 3) * 32) >> 4;
-                        umma_bf16(d, q + off, k + off, idesc_qk, kk > 0 ? 1u : 0u);
+                        umma_bf16(tm + kS, dq + off, k + off, idesc_qk, kk > 0 ? 1u : 0u);
                     }
                     umma_commit(bar(C::SF + t));
                 };
-                auto issue_pv = [&](int t, int vs, bool first) {
+                auto issue_pv = [&](int vs, int part, bool first) {  // keys 64 part ..
                     const uint64_t v = dv + (uint32_t)(vs * (C::kTile >> 4));
-                    const uint32_t d = tm + kO + t * 128;
                     if (!leader) return;
 #pragma unroll
-                    for (int kk = 0; kk < kBN / 16; ++kk)
-                        umma_bf16_ts(d, tm + kS + t * 128 + kk * 8, v + (uint32_t)(kk * 128),
-                                     idesc_pv, (first && kk == 0) ? 0u : 1u);
+                    for (int k4 = 0; k4 < 4; ++k4) {
+                        const int kk = part * 4 + k4;
+                        umma_bf16_ts(tm + kO, tm + kS + kk * 8, v + (uint32_t)(kk * 128), idesc_pv,
+                                     (first && k4 == 0) ? 0u : 1u);
+                    }
                 };
                 // ring positions and their phases
                 int ks = 0, vs = 0;
                 uint32_t kph = 0, vph = 0;
-                while (ok && walk.next(prm, c1, pc)) {
-                    const int nact = prm.x.npt < pc.ntok ? 2 : 1;
-                    const int n = pc.e - pc.a;
-                    // first S of each row tile
-                    wait(C::KF + ks, kph);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (!ok || t >= nact) break;
-                        wait(C::QF + t, kt[t]);
-                        tc_fence_after();
-                        if (ok) issue_s(t, ks);
-                        if (ok && n == 1 && leader) umma_commit(bar(C::QE + t));
-                    }
-                    if (!ok) break;
-                    if (leader) umma_commit(bar(C::KE + ks));
+                auto next_k = [&] {
+                    commit(C::KE + ks);
                     if (++ks == C::NK) {
                         ks = 0;
                         kph ^= 1;
                     }
-                    for (int j = 0; ok && j < n; ++j) {
+                };
+                auto next_v = [&] {
+                    commit(C::VE + vs);
+                    if (++vs == C::NV) {
+                        vs = 0;
+                        vph ^= 1;
+                    }
+                };
+                while (ok && walk.next(prm, c1, pc)) {
+                    const int n = pc.e - pc.a;
+                    if (t * prm.x.npt >= pc.ntok) {
+                        // no tokens in this row tile: its share of the rings' releases
+                        for (int j = 0; ok && j < n; ++j) {
+                            wait(C::KF + ks, kph);
+                            if (ok) next_k();
+                            wait(C::VF + vs, vph);
+                            if (ok) next_v();
+                        }
+                        continue;
+                    }
+                    // the first S
+                    wait(C::KF + ks, kph);
+                    wait(C::QF + t, kt);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_s(ks);
+                    if (n == 1) commit(C::QE + t);
+                    next_k();
+                    for (int j = 0; j < n; ++j) {
                         const bool more = j + 1 < n;
                         wait(C::VF + vs, vph);
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (!ok || t >= nact) break;
-                            if (j == 0 && kt[t] > 0) wait(C::OE + t, kt[t] - 1);
-                            wait(C::PF + t, gt[t]);
-                            if (!ok) break;
-                            ++gt[t];
-                            tc_fence_after();
-                            issue_pv(t, vs, j == 0);
-                            if (more) {
-                                if (t == 0) wait(C::KF + ks, kph);
-                                if (!ok) break;
-                                issue_s(t, ks);
-                                if (j + 2 == n && leader) umma_commit(bar(C::QE + t));
-                            } else if (leader) {
-                                umma_commit(bar(C::OF + t));
-                            }
-                        }
+                        if (j == 0 && kt > 0) wait(C::OE + t, kt - 1);
+                        wait(C::PF + 2 * t, gt);
                         if (!ok) break;
-                        if (leader) umma_commit(bar(C::VE + vs));
-                        if (++vs == C::NV) {
-                            vs = 0;
-                            vph ^= 1;
-                        }
+                        tc_fence_after();
+                        issue_pv(vs, 0, j == 0);
+                        if (more) wait(C::KF + ks, kph);
+                        wait(C::PF + 2 * t + 1, gt);
+                        if (!ok) break;
+                        ++gt;
+                        tc_fence_after();
+                        issue_pv(vs, 1, false);
                         if (more) {
-                            if (leader) umma_commit(bar(C::KE + ks));
-                            if (++ks == C::NK) {
-                                ks = 0;
-                                kph ^= 1;
-                            }
+                            issue_s(ks);
+                            if (j + 2 == n) commit(C::QE + t);
+                            next_v();
+                            next_k();
+                        } else {
+                            commit(C::OF + t);
+                            next_v();
                         }
                     }
-                    ++kt[0];
-                    if (nact == 2) ++kt[1];
+                    ++kt;
                 }
-                if (leader) umma_commit(bar(C::DR));
-                mbar_wait_drain(bar(C::DR), 0);
+                commit(C::DR + t);
+                mbar_wait_drain(bar(C::DR + t), 0);
             }
         }
     } else {
@@ -574,11 +582,13 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                         lacc[q & 1] = f2_add(lacc[q & 1], f2_pack(p0, p1));
                     }
                     tmem_st16(s_addr + c * 16, pk);
+                    if (c & 1) {  // half of P: its PV may start
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::PF + 2 * t + (c >> 1)));
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::PF + t));
             }
             if (!ok) break;
             // ---- end of the piece: o / l and the log2-sum-exp
@@ -626,7 +636,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (warp == C::kMma) {
+    if (warp == C::kMma0) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
