@@ -20,7 +20,8 @@
 // Inside a CTA (12 warps): warps 0-3 and 4-7 are the softmax of the two row
 // tiles, one thread a row; then a K producer (also Q), a V producer and an MMA
 // issuer for each row tile (one issuer for both spent more time on its waits,
-// commits and descriptors than the tensor cores on the MMAs).  A row tile's S (128 columns of TMEM) is read by its softmax, which
+// commits and descriptors than the tensor cores on the MMAs).  A row tile's S
+// (128 columns of TMEM) is read by its softmax, which
 // writes P as bf16 over it; PV takes P from TMEM.  The two tiles alternate on
 // the tensor cores -- while one tile's PV and next S run (1024 cycles at D =
 // 128), the other's softmax runs on the ALUs -- and share every K and V tile in
@@ -29,7 +30,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
+#include <limits.h>
 
 #include "attn_common.cuh"
 #include "attn_prefix.cuh"
@@ -67,7 +68,7 @@ struct PCfg {
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
     static constexpr int kSmem = kOffMisc + 256 + 1024;
     // a K producer (also Q), an MMA issuer for each row tile, a V producer
-    static constexpr int kProdK = 8, kMma0 = 9, kProdV = 10, kMma1 = 11;
+    static constexpr int kProdK = 8, kMma0 = 9, kProdV = 10;  // (kMma1 = 11)
     static constexpr int kThreads = 12 * 32;
     // Registers a thread: 168 at launch (12 warps of 65536 / 384), moved from
     // the producers' warpgroup to the softmax ones, whose 128 scores a thread
