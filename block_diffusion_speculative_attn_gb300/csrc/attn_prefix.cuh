@@ -5,12 +5,14 @@
 // Group g holds requests [off[g], off[g + 1]) and shares its first
 // P' = floor(P_g / 128) * 128 keys.  Its query rows of one KV head, (token, head
 // of the group) in token order, are cut into tiles of npt whole tokens (at most
-// kPrefixRows rows); a unit is two tiles over all P' keys.  Units are numbered
-// (group, KV head, tile pair); each is charged kPrefixUnitCost virtual tiles and
-// its P' / 128 real ones, and CTA b of S takes the cost range [b Wc / S,
-// (b + 1) Wc / S).  The piece that holds a unit's first tile goes to per-row
-// buffers (a row has one such piece); any other piece is the first of its CTA
-// and goes to that CTA's slot.
+// kPrefixRows rows), two tiles to a pair.  CTAs work in teams of T (1 or
+// 2, a cluster): a team takes T pairs of one KV head over the same keys, a pair a
+// member.  A unit is a team's T pairs over all P'
+// keys, numbered (group, KV head, T pairs); each is charged kPrefixUnitCost
+// virtual tiles and its P' / 128 real ones, and team b of S takes the cost range
+// [b Wc / S, (b + 1) Wc / S).  The piece that holds a unit's first tile goes to
+// per-row buffers (a row has one such piece); any other piece is the first of its
+// CTA and goes to that CTA's slot.
 #pragma once
 
 #include "attn_common.cuh"
@@ -22,9 +24,11 @@ namespace {
 constexpr int kPrefixRows = 128;     // query rows of a tile
 // Virtual tiles a unit switch is charged (a Q load, an epilogue).
 constexpr int kPrefixUnitCost = 2;
-// A CTA takes at least this cost: below it the pieces' partials and their merge
+// A team takes at least this cost: below it the pieces' partials and their merge
 // cost more than the CTAs gain.
 constexpr int kPrefixMinCost = 6;
+// The prefix kernel's CTAs: whole clusters of two.
+__host__ __device__ constexpr int prefix_grid(int ctas) { return ctas < 2 ? 2 : ctas & ~1; }
 
 // The keys of request r (length L) its group shares, in whole tiles; g its
 // group, or -1 (and 0 keys) when the groups do not place it or its prefix is
@@ -58,25 +62,31 @@ __device__ __forceinline__ int group_pairs(const PrefixParams &x, int tokens) {
     return (tokens + 2 * x.npt - 1) / (2 * x.npt);
 }
 
+// Units of a group and KV head, by teams of T.
+__device__ __forceinline__ int group_units(const PrefixParams &x, int tokens, int T) {
+    return (group_pairs(x, tokens) + T - 1) / T;
+}
+
 __device__ __forceinline__ long long prefix_range_start(long long b, long long Wc, long long S) {
     return b * Wc / S;
 }
-// The CTA whose cost range holds cost c.
-__device__ __forceinline__ int prefix_cta_of(long long c, long long Wc, long long S) {
+// The team whose cost range holds cost c.
+__device__ __forceinline__ int prefix_team_of(long long c, long long Wc, long long S) {
     return (int)(((c + 1) * S - 1) / Wc);
 }
 
 // The unit that holds block row i_blk of request r, KV head h (valid once the
 // prefix grid has finished).
 struct PrefixUnit {
-    long long cost, Wc, S;  // the unit's cost offset; the schedule's total and CTAs
+    long long cost, Wc, S;  // the unit's cost offset; the schedule's total and teams
                             // (S < 0: the group offsets are wrong)
     int nt;                 // its tiles (0: no shared prefix)
+    int T, member;          // CTAs a team, and the one with this row's pair
     int row;                // the block row's first row within the unit's 2 * kPrefixRows
 };
 __device__ __forceinline__ PrefixUnit prefix_unit(const PrefixParams &x, int g, int r, int i_blk,
                                                   int B, int G, int Hkv, int h) {
-    PrefixUnit u{0, 1, __ldcg(x.head + 1), 0, 0};
+    PrefixUnit u{0, 1, __ldcg(x.head + 1), 0, 1, 0, 0};
     if (g < 0 || u.S < 0) return u;
     int r0, tokens;
     group_shape(x, g, B, r0, tokens, u.nt);
@@ -85,8 +95,10 @@ __device__ __forceinline__ PrefixUnit prefix_unit(const PrefixParams &x, int g, 
     const int tile = t / x.npt, pair = tile >> 1;
     u.row = (tile & 1) * kPrefixRows + (t % x.npt) * G;
     u.Wc = __ldcg(x.head);
-    u.cost = __ldcg(x.goff + g) +
-             ((long long)h * group_pairs(x, tokens) + pair) * (kPrefixUnitCost + u.nt);
+    u.T = (int)__ldcg(x.head + 2);
+    u.member = pair % u.T;
+    u.cost = __ldcg(x.goff + g) + ((long long)h * group_units(x, tokens, u.T) + pair / u.T) *
+                                      (kPrefixUnitCost + u.nt);
     return u;
 }
 

@@ -45,7 +45,7 @@ struct PrefixParams {
     const int32_t *group_offsets, *prefix_lens;  // [ng + 1], [ng]
     int ng, bs;
     int npt;                    // whole tokens in a 128-row tile
-    long long *head;            // {total cost, CTAs}, written by the prefix kernel
+    long long *head;            // {total cost, teams, CTAs a team}, by the prefix kernel
     long long *goff;            // [ng] cost offset of each group's first unit
     float *row_lse, *row_o;     // [bs * B * Hq], [.., D]: first pieces
     float *slot_lse, *slot_o;   // [grid, 256], [.., D]: the other pieces, one slot a CTA

@@ -1110,12 +1110,13 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                 bad = bad || pu.S < 0;
                 if (pu.nt > 0 && valid_row && !bad) {
                     const long long c0 = pu.cost + kPrefixUnitCost;
-                    const int q0 = prefix_cta_of(c0, pu.Wc, pu.S);
-                    const int q1 = prefix_cta_of(c0 + pu.nt - 1, pu.Wc, pu.S);
+                    const int q0 = prefix_team_of(c0, pu.Wc, pu.S);
+                    const int q1 = prefix_team_of(c0 + pu.nt - 1, pu.Wc, pu.S);
                     for (int q = q0; q <= q1; ++q) {
                         const long src =
                             q == q0 ? e.orow
-                                    : (long)q * 2 * kPrefixRows + pu.row + row % G;
+                                    : ((long)q * pu.T + pu.member) * 2 * kPrefixRows +
+                                          pu.row + row % G;
                         const float ls =
                             __ldcg((q == q0 ? prm.pfx.row_lse : prm.pfx.slot_lse) + src);
                         if (ls == INFINITY) bad = true;  // a page outside the pool
@@ -1883,13 +1884,14 @@ PrefixPlan prefix_plan(int bs, int B, int Hq, int Hkv, int D, int num_groups, in
     PrefixPlan p;
     p.attn = attn_plan(bs, B, Hq, Hkv, D, 0, num_sms);
     size_t off = p.attn.workspace;
-    const size_t rows = (size_t)bs * B * Hq, slots = (size_t)p.attn.grid * 2 * kPrefixRows;
+    const size_t rows = (size_t)bs * B * Hq;
+    const size_t slots = (size_t)prefix_grid(p.attn.grid) * 2 * kPrefixRows;
     auto take = [&](size_t bytes) {
         const size_t at = off;
         off += align256(bytes);
         return at;
     };
-    p.off_head = take(2 * sizeof(int64_t));
+    p.off_head = take(3 * sizeof(int64_t));
     p.off_goff = take((size_t)num_groups * sizeof(int64_t));
     p.off_row_lse = take(rows * sizeof(float));
     p.off_slot_lse = take(slots * sizeof(float));

@@ -17,6 +17,11 @@
 // and persistent CTAs take equal cost ranges.  A piece leaves its rows' o / l
 // and log2-sum-exp in fp32.
 //
+// A team of two CTAs is a thread-block cluster whose members load half of every K
+// and V tile each and multicast it to both: the keys cross from L2 once a team
+// (with a load a CTA, 64 KB a tile, the SMs' 7.1 TB/s together bound the tile
+// loop).
+//
 // Inside a CTA (12 warps): warps 0-3 and 4-7 are the softmax of the two row
 // tiles, one thread a row; then a K producer (also Q), a V producer and an MMA
 // issuer for each row tile (one issuer for both spent more time on its waits,
@@ -64,9 +69,10 @@ struct PCfg {
     static constexpr int OF = PF + 4;    // 2: last PV of the piece done
     static constexpr int OE = OF + 2;    // 2: O read by the epilogue
     static constexpr int DR = OE + 2;    // 2: drain
-    static constexpr int kNumBars = DR + 2;
+    static constexpr int TK = DR + 2;    // 2: the other row tile's exponentials are done
+    static constexpr int kNumBars = TK + 2;
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-    static constexpr int kSmem = kOffMisc + 256 + 1024;
+    static constexpr int kSmem = kOffMisc + 448 + 1024;
     // a K producer (also Q), an MMA issuer for each row tile, a V producer
     static constexpr int kProdK = 8, kMma0 = 9, kProdV = 10;  // (kMma1 = 11)
     static constexpr int kThreads = 12 * 32;
@@ -80,13 +86,13 @@ struct PCfg {
 struct PSched {
     uint32_t tmem;
     int abort;
-    long long wsum[12];
-    long long Wc, S;       // total cost, CTAs that take part
+    long long wsum[12], wsum2[2][12];
+    int T, member;         // CTAs a team, this one's place
     long long c0, c1;      // this CTA's cost range
     long long gbase;       // cost offset of the group holding c0
     int g0;
 };
-static_assert(sizeof(PSched) <= 256, "the schedule state has 256 bytes");
+static_assert(sizeof(PSched) <= 448, "the schedule state has 448 bytes");
 
 struct PParams {
     PrefixParams x;
@@ -106,17 +112,18 @@ struct PPiece {
 struct PWalk {
     int g;
     long long base;       // cost offset of group g
-    int r0, tokens, nt, pairs;
+    int r0, tokens, nt, units;
+    int T, member;
     long long c;          // next cost
     __device__ void load(const PParams &p) {
         group_shape(p.x, g, p.B, r0, tokens, nt);
-        pairs = group_pairs(p.x, tokens);
+        units = group_units(p.x, tokens, T);
     }
     // The next piece, or false at the end of the range.
     __device__ bool next(const PParams &p, long long c1, PPiece &pc) {
         while (c < c1) {
             const long long span = kPrefixUnitCost + nt;
-            const long long gcost = nt > 0 ? span * p.Hkv * pairs : 0;
+            const long long gcost = nt > 0 ? span * p.Hkv * units : 0;
             if (c >= base + gcost) {
                 if (++g >= p.x.ng) return false;
                 base += gcost;
@@ -129,11 +136,12 @@ struct PWalk {
             const int a = (int)max(0LL, lo - kPrefixUnitCost);
             const int e = (int)max(0LL, hi - kPrefixUnitCost);
             if (a >= e) continue;
-            const int pair = (int)(u % pairs);
-            pc.h = (int)(u / pairs);
+            const int pair = (int)(u % units) * T + member;
+            pc.h = (int)(u / units);
             pc.r0 = r0;
             pc.tok0 = r0 * p.B + pair * 2 * p.x.npt;
             pc.ntok = tokens - pair * 2 * p.x.npt;
+            // (no tokens left for this member: it still loads its half of the keys)
             pc.a = a;
             pc.e = e;
             pc.nt = nt;
@@ -152,6 +160,30 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// A tile load to the same place in both CTAs of the cluster, completing on the
+// barrier at the same place in each.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap, int32_t x,
+                                                 int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "h"((uint16_t)3)
+        : "memory");
+}
+// umma_commit to the barrier at the same place in both CTAs of the cluster.
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void pair_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // One lane of the (converged) warp, always the same.
@@ -177,7 +209,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 }
 
 template <int D>
-__global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PParams prm) {
@@ -209,14 +241,16 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
         }
         for (int k = 0; k < C::NK; ++k) {
             mbar_init(bar(C::KF + k), 1);
-            mbar_init(bar(C::KE + k), 2);
+            mbar_init(bar(C::KE + k), 4);
         }
         for (int k = 0; k < C::NV; ++k) {
             mbar_init(bar(C::VF + k), 1);
-            mbar_init(bar(C::VE + k), 2);
+            mbar_init(bar(C::VE + k), 4);
         }
         mbar_init(bar(C::DR), 1);
         mbar_init(bar(C::DR + 1), 1);
+        mbar_init(bar(C::TK), 4);
+        mbar_init(bar(C::TK + 1), 4);
         *abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -234,7 +268,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     }
     fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();
+    pair_sync();  // (both CTAs' barriers are set up before either is signalled)
     tc_fence_after();
     const uint32_t tmem = sch->tmem;
 
@@ -249,22 +283,43 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
         const int ng = prm.x.ng;
         const int per = (ng + C::kThreads - 1) / C::kThreads;
         const int i0 = min(ng, tid * per), i1 = min(ng, i0 + per);
-        auto cost = [&](int g) -> long long {
+        auto cost = [&](int g, int T) -> long long {
             int r0, tokens, nt;
             group_shape(prm.x, g, prm.B, r0, tokens, nt);
-            return nt > 0 ? (long long)(kPrefixUnitCost + nt) * prm.Hkv * group_pairs(prm.x, tokens)
+            return nt > 0 ? (long long)(kPrefixUnitCost + nt) * prm.Hkv *
+                                group_units(prm.x, tokens, T)
                           : 0;
         };
         // offsets that do not run up from 0 to bs place nothing: no work, and
         // the block attention writes zeros
         bool wrong = false;
-        long long sum = 0;
+        long long sum2[2] = {0, 0};  // costs by teams of 1 and of 2
         for (int g = i0; g < i1; ++g) {
-            sum += cost(g);
+            sum2[0] += cost(g, 1);
+            sum2[1] += cost(g, 2);
             const int o0 = __ldg(prm.x.group_offsets + g), o1 = __ldg(prm.x.group_offsets + g + 1);
             wrong |= o1 < o0 || (g == 0 && o0 != 0) || (g == ng - 1 && o1 != prm.x.bs);
         }
         wrong = __syncthreads_or(wrong);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            long long v = sum2[k];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == 0) sch->wsum2[k][warp] = v;
+        }
+        __syncthreads();
+        long long c1s = 0, c2s = 0;
+        for (int w = 0; w < C::kThreads / 32; ++w) {
+            c1s += sch->wsum2[0][w];
+            c2s += sch->wsum2[1][w];
+        }
+        // Teams of two unless the pairs they leave without a partner cost more
+        // than 1/16.
+        const int T = 2 * c2s <= c1s + c1s / 16 ? 2 : 1;
+        const long long Wc = T == 2 ? c2s : c1s;
+        long long sum = 0;
+        for (int g = i0; g < i1; ++g) sum += cost(g, T);
         long long inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -273,20 +328,17 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
         }
         if (lane == 31) sch->wsum[warp] = inc;
         __syncthreads();
-        long long wex = 0, Wc = 0;
-        for (int w = 0; w < C::kThreads / 32; ++w) {
-            if (w < warp) wex += sch->wsum[w];
-            Wc += sch->wsum[w];
-        }
-        const long long S = max(1LL, min((long long)gridDim.x, Wc / kPrefixMinCost));
-        const long long b = blockIdx.x;
+        long long wex = 0;
+        for (int w = 0; w < warp; ++w) wex += sch->wsum[w];
+        const long long S = max(1LL, min((long long)(gridDim.x / T), Wc / kPrefixMinCost));
+        const long long b = blockIdx.x / T;
         const bool mine = b < S && !wrong;
         const long long c0 = mine ? prefix_range_start(b, Wc, S) : Wc;
         const long long c1 = mine ? prefix_range_start(b + 1, Wc, S) : Wc;
         long long at = wex + inc - sum;
         for (int g = i0; g < i1; ++g) {
-            const long long cg = cost(g);
-            if (b == 0) prm.x.goff[g] = at;
+            const long long cg = cost(g, T);
+            if (blockIdx.x == 0) prm.x.goff[g] = at;
             if (at <= c0 && c0 < at + cg) {
                 sch->g0 = g;
                 sch->gbase = at;
@@ -296,9 +348,12 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
         if (tid == 0) {
             sch->c0 = c0;
             sch->c1 = c1;
-            if (b == 0) {
+            sch->T = T;
+            sch->member = blockIdx.x % T;
+            if (blockIdx.x == 0) {
                 prm.x.head[0] = Wc;
                 prm.x.head[1] = wrong ? -1 : S;
+                prm.x.head[2] = T;
                 if (wrong) report_status(prm.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
             }
         }
@@ -307,6 +362,8 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     const long long c1 = sch->c1;
     PWalk walk;
     walk.c = sch->c0;
+    walk.T = sch->T;
+    walk.member = sch->member;
     if (walk.c < c1) {
         walk.g = sch->g0;
         walk.base = sch->gbase;
@@ -326,7 +383,9 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                 const int EMPTY = is_k ? C::KE : C::VE;
                 const uint32_t dst0 = sbase + (is_k ? C::kOffK : C::kOffV);
                 const void *tmap = is_k ? (const void *)&tm_k : (const void *)&tm_v;
-                const int rows_box = prm.box_rows, nbox = kBN / rows_box;
+                const int rows_box = prm.box_rows;
+                // a team's members each load half of a tile, to both
+                const int nbox = kBN / walk.T / rows_box, half = walk.member * (kBN / 2);
                 const long ps = 1L << prm.log2_ps;
                 long g = 0;
                 int kq[2] = {0, 0};  // pieces each row tile took part in
@@ -357,7 +416,8 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
 #pragma unroll
                         for (int bx = 0; bx < kMaxBoxes; ++bx) {
                             if (bx >= nbox) break;
-                            const long t = t0 + (long)bx * rows_box, page = t >> prm.log2_ps;
+                            const long t = t0 + half + (long)bx * rows_box;
+                            const long page = t >> prm.log2_ps;
                             const int32_t id = page < prm.max_pages ? __ldg(bt + page) : -1;
                             slot[bx] = id >= 0 && id < prm.num_pages
                                            ? (int32_t)(id * ps + (t & (ps - 1)))
@@ -371,10 +431,16 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
 #pragma unroll
                         for (int bx = 0; bx < kMaxBoxes; ++bx) {
                             if (bx >= nbox) break;
-                            for (int c = 0; c < C::DH; ++c)
-                                tma_load_2d(
-                                    dst0 + st * C::kTile + c * C::kSlab + bx * rows_box * 128,
-                                    tmap, pc.h * D + c * 64, slot[bx], bar(FULL + st));
+                            for (int c = 0; c < C::DH; ++c) {
+                                const uint32_t dst = dst0 + st * C::kTile + c * C::kSlab +
+                                                     (half + bx * rows_box) * 128;
+                                if (walk.T == 2)
+                                    tma_load_2d_pair(dst, tmap, pc.h * D + c * 64, slot[bx],
+                                                     bar(FULL + st));
+                                else
+                                    tma_load_2d(dst, tmap, pc.h * D + c * 64, slot[bx],
+                                                bar(FULL + st));
+                            }
                         }
                     }
                 }
@@ -434,15 +500,27 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                 // ring positions and their phases
                 int ks = 0, vs = 0;
                 uint32_t kph = 0, vph = 0;
+                // a ring slot's release: to both members of a team, which each
+                // write the other's half; twice to itself without one (four
+                // arrivals free a slot)
+                auto release = [&](int i) {
+                    if (!leader) return;
+                    if (walk.T == 2) {
+                        umma_commit_pair(bar(i));
+                    } else {
+                        umma_commit(bar(i));
+                        umma_commit(bar(i));
+                    }
+                };
                 auto next_k = [&] {
-                    commit(C::KE + ks);
+                    release(C::KE + ks);
                     if (++ks == C::NK) {
                         ks = 0;
                         kph ^= 1;
                     }
                 };
                 auto next_v = [&] {
-                    commit(C::VE + vs);
+                    release(C::VE + vs);
                     if (++vs == C::NV) {
                         vs = 0;
                         vph ^= 1;
@@ -510,6 +588,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
         const int node = row / prm.G;                  // token within the tile
         long gs = 0;
         int k = 0;
+        uint32_t turn = 0;  // tiles that both row tiles took
         bool ok = true, first_piece = true;
         while (ok && walk.next(prm, c1, pc)) {
             const bool slot0 = first_piece && pc.a > 0;  // continues an earlier CTA's unit
@@ -527,6 +606,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                 }
                 bad = __any_sync(0xffffffffu, bad);
             }
+            const bool both = prm.x.npt < pc.ntok;       // both row tiles have tokens
             float m_used = -INFINITY;
             uint64_t lacc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
             for (int j = pc.a; j < pc.e; ++j, ++gs) {
@@ -539,11 +619,15 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                 for (int c = 0; c < 4; ++c)
                     tmem_ld32(s_addr + c * 32, *reinterpret_cast<float(*)[32]>(&sv[c * 32]));
                 tmem_wait_ld();
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float mx[8];
 #pragma unroll
-                for (int c = 0; c < 128; c += 2)
-                    mx[(c >> 1) & 3] = max3f(mx[(c >> 1) & 3], sv[c], sv[c + 1]);
-                const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                for (int c = 0; c < 8; ++c) mx[c] = sv[c];
+#pragma unroll
+                for (int c = 8; c < 128; c += 2)
+                    mx[(c >> 1) & 7] = max3f(mx[(c >> 1) & 7], sv[c], sv[c + 1]);
+                const float m_new = fmaxf(max3f(max3f(mx[0], mx[1], mx[2]), mx[3], mx[4]),
+                                          max3f(mx[5], mx[6], mx[7])) *
+                                    sl2;
                 float alpha = 1.f;
                 bool resc = false;
                 if (m_new > m_used + kRescaleLog2) {
@@ -569,6 +653,15 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                         }
                     }
                 }
+                // The row tiles' exponentials in turn: at the same time each takes
+                // twice as long (the special function unit is shared), and then
+                // both row tiles' MMAs come at once and nothing overlaps.
+                if (both && (t == 1 || turn > 0)) {
+                    ok = mbar_wait(bar(C::TK + t), (t == 1 ? turn : turn - 1) & 1, abort_flag,
+                                   prm.dev_status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                }
                 const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
                 const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(neg_m, neg_m);
 #pragma unroll
@@ -589,6 +682,10 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(C::PF + 2 * t + (c >> 1)));
                     }
+                }
+                if (both) {
+                    if (lane == 0) mbar_arrive(bar(C::TK + 1 - t));
+                    ++turn;
                 }
             }
             if (!ok) break;
@@ -636,7 +733,7 @@ __global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     }
 
     tc_fence_before();
-    __syncthreads();
+    pair_sync();  // (neither leaves while the other may still write or signal here)
     if (warp == C::kMma0) {
         __syncwarp();
         tc_fence_after();
@@ -666,7 +763,7 @@ int launch_partials(const AttnArgs &a, const PrefixParams &x, int grid, cudaStre
             CUDA_SUCCESS)
             return BDSA_CUDA_ERROR;
     }
-    const int box_rows = a.page_size < kBN ? a.page_size : kBN;
+    const int box_rows = a.page_size < kBN / 2 ? a.page_size : kBN / 2;
     for (int which = 0; which < 2; ++which) {
         cuuint64_t dims[2] = {(cuuint64_t)a.Hkv * D, (cuuint64_t)a.num_pages * a.page_size};
         cuuint64_t strides[1] = {(cuuint64_t)a.Hkv * D * 2};
@@ -697,8 +794,8 @@ int launch_partials(const AttnArgs &a, const PrefixParams &x, int grid, cudaStre
     if (cudaFuncSetAttribute(prefix_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmem) != cudaSuccess)
         return BDSA_CUDA_ERROR;
-    return launch_pdl(prefix_attn_kernel<D>, dim3(grid), dim3(C::kThreads), (size_t)C::kSmem,
-                      stream, tq, tk, tv, p) == cudaSuccess
+    return launch_pdl(prefix_attn_kernel<D>, dim3(prefix_grid(grid)), dim3(C::kThreads),
+                      (size_t)C::kSmem, stream, tq, tk, tv, p) == cudaSuccess
                ? BDSA_OK
                : BDSA_CUDA_ERROR;
 }
