@@ -70,36 +70,54 @@ __device__ __forceinline__ int group_units(const PrefixParams &x, int tokens, in
 __device__ __forceinline__ long long prefix_range_start(long long b, long long Wc, long long S) {
     return b * Wc / S;
 }
-// The team whose cost range holds cost c.
-__device__ __forceinline__ int prefix_team_of(long long c, long long Wc, long long S) {
-    return (int)(((c + 1) * S - 1) / Wc);
-}
 
-// The unit that holds block row i_blk of request r, KV head h (valid once the
-// prefix grid has finished).
-struct PrefixUnit {
-    long long cost, Wc, S;  // the unit's cost offset; the schedule's total and teams
-                            // (S < 0: the group offsets are wrong)
-    int nt;                 // its tiles (0: no shared prefix)
-    int T, member;          // CTAs a team, and the one with this row's pair
-    int row;                // the block row's first row within the unit's 2 * kPrefixRows
+// A block row's place in its group (nt 0: nothing shared).
+struct PrefixRow {
+    int nt, g, units1;  // shared tiles, group, pairs of a KV head
+    int pair;           // the row's pair
+    int row;            // the block row's first row within the pair's 2 * kPrefixRows
 };
-__device__ __forceinline__ PrefixUnit prefix_unit(const PrefixParams &x, int g, int r, int i_blk,
-                                                  int B, int G, int Hkv, int h) {
-    PrefixUnit u{0, 1, __ldcg(x.head + 1), 0, 1, 0, 0};
-    if (g < 0 || u.S < 0) return u;
+__device__ __forceinline__ PrefixRow prefix_row(const PrefixParams &x, int g, int r, int i_blk,
+                                                int B, int G) {
+    PrefixRow u{0, g, 0, 0, 0};
+    if (g < 0) return u;
     int r0, tokens;
     group_shape(x, g, B, r0, tokens, u.nt);
-    if (u.nt == 0) return u;
-    const int t = (r - r0) * B + i_blk;   // token within the group
-    const int tile = t / x.npt, pair = tile >> 1;
-    u.row = (tile & 1) * kPrefixRows + (t % x.npt) * G;
-    u.Wc = __ldcg(x.head);
-    u.T = (int)__ldcg(x.head + 2);
-    u.member = pair % u.T;
-    u.cost = __ldcg(x.goff + g) + ((long long)h * group_units(x, tokens, u.T) + pair / u.T) *
-                                      (kPrefixUnitCost + u.nt);
+    u.units1 = group_pairs(x, tokens);
+    const int t = (r - r0) * B + i_blk;  // token within the group
+    const int tile = t / x.npt;
+    u.pair = tile >> 1;
+    u.row = (tile & 1) * kPrefixRows + (t - tile * x.npt) * G;
     return u;
+}
+
+// The prefix kernel's schedule, once its grid has finished: the total cost, the
+// teams (S < 0: the group offsets are wrong), CTAs a team.
+struct PrefixTeams {
+    long long Wc;
+    int S, T;
+};
+__device__ __forceinline__ PrefixTeams prefix_plan_of(const PrefixParams &x) {
+    return {__ldcg(x.head), (int)__ldcg(x.head + 1), (int)__ldcg(x.head + 2)};
+}
+// The team whose cost range holds cost c: the largest b with b Wc / S <= c (an fp32
+// estimate, then exact steps: 64-bit division is a long subroutine here).
+__device__ __forceinline__ int prefix_team_of(long long c, const PrefixTeams &p) {
+    int b = (int)((float)(c + 1) * (float)p.S / (float)p.Wc);
+    b = max(0, min(b, p.S - 1));
+    while (b > 0 && b * p.Wc > c * p.S + p.S - 1) --b;
+    while (b + 1 < p.S && (b + 1) * p.Wc <= c * p.S + p.S - 1) ++b;
+    return b;
+}
+// Teams [q0, q1] hold the pieces of the row's unit of KV head h, in key order.
+__device__ __forceinline__ void prefix_teams(const PrefixParams &x, const PrefixTeams &p,
+                                             const PrefixRow &u, int h, int &q0, int &q1) {
+    const int units = (u.units1 + p.T - 1) / p.T;
+    const long long c0 = __ldcg(x.goff + u.g) +
+                         ((long long)h * units + u.pair / p.T) * (kPrefixUnitCost + u.nt) +
+                         kPrefixUnitCost;
+    q0 = prefix_team_of(c0, p);
+    q1 = prefix_team_of(c0 + u.nt - 1, p);
 }
 
 }  // namespace

@@ -1072,7 +1072,9 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
         // kPre: a unit's output also takes in its group's prefix partials,
         // whether this CTA holds the whole unit or owns a cut one.
         bool pfx_ready = false;
-        auto owner_gather = [&](Epi &e, const Piece &pc, float lr, int grp) -> bool {
+        PrefixTeams pfx_plan{};
+        PrefixRow pfx_row{};
+        auto owner_gather = [&](Epi &e, const Piece &pc, float lr) -> bool {
             const long long cu =
                 (long long)pc.u_off +
                 (long long)prm.unit_cost * ((long long)pc.r * vreq_units<kTree>(prm) + pc.u);
@@ -1085,12 +1087,13 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
 #pragma unroll
             for (int c = 0; c < OC; ++c) madd[c] = 0.f;
             // one more piece of the row: log2-sum-exp ls, normalised output at src
-            auto fold = [&](float ls, const float *src) {
+            auto load_row = [&](const float *src, float (&po)[OC]) {
                 // this thread's OC columns of the row: 32-byte loads (whole
                 // sectors), all in flight before the first is used
-                float po[OC];
 #pragma unroll
                 for (int v = 0; v < OC / 8; ++v) ld_cg_v8(src + 8 * v, &po[8 * v]);
+            };
+            auto fold = [&](float ls, const float (&po)[OC]) {
                 if (ls == -INFINITY) return;  // no key of that piece is visible to the row
                 const float m_new = fmaxf(m_run, ls);
                 const float a = m_run == -INFINITY ? 0.f : exp2f(m_run - m_new);
@@ -1104,24 +1107,29 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
             int bb = b + 1;
             if constexpr (kPre) {
                 if (!e.owner) bb = S;
-                if (!pfx_ready) grid_dependency_wait();
-                pfx_ready = true;
-                const PrefixUnit pu = prefix_unit(prm.pfx, grp, e.r, i_blk, B, G, prm.Hkv, pc.h);
-                bad = bad || pu.S < 0;
-                if (pu.nt > 0 && valid_row && !bad) {
-                    const long long c0 = pu.cost + kPrefixUnitCost;
-                    const int q0 = prefix_team_of(c0, pu.Wc, pu.S);
-                    const int q1 = prefix_team_of(c0 + pu.nt - 1, pu.Wc, pu.S);
-                    for (int q = q0; q <= q1; ++q) {
-                        const long src =
-                            q == q0 ? e.orow
-                                    : ((long)q * pu.T + pu.member) * 2 * kPrefixRows +
-                                          pu.row + row % G;
-                        const float ls =
-                            __ldcg((q == q0 ? prm.pfx.row_lse : prm.pfx.slot_lse) + src);
+                if (!pfx_ready) {
+                    grid_dependency_wait();
+                    pfx_plan = prefix_plan_of(prm.pfx);
+                    pfx_ready = true;
+                }
+                bad = bad || pfx_plan.S < 0;
+                if (pfx_row.nt > 0 && valid_row && !bad) {
+                    // the first piece's row is where the output row is; the others'
+                    // are looked up while it is on its way
+                    float po[OC];
+                    float ls = __ldcg(prm.pfx.row_lse + e.orow);
+                    load_row(prm.pfx.row_o + e.orow * D + half * OC, po);
+                    int q0, q1;
+                    prefix_teams(prm.pfx, pfx_plan, pfx_row, pc.h, q0, q1);
+                    for (int q = q0;;) {
                         if (ls == INFINITY) bad = true;  // a page outside the pool
-                        else fold(ls, (q == q0 ? prm.pfx.row_o : prm.pfx.slot_o) + src * D +
-                                          half * OC);
+                        else fold(ls, po);
+                        if (++q > q1) break;
+                        const long src =
+                            ((long)q * pfx_plan.T + pfx_row.pair % pfx_plan.T) * 2 * kPrefixRows +
+                            pfx_row.row + row % G;
+                        ls = __ldcg(prm.pfx.slot_lse + src);
+                        load_row(prm.pfx.slot_o + src * D + half * OC, po);
                     }
                 }
             }
@@ -1152,7 +1160,9 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                 const float *src = prm.part_o + ((long)sl * prm.rows + row) * D + half * OC;
                 const float ls = __ldcg(prm.part_lse + (long)sl * prm.rows + row);
                 bad = bad || __ldcg(prm.part_bad + sl) != 0;
-                fold(ls, src);
+                float po[OC];
+                load_row(src, po);
+                fold(ls, po);
             }
             // every softmax warp has read the words (a bounded wait on MR, one
             // phase per owned unit) before thread 0 resets them
@@ -1198,10 +1208,11 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
             // and checked during the next one (or the epilogue).
             bool shape_bad =
                 pc.L < 0 || ((long)pc.L + B + ps - 1) / ps > (long)prm.max_pages;
-            int grp = -1;  // the request's group (kPre)
             if constexpr (kPre) {
+                int grp;  // the request's group, and this row's place in it
                 request_prefix(prm.pfx, rr, pc.L, grp);
                 shape_bad = shape_bad || grp < 0;
+                pfx_row = prefix_row(prm.pfx, grp, rr, i_blk, B, G);
             }
             const int32_t *bt_row = prm.block_table + (long)rr * prm.max_pages;
             bool page_bad = false, pend = false;
@@ -1464,7 +1475,7 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                 if (e.bad && tid == 0) report_status(prm.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
                 if constexpr (kOwner) {
                     if (e.owner || (kPre && e.complete)) {
-                        ok = owner_gather(e, pc, lr, grp);
+                        ok = owner_gather(e, pc, lr);
                         if (!ok) break;
                     } else {
 #pragma unroll
