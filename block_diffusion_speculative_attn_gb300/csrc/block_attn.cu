@@ -1693,10 +1693,12 @@ bool expire_owner_waits() {
 // for the DRAFT / VERIFY tiles (Qwen3-8B-shaped verify call 64.5 -> 63.7 us,
 // long-context verify 331.2 -> 330.0 us, LLaDA2.0-style draft and Uno within
 // noise) and four for TREE calls, whose units are short row tiles (481-node
-// trees 1053 -> 994 us; three: 1009, five: 998).
-int unit_cost_for(int M, bool tree) {
+// trees 1053 -> 994 us; three: 1009, five: 998).  Six after a shared prefix, where
+// a switch also folds the partials in (32 verify blocks of 16 after 4096 keys 73.5
+// -> 71.8 us, 8 after 131072 keys 370 -> 362 us; ten: 72.3 and 362).
+int unit_cost_for(int M, bool tree, bool prefix) {
     (void)M;
-    return tree ? 4 : 3;
+    return prefix ? 6 : tree ? 4 : 3;
 }
 
 template <int D, int M>
@@ -1819,7 +1821,7 @@ int launch_impl(const AttnArgs &a, const AttnPlan &plan, cudaStream_t stream,
     prm.scale_log2 = a.scale * 1.4426950408889634f;
     prm.pfx = PrefixParams{};
     prm.magic_S = UINT64_MAX / (uint64_t)plan.grid;
-    prm.unit_cost = unit_cost_for(M, n_rt > 1 || a.mode == BDSA_MODE_TREE);
+    prm.unit_cost = unit_cost_for(M, n_rt > 1 || a.mode == BDSA_MODE_TREE, pfx != nullptr);
     if (pfx != nullptr) prm.pfx = *pfx;
     AppendParams app;
     app.k_new = a.k_new;
