@@ -55,6 +55,8 @@ constexpr int kBins = 512;         // one a thread of sample_cut
 constexpr int kParts = 8;          // parts of a thread's share of a slice, a maximum each
 constexpr int kMaxCluster = 8;
 constexpr int kListMax = 1024;  // candidates the sorted list holds
+constexpr int kWinBins = 2048;  // bins of a flat row's counts, four a thread
+constexpr int kWinMax = 8;      // the window: at most so many bins on either side
 constexpr uint32_t kAll = 0xffffffffu;
 
 // ------------------------------------------------------------ 2^(j / 16)
@@ -821,12 +823,14 @@ struct CutShared {
     uint64_t scan[kWarps], scan_c[kWarps];
     DrawShared draw;
     uint32_t wties[kWarps];       // cut-key elements of each warp's segment
+    uint64_t wextra[kWarps];      // kept weight of each warp's segment in the window
+    uint32_t near[kWinMax + 1];   // elements so many bins from the window's middle
     float red[2][kWarps];
     uint32_t hit[kListMax];       // parts that reach the pivot: thread * kParts + part
     int n_hit, n_list, n_below, n_min;
     // cluster exchange: written by this CTA, read by all, one use each
     float x_max, x_low;
-    uint64_t x_all;
+    uint64_t x_all, x_above;
     uint32_t x_ties, x_min;
     // the bin a select level (or the pivot search) chose
     int bin;
@@ -1062,6 +1066,64 @@ __device__ __forceinline__ void scan_list(uint64_t *a, int n, uint64_t *scratch)
     if (i < n) a[i] = t - y;
     if (i + 1 < n) a[i + 1] = t;
     __syncthreads();
+}
+
+// The CTAs' lists (n_list entries of list.own each) to list.a of every CTA, after
+// a cluster_sync; returns their entries (past kListMax: nothing is copied).  The
+// counts one a lane, then every entry of every list at once: a remote read takes
+// most of a microsecond.
+__device__ __forceinline__ int gather_lists(CutShared &sm, uint32_t ncta) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int m = lane < (int)ncta ? *map_to_rank(&sm.n_list, lane) : 0;
+    int ends = min(m, kListMax + 1);
+#pragma unroll
+    for (int o = 1; o < kMaxCluster; o <<= 1) {
+        const int t = __shfl_up_sync(kAll, ends, o);
+        if (lane >= o) ends += t;
+    }
+    const int n = __shfl_sync(kAll, ends, kMaxCluster - 1);
+    if (n > kListMax) return n;
+    for (int x0 = warp * 32; x0 < n; x0 += kThreads) {
+        const int x = x0 + lane;
+        int c = 0, from = 0;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster - 1; ++q) {
+            const int e = __shfl_sync(kAll, ends, q);
+            if (x >= e) {
+                c = q + 1;
+                from = e;
+            }
+        }
+        if (x < n) sm.list.a[x] = map_to_rank(sm.list.own, c)[x - from];
+    }
+    return n;
+}
+
+// Runs body(logit, position) for this thread's share of the slice: vectors tid +
+// kThreads j, and a position of each ragged end.
+template <typename T, bool kRes, class B>
+__device__ __forceinline__ void for_slice(const Row<T, kRes> &row, const Span &sp, B body) {
+    using L = Logit<T>;
+    using Raw = typename L::Raw;
+    constexpr int kVec = 16 / (int)sizeof(Raw);
+    const int tid = threadIdx.x;
+    if (tid < sp.head) body(row.at(tid));
+    if (tid < row.n - sp.tail) body(row.at(sp.tail + tid));
+    const uint4 *gv = reinterpret_cast<const uint4 *>((kRes ? row.s : row.g) + sp.head);
+    constexpr int kU = 4;
+    for (int x = tid; x < sp.nvec; x += kU * kThreads) {
+        uint4 q[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            if (x + u * kThreads < sp.nvec) q[u] = row.vec(gv + x + u * kThreads);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            if (x + u * kThreads >= sp.nvec) break;
+            const Raw *e = reinterpret_cast<const Raw *>(&q[u]);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) body(clean(L::wide(e[k])));
+        }
+    }
 }
 
 // The weight of the slice in units, this thread's share (every thread of the CTA).
@@ -1408,31 +1470,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
         cluster_sync();
         int n = 0;
         if (list) {
-            // the CTAs' counts, one a lane, then every entry of every list at once:
-            // a remote read takes most of a microsecond
-            const int m = lane < (int)ncta ? *map_to_rank(&sm.n_list, lane) : 0;
-            int ends = min(m, kListMax + 1);
-#pragma unroll
-            for (int o = 1; o < kMaxCluster; o <<= 1) {
-                const int t = __shfl_up_sync(kAll, ends, o);
-                if (lane >= o) ends += t;
-            }
-            n = __shfl_sync(kAll, ends, kMaxCluster - 1);
-            if (n <= kListMax) {
-                for (int x0 = warp * 32; x0 < n; x0 += kThreads) {
-                    const int x = x0 + lane;
-                    int c = 0, from = 0;
-#pragma unroll
-                    for (int q = 0; q < kMaxCluster - 1; ++q) {
-                        const int e = __shfl_sync(kAll, ends, q);
-                        if (x >= e) {
-                            c = q + 1;
-                            from = e;
-                        }
-                    }
-                    if (x < n) sm.list.a[x] = map_to_rank(sm.list.own, c)[x - from];
-                }
-            }
+            n = gather_lists(sm, ncta);
             list = n <= kListMax && n > 0;
         }
         cluster_reads_done();  // (of the lists)
@@ -1534,6 +1572,227 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
         cluster_wait_reads();  // the lists have been read everywhere: histograms may follow
     }
 
+    // top-p alone: a logit below which the cut cannot be, the one whose weight V
+    // times makes the share that may be left out (margins cover the fp32
+    // roundings); -inf when there is none
+    float low_p = -INFINITY;
+    if (use_p && !use_k && all_sum > 0 && top_p < 0.9999f) {
+        const float share = (1.f - fmaxf(top_p, 0.f)) * (float)all_sum /
+                            (kUnits * (float)a.V * wmax_f);
+        if (share > 0.f)
+            low_p = rs.lmax + (__logf(share) - 0.01f) / (rs.ch * 0.693147181f) -
+                    1e-4f * fabsf(rs.lmax) - 1e-5f;
+    }
+
+    // ================================================= a flat row's nucleus
+    // The logits above low_p are counted in equal bins; the counts times the bins'
+    // middle weights say in which bin the cut is, to a fraction of a bin.  One pass
+    // then adds up the exact weight above a window of a few bins around it and
+    // lists the window's logits, which are sorted and cut exactly.  (If the cut is
+    // outside the window, or the window holds too many, by selection below.)
+    if (low_p > -INFINITY && low_p < rs.lmax && !use_m && !row.inf && !rs.wide) {
+        const float hi = rs.lmax, scale = (float)kWinBins / (hi - low_p);
+        uint32_t *win = reinterpret_cast<uint32_t *>(sm.list.b);
+        static_assert(kWinBins == 4 * kThreads && sizeof(sm.list.b) == 4 * kWinBins, "counts");
+#pragma unroll
+        for (int k = 0; k < 4; ++k) win[tid + k * kThreads] = 0;
+        if (tid < kWarps) sm.wextra[tid] = 0;
+        if (tid <= kWinMax) sm.near[tid] = 0;
+        if (tid == 0) {
+            sm.n_list = sm.n_below = 0;
+            sm.bin = -1;
+        }
+        __syncthreads();
+        // (a logit's bin: monotone in the logit, and the same in either pass)
+        for_slice(row, sp, [&](float v) {
+            const float t = (hi - v) * scale;
+            if (t < (float)kWinBins) atomicAdd(win + (int)t, 1u);
+        });
+        cluster_sync();
+        uint4 x[kMaxCluster];
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+            x[c] = c < ncta ? *(map_to_rank(reinterpret_cast<const uint4 *>(win), c) + tid)
+                            : make_uint4(0, 0, 0, 0);
+        uint32_t cnt[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            cnt[0] += x[c].x;
+            cnt[1] += x[c].y;
+            cnt[2] += x[c].z;
+            cnt[3] += x[c].w;
+        }
+        const uint64_t goal = top_p > 0.f ? max((uint64_t)1, scaled(top_p, all_sum, true)) : 1;
+        uint64_t est[4], mine = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float wf;
+            est[k] = cnt[k] * weight(hi - ((float)(4 * tid + k) + 0.5f) / scale, rs, sm.tab, wf);
+            mine += est[k];
+        }
+        uint64_t upto = block_scan64(mine, sm.scan) - mine;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (upto < goal && upto + est[k] >= goal) sm.bin = 4 * tid + k;
+            upto += est[k];
+        }
+        __syncthreads();
+        const int b = sm.bin;
+        if (b >= 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int d = abs(4 * tid + k - b);
+                if (d <= kWinMax && cnt[k]) atomicAdd(sm.near + d, cnt[k]);
+            }
+        }
+        __syncthreads();
+        // as wide as the quick sort takes, the bin alone as long as the list does
+        int d = -1;
+        uint32_t in_win = 0;
+        for (int q = 0; q <= kWinMax && b >= 0 && b + q < kWinBins; ++q) {
+            in_win += sm.near[q];
+            if (in_win > (uint32_t)(q ? kThreads : kListMax)) break;
+            d = q;
+        }
+        bool found = d >= 0;
+        if (found) {  // (uniform over the cluster)
+            const float t0 = (float)(b - d), t1 = (float)(b + d + 1);
+            const Segment sg = segment_of(sp, row.n, warp);
+            Running run;
+            run.clear();
+            auto take = [&](float v, int at) {  // the logit, unless it is not above the window
+                const float t = (hi - v) * scale;
+                if (t < t0) return v;
+                if (t < t1) {
+                    const int n = atomicAdd(&sm.n_list, 1);
+                    if (n < kListMax)
+                        sm.list.own[n] = (uint64_t)~float_key(v) << 32 | (uint32_t)(e0 + at);
+                }
+                return -INFINITY;
+            };
+            auto add = [&](float v0, float v1) {
+                V2 h, l;
+                weight_ff<V2, false>(V2{f2_pack(v0, v1)}, rs, sm.tab, h, l);
+                run.add(h, l);
+            };
+            for (int x = sg.head0 + lane; x < sg.head1; x += 32) add(take(row.at(x), x), -INFINITY);
+            for (int x = sg.tail0 + lane; x < sg.tail1; x += 32) add(take(row.at(x), x), -INFINITY);
+            const uint4 *sv = reinterpret_cast<const uint4 *>((kRes ? row.s : row.g) + sp.head);
+            constexpr int kU = kRes ? 2 : 4;
+            for (int x0 = sg.v0 + lane; x0 < sg.v1; x0 += 32 * kU) {
+                uint4 q[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    if (x0 + 32 * u < sg.v1) q[u] = row.vec(sv + x0 + 32 * u);
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    if (x0 + 32 * u >= sg.v1) break;
+                    const Raw *e = reinterpret_cast<const Raw *>(&q[u]);
+                    const int at = sp.head + (x0 + 32 * u) * kVec;
+#pragma unroll
+                    for (int k = 0; k < kVec; k += 2)
+                        add(take(clean(L::wide(e[k])), at + k),
+                            take(clean(L::wide(e[k + 1])), at + k + 1));
+                }
+            }
+            __syncwarp();
+            uint64_t sum = warp_sum64(run.units(0, 0));
+            if (lane == 0) sm.scan[warp] = sum;
+            __syncthreads();
+            if (tid == 0) {
+                uint64_t v = 0;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) v += sm.scan[w];
+                sm.x_above = v;
+            }
+            cluster_sync();
+            uint64_t above = 0, xa[kMaxCluster];
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c)
+                xa[c] = c < ncta ? *map_to_rank(&sm.x_above, c) : 0;
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) above += xa[c];
+            const int n = gather_lists(sm, ncta);
+            __syncthreads();
+            found = n > 0 && n <= kListMax && above < goal;
+            if (found) {
+                uint64_t *keys = sort_list(sm.list.a, sm.list.b, n);
+                uint64_t *cum = keys == sm.list.a ? sm.list.b : sm.list.a;
+                for (int x = tid; x < n; x += kThreads) {
+                    float wf;
+                    cum[x] = weight(key_float(~(uint32_t)(keys[x] >> 32)), rs, sm.tab, wf);
+                }
+                __syncthreads();
+                scan_list(cum, n, sm.scan);
+                int below = 0;
+                for (int x = tid; x < n; x += kThreads) below += above + cum[x] < goal;
+                below = __reduce_add_sync(kAll, below);
+                if (lane == 0 && below) atomicAdd(&sm.n_below, below);
+                __syncthreads();
+                below = sm.n_below;
+                found = below < n;
+                if (found) {
+                    // the kept ones of the window, to their warps' segments
+                    const int per = (sp.nvec + kWarps - 1) / kWarps * kVec;
+                    for (int x = tid; x <= below; x += kThreads) {
+                        const int e = (int)(uint32_t)keys[x] - e0;
+                        if (e < 0 || e >= row.n) continue;
+                        const int w = e < sp.head   ? 0
+                                      : e >= sp.tail ? kWarps - 1
+                                                     : (e - sp.head) / per;
+                        atomicAdd((unsigned long long *)&sm.wextra[w],
+                                  (unsigned long long)(cum[x] - (x ? cum[x - 1] : 0)));
+                    }
+                    const uint64_t last = keys[below];
+                    __syncthreads();
+                    sum += sm.wextra[warp];
+                    uint64_t total, before;
+                    share_sums(sm.draw, sum, ncta, rank, total, before);
+                    cluster_reads_done();
+                    auto kept = [&](float v, int x) {
+                        return ((uint64_t)~float_key(v) << 32 | (uint32_t)(e0 + x)) <= last;
+                    };
+                    if (a.tokens) {
+                        const uint64_t target = draw_target(u01, total);
+                        const int w = warp_of_target(sm.draw, target, before);
+                        if (w >= 0) {
+                            const Segment g = segment_of(sp, row.n, w);
+                            const int x0 = g.head1 > g.head0 ? 0 : sp.head + g.v0 * kVec;
+                            const int x1 = g.tail1 > g.tail0 ? row.n : sp.head + g.v1 * kVec;
+                            for (int base = x0; base < x1; base += 4 * kThreads) {
+                                const int x = base + 4 * tid;
+                                uint64_t q[4], s4 = 0;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const float v = x + k < x1 ? row.at(x + k) : -INFINITY;
+                                    float wf;
+                                    q[k] = x + k < x1 && kept(v, x + k) ? weight(v, rs, sm.tab, wf)
+                                                                        : 0;
+                                    s4 += q[k];
+                                }
+                                draw_in_block(sm.draw, target, before, q, s4, e0 + x,
+                                              a.tokens + rowi);
+                            }
+                        }
+                    }
+                    if (prow) {  // over the zeros of the first pass
+                        const float inv = inverse(total);
+                        const int seg = ((row.n + kWarps - 1) / kWarps + 31) & ~31;
+                        const int w0 = min(row.n, warp * seg), w1 = min(row.n, w0 + seg);
+                        for_selected(row, w0, w1, lane, kept, [&](int x) {
+                            float wf;
+                            weight(row.at(x), rs, sm.tab, wf);
+                            prow[x] = wf * inv;
+                        });
+                    }
+                    cluster_wait_reads();
+                    return;
+                }
+            }
+        }
+        cluster_sync();  // counts and lists have been read everywhere
+    }
+
     // ================================================= any row, by selection
     const int seg = ((row.n + kWarps - 1) / kWarps + 31) & ~31;
     const int w0 = min(row.n, warp * seg), w1 = min(row.n, w0 + seg);
@@ -1541,19 +1800,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
     uint64_t key_count = 0;  // elements with the cut's key
     if (use_k || use_p) {
         // The keys the cut can be among: from the pivot of top-k (want_k logits
-        // are at or above it); for top-p alone from the logit whose weight V
-        // times makes the share that may be left out (margins cover the fp32
-        // roundings); else from the smallest logit.
+        // are at or above it); for top-p alone from low_p; else from the smallest
+        // logit.
         const uint32_t kmax = R::key(rs.lmax);
         uint32_t kmin = 0xffffffffu;
         if (pivot_k > -INFINITY) {
             kmin = R::key(pivot_k);
-        } else if (!use_k && all_sum > 0 && top_p < 0.9999f) {
-            const float share = (1.f - fmaxf(top_p, 0.f)) * (float)all_sum /
-                                (kUnits * (float)a.V * wmax_f);
-            const float l = rs.lmax + (__logf(share) - 0.01f) / (rs.ch * 0.693147181f) -
-                            1e-4f * fabsf(rs.lmax) - 1e-5f;
-            if (l > -INFINITY && share > 0.f) kmin = min(kmax, R::key(l));
+        } else if (low_p > -INFINITY) {
+            kmin = min(kmax, R::key(low_p));
         }
         if (kmin == 0xffffffffu) {
             const uint32_t kinf = R::key(-INFINITY);
