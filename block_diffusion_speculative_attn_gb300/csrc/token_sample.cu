@@ -42,6 +42,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <limits.h>
+#include <stddef.h>
 
 #include "bdsa_device.cuh"
 #include "bdsa_internal.h"
@@ -56,7 +57,7 @@ constexpr int kParts = 8;          // parts of a thread's share of a slice, a ma
 constexpr int kMaxCluster = 8;
 constexpr int kListMax = 1024;  // candidates the sorted list holds
 constexpr int kWinBins = 2048;  // bins of a flat row's counts, four a thread
-constexpr int kWinMax = 8;      // the window: at most so many bins on either side
+constexpr int kWinMax = 4;      // the window: at most so many bins on either side
 constexpr uint32_t kAll = 0xffffffffu;
 
 // ------------------------------------------------------------ 2^(j / 16)
@@ -825,9 +826,10 @@ struct CutShared {
     uint32_t wties[kWarps];       // cut-key elements of each warp's segment
     uint64_t wextra[kWarps];      // kept weight of each warp's segment in the window
     uint32_t near[kWinMax + 1];   // elements so many bins from the window's middle
+    uint32_t wbin[2 * kWinMax + 1][3];  // weights of the window's bins (as Hist's)
     float red[2][kWarps];
     uint32_t hit[kListMax];       // parts that reach the pivot: thread * kParts + part
-    int n_hit, n_list, n_below, n_min;
+    int n_hit, n_list, n_below, n_min, n_cut;
     // cluster exchange: written by this CTA, read by all, one use each
     float x_max, x_low;
     uint64_t x_all, x_above;
@@ -1585,49 +1587,69 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
     }
 
     // ================================================= a flat row's nucleus
-    // The logits above low_p are counted in equal bins; the counts times the bins'
-    // middle weights say in which bin the cut is, to a fraction of a bin.  One pass
-    // then adds up the exact weight above a window of a few bins around it and
+    // The logits above low_p are counted in equal bins, with their places in the
+    // bins (in 256ths) added up; each bin's count times the weight of its mean logit
+    // says in which bin the cut is, to a fraction of a bin.  (The bins' middles
+    // would not do: when one logit holds most of the weight, half a bin of it is
+    // more than the few per cent behind the cut.)  One pass then adds up the exact weight above a window of a few bins around it and
     // lists the window's logits, which are sorted and cut exactly.  (If the cut is
     // outside the window, or the window holds too many, by selection below.)
     if (low_p > -INFINITY && low_p < rs.lmax && !use_m && !row.inf && !rs.wide) {
         const float hi = rs.lmax, scale = (float)kWinBins / (hi - low_p);
-        uint32_t *win = reinterpret_cast<uint32_t *>(sm.list.b);
-        static_assert(kWinBins == 4 * kThreads && sizeof(sm.list.b) == 4 * kWinBins, "counts");
+        uint32_t *win = reinterpret_cast<uint32_t *>(sm.list.a), *place = win + kWinBins;
+        static_assert(kWinBins == 4 * kThreads && sizeof(sm.list.a) == 4 * kWinBins &&
+                          offsetof(Lists, b) == offsetof(Lists, a) + sizeof(sm.list.a),
+                      "counts and places over a and b");
 #pragma unroll
-        for (int k = 0; k < 4; ++k) win[tid + k * kThreads] = 0;
+        for (int k = 0; k < 8; ++k) win[tid + k * kThreads] = 0;
         if (tid < kWarps) sm.wextra[tid] = 0;
         if (tid <= kWinMax) sm.near[tid] = 0;
+        if (tid < 3 * (2 * kWinMax + 1)) (&sm.wbin[0][0])[tid] = 0;
         if (tid == 0) {
-            sm.n_list = sm.n_below = 0;
+            sm.n_list = sm.n_below = sm.n_cut = 0;
             sm.bin = -1;
         }
         __syncthreads();
         // (a logit's bin: monotone in the logit, and the same in either pass)
         for_slice(row, sp, [&](float v) {
             const float t = (hi - v) * scale;
-            if (t < (float)kWinBins) atomicAdd(win + (int)t, 1u);
+            if (t < (float)kWinBins) {
+                atomicAdd(win + (int)t, 1u);
+                atomicAdd(place + (int)t, (uint32_t)((t - (float)(int)t) * 256.f));
+            }
         });
         cluster_sync();
-        uint4 x[kMaxCluster];
+        uint32_t cnt[4] = {0, 0, 0, 0}, at[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)
-            x[c] = c < ncta ? *(map_to_rank(reinterpret_cast<const uint4 *>(win), c) + tid)
-                            : make_uint4(0, 0, 0, 0);
-        uint32_t cnt[4] = {0, 0, 0, 0};
+        for (int c0 = 0; c0 < kMaxCluster; c0 += 4) {
+            uint4 x[4], y[4];
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-            cnt[0] += x[c].x;
-            cnt[1] += x[c].y;
-            cnt[2] += x[c].z;
-            cnt[3] += x[c].w;
+            for (int c = 0; c < 4; ++c) {
+                x[c] = y[c] = make_uint4(0, 0, 0, 0);
+                if (c0 + c < (int)ncta) {
+                    x[c] = map_to_rank(reinterpret_cast<const uint4 *>(win), c0 + c)[tid];
+                    y[c] = map_to_rank(reinterpret_cast<const uint4 *>(place), c0 + c)[tid];
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                cnt[0] += x[c].x;
+                cnt[1] += x[c].y;
+                cnt[2] += x[c].z;
+                cnt[3] += x[c].w;
+                at[0] += y[c].x;
+                at[1] += y[c].y;
+                at[2] += y[c].z;
+                at[3] += y[c].w;
+            }
         }
         const uint64_t goal = top_p > 0.f ? max((uint64_t)1, scaled(top_p, all_sum, true)) : 1;
         uint64_t est[4], mine = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             float wf;
-            est[k] = cnt[k] * weight(hi - ((float)(4 * tid + k) + 0.5f) / scale, rs, sm.tab, wf);
+            const float mean = cnt[k] ? ((float)at[k] / (float)cnt[k] + 0.5f) * (1.f / 256.f) : 0.f;
+            est[k] = cnt[k] * weight(hi - ((float)(4 * tid + k) + mean) / scale, rs, sm.tab, wf);
             mine += est[k];
         }
         uint64_t upto = block_scan64(mine, sm.scan) - mine;
@@ -1646,12 +1668,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
             }
         }
         __syncthreads();
-        // as wide as the quick sort takes, the bin alone as long as the list does
+        // as wide as the list takes
         int d = -1;
         uint32_t in_win = 0;
         for (int q = 0; q <= kWinMax && b >= 0 && b + q < kWinBins; ++q) {
             in_win += sm.near[q];
-            if (in_win > (uint32_t)(q ? kThreads : kListMax)) break;
+            if (in_win > (uint32_t)kListMax) break;
             d = q;
         }
         bool found = d >= 0;
@@ -1716,34 +1738,68 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
             __syncthreads();
             found = n > 0 && n <= kListMax && above < goal;
             if (found) {
-                uint64_t *keys = sort_list(sm.list.a, sm.list.b, n);
-                uint64_t *cum = keys == sm.list.a ? sm.list.b : sm.list.a;
-                for (int x = tid; x < n; x += kThreads) {
+                // the weights of the window's bins, then of the cut's bin one by one
+                uint64_t key[2], w[2];
+                int bin[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int x = tid + k * kThreads;
+                    key[k] = x < n ? sm.list.a[x] : ~0ull;
+                    const float v = key_float(~(uint32_t)(key[k] >> 32));
                     float wf;
-                    cum[x] = weight(key_float(~(uint32_t)(keys[x] >> 32)), rs, sm.tab, wf);
+                    w[k] = x < n ? weight(v, rs, sm.tab, wf) : 0;
+                    bin[k] = x < n ? (int)((hi - v) * scale) - (b - d) : -1;
+                    if (x < n) {
+                        const uint32_t l0 = (uint32_t)w[k] & 0x3fffu;
+                        const uint32_t l1 = (uint32_t)(w[k] >> 14) & 0x3fffu;
+                        atomicAdd(&sm.wbin[bin[k]][0], l0);
+                        atomicAdd(&sm.wbin[bin[k]][1], l1);
+                        atomicAdd(&sm.wbin[bin[k]][2], (uint32_t)(w[k] >> 28));
+                    }
                 }
                 __syncthreads();
-                scan_list(cum, n, sm.scan);
-                int below = 0;
-                for (int x = tid; x < n; x += kThreads) below += above + cum[x] < goal;
-                below = __reduce_add_sync(kAll, below);
-                if (lane == 0 && below) atomicAdd(&sm.n_below, below);
-                __syncthreads();
-                below = sm.n_below;
-                found = below < n;
+                int cut = -1;
+                for (int q = 0; q <= 2 * d; ++q) {
+                    const uint64_t m = (uint64_t)sm.wbin[q][0] + ((uint64_t)sm.wbin[q][1] << 14) +
+                                       ((uint64_t)sm.wbin[q][2] << 28);
+                    if (above + m >= goal) {
+                        cut = q;
+                        break;
+                    }
+                    above += m;
+                }
+                found = cut >= 0;
                 if (found) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (bin[k] == cut) sm.list.b[atomicAdd(&sm.n_cut, 1)] = key[k];
+                    __syncthreads();
+                    const int m = sm.n_cut;
+                    uint64_t *keys = sort_list(sm.list.b, sm.list.a, m);
+                    uint64_t *cum = keys == sm.list.a ? sm.list.b : sm.list.a;
+                    for (int x = tid; x < m; x += kThreads) {
+                        float wf;
+                        cum[x] = weight(key_float(~(uint32_t)(keys[x] >> 32)), rs, sm.tab, wf);
+                    }
+                    __syncthreads();
+                    scan_list(cum, m, sm.scan);
+                    int below = 0;
+                    for (int x = tid; x < m; x += kThreads) below += above + cum[x] < goal;
+                    below = __reduce_add_sync(kAll, below);
+                    if (lane == 0 && below) atomicAdd(&sm.n_below, below);
+                    __syncthreads();
+                    const uint64_t last = keys[sm.n_below];
                     // the kept ones of the window, to their warps' segments
                     const int per = (sp.nvec + kWarps - 1) / kWarps * kVec;
-                    for (int x = tid; x <= below; x += kThreads) {
-                        const int e = (int)(uint32_t)keys[x] - e0;
-                        if (e < 0 || e >= row.n) continue;
-                        const int w = e < sp.head   ? 0
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int e = (int)(uint32_t)key[k] - e0;
+                        if (key[k] > last || e < 0 || e >= row.n) continue;
+                        const int q = e < sp.head   ? 0
                                       : e >= sp.tail ? kWarps - 1
                                                      : (e - sp.head) / per;
-                        atomicAdd((unsigned long long *)&sm.wextra[w],
-                                  (unsigned long long)(cum[x] - (x ? cum[x - 1] : 0)));
+                        atomicAdd((unsigned long long *)&sm.wextra[q], (unsigned long long)w[k]);
                     }
-                    const uint64_t last = keys[below];
                     __syncthreads();
                     sum += sm.wextra[warp];
                     uint64_t total, before;
