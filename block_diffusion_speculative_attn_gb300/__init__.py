@@ -581,10 +581,10 @@ def block_table_update(seq_lens, new_lens, owned, block_table, free_pages, free_
     if out is None:
         pad = -n % 4  # slot_map and positions start on 16-byte boundaries
         buf = torch.empty(2 * (n + pad) + 2 * bs + 3, dtype=i32, device=block_table.device)
-        if pad:
-            slot, _, pos, _, own, cu, state = buf.split((n, pad, n, pad, bs, bs + 1, 2))
-        else:
-            slot, pos, own, cu, state = buf.split((n, n, bs, bs + 1, 2))
+        sizes = (n, pad, n, pad, bs, bs + 1, 2) if pad else (n, n, bs, bs + 1, 2)
+        parts = buf.split_with_sizes(sizes)
+        slot, pos = parts[0], parts[2 if pad else 1]
+        own, cu, state = parts[-3:]
         out = dict(owned=own, free_state=state, cu_tokens=cu, slot_map=slot, positions=pos)
         p = buf.data_ptr()
         q = p + 8 * (n + pad)
