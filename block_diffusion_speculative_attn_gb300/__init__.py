@@ -579,16 +579,10 @@ def block_table_update(seq_lens, new_lens, owned, block_table, free_pages, free_
     if n < 0:
         raise ValueError("total_tokens must be >= 0")
     if out is None:
-        pad = -n % 4  # slot_map and positions start on 16-byte boundaries
-        buf = torch.empty(2 * (n + pad) + 2 * bs + 3, dtype=i32, device=block_table.device)
-        sizes = (n, pad, n, pad, bs, bs + 1, 2) if pad else (n, n, bs, bs + 1, 2)
-        parts = buf.split_with_sizes(sizes)
-        slot, pos = parts[0], parts[2 if pad else 1]
-        own, cu, state = parts[-3:]
-        out = dict(owned=own, free_state=state, cu_tokens=cu, slot_map=slot, positions=pos)
-        p = buf.data_ptr()
-        q = p + 8 * (n + pad)
-        outs = (q, q + 8 * bs + 4, q + 4 * bs, p if n else None, p + 4 * (n + pad) if n else None)
+        dev = block_table.device
+        out = {k: torch.empty(m, dtype=i32, device=dev)
+               for k, m in zip(TABLE_KEYS, (bs, 2, bs + 1, n, n))}
+        outs = [t.data_ptr() for t in out.values()]
     else:
         outs = [_arg(out[k], k, i32, sh, index) for k, sh in
                 zip(TABLE_KEYS, ((bs,), (2,), (bs + 1,), (n,), (n,)))]
