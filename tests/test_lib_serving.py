@@ -102,6 +102,36 @@ def test_prefix_refusals(L):
     assert _prefix(L, out=A + 2) == 3
 
 
+def test_outputs_apart_from_inputs_and_one_another(L):
+    M = 1 << 24
+    ins = dict(zip(("seq", "new", "own", "shared", "state"), range(M, 6 * M, M)))
+    outs = dict(zip(("bt", "ring", "own_out", "state_out", "cu", "slot", "pos"),
+                    range(6 * M, 13 * M, M)))
+    for o in outs:
+        for i in list(ins) + [x for x in outs if x != o]:
+            a = {**ins, **outs, "bs": 32, "np": 64, "mt": 64}
+            a[o] = a[i] + 4
+            assert _table(L, **a) == 1, (o, i)
+    ins = dict(zip(("l", "u", "T", "k", "p", "m"), range(M, 7 * M, M)))
+    outs = dict(tok=7 * M, pr=8 * M)
+    for o in outs:
+        for i in list(ins) + [x for x in outs if x != o]:
+            a = {**ins, **outs}
+            a[o] = a[i] + 4
+            assert _sample(L, **a) == 1, (o, i)
+    a = {**ins, **outs, "l": 8 * M - 4 * 32000 + 16}  # the last logit row meets probs
+    assert _sample(L, **a) == 1
+    assert _sample(L, **{**a, "l": 8 * M + 4 * 32000 - 16}) == 1
+    M = 1 << 32
+    ins = dict(zip(("q", "k", "v", "bt", "sl", "go", "pl"), range(M, 8 * M, M)))
+    outs = dict(out=8 * M, lse=9 * M, ws=10 * M, wsb=1 << 30)
+    for o in ("out", "lse", "ws"):
+        for i in list(ins) + [x for x in ("out", "lse", "ws") if x != o]:
+            a = {**ins, **outs}
+            a[o] = a[i]
+            assert _prefix(L, **a) == 1, (o, i)
+
+
 def test_prefix_workspace(L):
     f = L.bdsa_block_attn_prefix_workspace_bytes
     al = lambda x: (x + 255) // 256 * 256
