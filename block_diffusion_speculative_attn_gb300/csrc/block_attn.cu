@@ -1491,6 +1491,9 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
     }
 
     if (tid == 0) bulk_wait_group0();  // epilogue tile stores complete
+    // kPre: this grid ends after the prefix kernel's even if no epilogue waited for
+    // it (units given up), so that what follows on the stream may use the workspace
+    if (kPre && b == 0) grid_dependency_wait();
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
