@@ -11,8 +11,9 @@
 // keys, numbered (group, KV head, T pairs); each is charged kPrefixUnitCost
 // virtual tiles and its P' / 128 real ones, and team b of S takes the cost range
 // [b Wc / S, (b + 1) Wc / S).  The piece that holds a unit's first tile goes to
-// per-row buffers (a row has one such piece); any other piece is the first of its
-// CTA and goes to that CTA's slot.
+// per-row buffers (a row has one such piece), with the numbers of the teams that
+// hold the unit's first and last tile; any other piece is the first of its CTA and
+// goes to that CTA's slot.
 #pragma once
 
 #include "attn_common.cuh"
@@ -73,17 +74,16 @@ __device__ __forceinline__ long long prefix_range_start(long long b, long long W
 
 // A block row's place in its group (nt 0: nothing shared).
 struct PrefixRow {
-    int nt, g, units1;  // shared tiles, group, pairs of a KV head
-    int pair;           // the row's pair
-    int row;            // the block row's first row within the pair's 2 * kPrefixRows
+    int nt;    // shared tiles
+    int pair;  // the row's pair
+    int row;   // the block row's first row within the pair's 2 * kPrefixRows
 };
 __device__ __forceinline__ PrefixRow prefix_row(const PrefixParams &x, int g, int r, int i_blk,
                                                 int B, int G) {
-    PrefixRow u{0, g, 0, 0, 0};
+    PrefixRow u{0, 0, 0};
     if (g < 0) return u;
     int r0, tokens;
     group_shape(x, g, B, r0, tokens, u.nt);
-    u.units1 = group_pairs(x, tokens);
     const int t = (r - r0) * B + i_blk;  // token within the group
     const int tile = t / x.npt;
     u.pair = tile >> 1;
@@ -91,33 +91,14 @@ __device__ __forceinline__ PrefixRow prefix_row(const PrefixParams &x, int g, in
     return u;
 }
 
-// The prefix kernel's schedule, once its grid has finished: the total cost, the
-// teams (S < 0: the group offsets are wrong), CTAs a team.
-struct PrefixTeams {
-    long long Wc;
-    int S, T;
-};
-__device__ __forceinline__ PrefixTeams prefix_plan_of(const PrefixParams &x) {
-    return {__ldcg(x.head), (int)__ldcg(x.head + 1), (int)__ldcg(x.head + 2)};
-}
 // The team whose cost range holds cost c: the largest b with b Wc / S <= c (an fp32
 // estimate, then exact steps: 64-bit division is a long subroutine here).
-__device__ __forceinline__ int prefix_team_of(long long c, const PrefixTeams &p) {
-    int b = (int)((float)(c + 1) * (float)p.S / (float)p.Wc);
-    b = max(0, min(b, p.S - 1));
-    while (b > 0 && b * p.Wc > c * p.S + p.S - 1) --b;
-    while (b + 1 < p.S && (b + 1) * p.Wc <= c * p.S + p.S - 1) ++b;
+__device__ __forceinline__ int prefix_team_of(long long c, long long Wc, int S) {
+    int b = (int)((float)(c + 1) * (float)S / (float)Wc);
+    b = max(0, min(b, S - 1));
+    while (b > 0 && b * Wc > c * S + S - 1) --b;
+    while (b + 1 < S && (b + 1) * Wc <= c * S + S - 1) ++b;
     return b;
-}
-// Teams [q0, q1] hold the pieces of the row's unit of KV head h, in key order.
-__device__ __forceinline__ void prefix_teams(const PrefixParams &x, const PrefixTeams &p,
-                                             const PrefixRow &u, int h, int &q0, int &q1) {
-    const int units = (u.units1 + p.T - 1) / p.T;
-    const long long c0 = __ldcg(x.goff + u.g) +
-                         ((long long)h * units + u.pair / p.T) * (kPrefixUnitCost + u.nt) +
-                         kPrefixUnitCost;
-    q0 = prefix_team_of(c0, p);
-    q1 = prefix_team_of(c0 + u.nt - 1, p);
 }
 
 }  // namespace

@@ -236,7 +236,7 @@ size_t bdsa_block_attn_prefix_workspace_bytes(int32_t bs, int32_t B, int32_t Hq,
                                               int32_t num_sms) {
     if (bs <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_ctx_len < 0 || num_groups <= 0)
         return 0;
-    return bdsa::prefix_plan(bs, B, Hq, Hkv, D, num_groups, bdsa::device_num_sms(num_sms))
+    return bdsa::prefix_plan(bs, B, Hq, Hkv, D, bdsa::device_num_sms(num_sms))
         .workspace;
 }
 

@@ -45,19 +45,19 @@ struct PrefixParams {
     const int32_t *group_offsets, *prefix_lens;  // [ng + 1], [ng]
     int ng, bs;
     int npt;                    // whole tokens in a 128-row tile
-    long long *head;            // {total cost, teams, CTAs a team}, by the prefix kernel
-    long long *goff;            // [ng] cost offset of each group's first unit
+    int32_t *head;              // {CTAs a team, or -1: the group offsets are wrong}
     float *row_lse, *row_o;     // [bs * B * Hq], [.., D]: first pieces
+    uint32_t *row_teams;        // [bs * B * Hq]: the teams of a row's first and last piece
     float *slot_lse, *slot_o;   // [grid, 256], [.., D]: the other pieces, one slot a CTA
 };
 
 struct PrefixPlan {
     AttnPlan attn;
-    size_t off_head, off_goff, off_row_lse, off_slot_lse, off_row_o, off_slot_o;
+    size_t off_head, off_row_lse, off_row_teams, off_slot_lse, off_row_o, off_slot_o;
     size_t workspace;
 };
 
-PrefixPlan prefix_plan(int bs, int B, int Hq, int Hkv, int D, int num_groups, int num_sms);
+PrefixPlan prefix_plan(int bs, int B, int Hq, int Hkv, int D, int num_sms);
 int launch_prefix_partials(const AttnArgs &a, const PrefixParams &x, int grid,
                            cudaStream_t stream);
 int launch_prefix_attn(const AttnArgs &a, const int32_t *group_offsets,

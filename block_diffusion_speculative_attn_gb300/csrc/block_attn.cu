@@ -1072,7 +1072,7 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
         // kPre: a unit's output also takes in its group's prefix partials,
         // whether this CTA holds the whole unit or owns a cut one.
         bool pfx_ready = false;
-        PrefixTeams pfx_plan{};
+        int pfx_T = 1;  // CTAs a team of the prefix kernel; -1: nothing to read
         PrefixRow pfx_row{};
         auto owner_gather = [&](Epi &e, const Piece &pc, float lr) -> bool {
             const long long cu =
@@ -1109,24 +1109,24 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                 if (!e.owner) bb = S;
                 if (!pfx_ready) {
                     grid_dependency_wait();
-                    pfx_plan = prefix_plan_of(prm.pfx);
+                    pfx_T = __ldcg(prm.pfx.head);
                     pfx_ready = true;
                 }
-                bad = bad || pfx_plan.S < 0;
+                bad = bad || pfx_T < 0;
                 if (pfx_row.nt > 0 && valid_row && !bad) {
-                    // the first piece's row is where the output row is; the others'
-                    // are looked up while it is on its way
+                    // the first piece's row is where the output row is, with the
+                    // numbers of the teams that hold the others
                     float po[OC];
                     float ls = __ldcg(prm.pfx.row_lse + e.orow);
+                    const uint32_t teams = __ldcg(prm.pfx.row_teams + e.orow);
                     load_row(prm.pfx.row_o + e.orow * D + half * OC, po);
-                    int q0, q1;
-                    prefix_teams(prm.pfx, pfx_plan, pfx_row, pc.h, q0, q1);
-                    for (int q = q0;;) {
+                    const int q1 = (int)(teams & 0xffffu);
+                    for (int q = (int)(teams >> 16);;) {
                         if (ls == INFINITY) bad = true;  // a page outside the pool
                         else fold(ls, po);
                         if (++q > q1) break;
                         const long src =
-                            ((long)q * pfx_plan.T + pfx_row.pair % pfx_plan.T) * 2 * kPrefixRows +
+                            ((long)q * pfx_T + (pfx_row.pair & (pfx_T - 1))) * 2 * kPrefixRows +
                             pfx_row.row + row % G;
                         ls = __ldcg(prm.pfx.slot_lse + src);
                         load_row(prm.pfx.slot_o + src * D + half * OC, po);
@@ -1896,7 +1896,7 @@ int launch_block_attn(const AttnArgs &a, cudaStream_t stream) {
 // The shared-prefix call: the prefix kernel's partials (prefix_attn.cu), then
 // the block attention over the keys behind the prefix.  The owner merge wants
 // the whole grid resident, so there are at most as many CTAs as SMs.
-PrefixPlan prefix_plan(int bs, int B, int Hq, int Hkv, int D, int num_groups, int num_sms) {
+PrefixPlan prefix_plan(int bs, int B, int Hq, int Hkv, int D, int num_sms) {
     PrefixPlan p;
     p.attn = attn_plan(bs, B, Hq, Hkv, D, 0, num_sms);
     size_t off = p.attn.workspace;
@@ -1907,9 +1907,9 @@ PrefixPlan prefix_plan(int bs, int B, int Hq, int Hkv, int D, int num_groups, in
         off += align256(bytes);
         return at;
     };
-    p.off_head = take(3 * sizeof(int64_t));
-    p.off_goff = take((size_t)num_groups * sizeof(int64_t));
+    p.off_head = take(sizeof(int32_t));
     p.off_row_lse = take(rows * sizeof(float));
+    p.off_row_teams = take(rows * sizeof(uint32_t));
     p.off_slot_lse = take(slots * sizeof(float));
     p.off_row_o = take(rows * D * sizeof(float));
     p.off_slot_o = take(slots * D * sizeof(float));
@@ -1922,8 +1922,7 @@ int launch_prefix_attn(const AttnArgs &a, const int32_t *group_offsets,
     AttnArgs b = a;
     const int sms = device_num_sms(0);
     if (b.num_sms > sms) b.num_sms = sms;
-    const PrefixPlan plan =
-        prefix_plan(b.bs, b.B, b.Hq, b.Hkv, b.D, num_groups, b.num_sms);
+    const PrefixPlan plan = prefix_plan(b.bs, b.B, b.Hq, b.Hkv, b.D, b.num_sms);
     if (b.workspace == nullptr || b.workspace_bytes < plan.workspace)
         return BDSA_WORKSPACE_TOO_SMALL;
     char *ws = static_cast<char *>(b.workspace);
@@ -1933,8 +1932,8 @@ int launch_prefix_attn(const AttnArgs &a, const int32_t *group_offsets,
     x.ng = num_groups;
     x.bs = b.bs;
     x.npt = kPrefixRows / (b.Hq / b.Hkv);
-    x.head = reinterpret_cast<long long *>(ws + plan.off_head);
-    x.goff = reinterpret_cast<long long *>(ws + plan.off_goff);
+    x.head = reinterpret_cast<int32_t *>(ws + plan.off_head);
+    x.row_teams = reinterpret_cast<uint32_t *>(ws + plan.off_row_teams);
     x.row_lse = reinterpret_cast<float *>(ws + plan.off_row_lse);
     x.slot_lse = reinterpret_cast<float *>(ws + plan.off_slot_lse);
     x.row_o = reinterpret_cast<float *>(ws + plan.off_row_o);

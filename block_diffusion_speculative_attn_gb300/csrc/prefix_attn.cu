@@ -87,7 +87,8 @@ struct PSched {
     uint32_t tmem;
     int abort;
     long long wsum[12], wsum2[2][12];
-    int T, member;         // CTAs a team, this one's place
+    int T, member, S;      // CTAs a team, this one's place, teams
+    long long Wc;
     long long c0, c1;      // this CTA's cost range
     long long gbase;       // cost offset of the group holding c0
     int g0;
@@ -106,6 +107,7 @@ struct PParams {
 struct PPiece {
     int r0, tok0, ntok;   // the group's first request; this unit's first token, tokens left
     int h, a, e, nt;      // KV head, tiles [a, e) of nt
+    long long last;       // the cost of the unit's last tile
 };
 
 // Walks the pieces of a cost range, group by group.
@@ -145,6 +147,7 @@ struct PWalk {
             pc.a = a;
             pc.e = e;
             pc.nt = nt;
+            pc.last = cu + span - 1;
             return true;
         }
         return false;
@@ -338,7 +341,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
         long long at = wex + inc - sum;
         for (int g = i0; g < i1; ++g) {
             const long long cg = cost(g, T);
-            if (blockIdx.x == 0) prm.x.goff[g] = at;
             if (at <= c0 && c0 < at + cg) {
                 sch->g0 = g;
                 sch->gbase = at;
@@ -349,11 +351,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
             sch->c0 = c0;
             sch->c1 = c1;
             sch->T = T;
+            sch->S = (int)S;
+            sch->Wc = Wc;
             sch->member = blockIdx.x % T;
             if (blockIdx.x == 0) {
-                prm.x.head[0] = Wc;
-                prm.x.head[1] = wrong ? -1 : S;
-                prm.x.head[2] = T;
+                prm.x.head[0] = wrong ? -1 : T;
                 if (wrong) report_status(prm.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
             }
         }
@@ -690,6 +692,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
             }
             if (!ok) break;
             // ---- end of the piece: o / l and the log2-sum-exp
+            const uint32_t team = blockIdx.x / sch->T;
+            const uint32_t teams =
+                team << 16 | (pc.e == pc.nt ? team
+                                            : (uint32_t)prefix_team_of(pc.last, sch->Wc, sch->S));
             ok = mbar_wait(bar(C::OF + t), (uint32_t)(k & 1), abort_flag, prm.dev_status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -724,9 +730,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::OE + t));
             // a bad piece is marked by +inf
-            if (real)
+            if (real) {
                 (slot0 ? prm.x.slot_lse : prm.x.row_lse)[dst] =
                     bad ? INFINITY : (l > 0.f ? m_used + log2f(l) : -INFINITY);
+                if (!slot0) prm.x.row_teams[dst] = teams;
+            }
             if (bad && lane == 0) report_status(prm.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
             ++k;
         }

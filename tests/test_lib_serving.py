@@ -138,7 +138,7 @@ def test_prefix_workspace(L):
     bs, B, Hq, Hkv, D, ng, sms = 32, 16, 32, 8, 128, 3, 152
     rows, slots = bs * B * Hq, 256 * sms
     want = L.bdsa_block_attn_workspace_bytes(bs, B, Hq, Hkv, D, 4096, sms)
-    want += al(24) + al(8 * ng) + al(4 * rows) + al(4 * slots) + al(4 * rows * D) + \
+    want += al(4) + 2 * al(4 * rows) + al(4 * slots) + al(4 * rows * D) + \
         al(4 * slots * D)
     assert f(bs, B, Hq, Hkv, D, 4096, ng, sms) == want
     assert f(bs, B, Hq, Hkv, D, 4096, 0, sms) == 0
