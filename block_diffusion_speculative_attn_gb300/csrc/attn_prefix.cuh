@@ -49,12 +49,12 @@ __device__ __forceinline__ int request_prefix(const PrefixParams &x, int r, int 
 }
 
 // Group g's first request, tokens and shared tiles (no tokens when its bounds
-// are not within [0, bs]).
+// are not within [0, bs], or no row can hold its prefix).
 __device__ __forceinline__ void group_shape(const PrefixParams &x, int g, int B, int &r0,
                                             int &tokens, int &nt) {
     const int o0 = __ldg(x.group_offsets + g), o1 = __ldg(x.group_offsets + g + 1);
     const int P = __ldg(x.prefix_lens + g);
-    const bool ok = o0 >= 0 && o0 < o1 && o1 <= x.bs && P >= kBN;
+    const bool ok = o0 >= 0 && o0 < o1 && o1 <= x.bs && P >= kBN && P <= x.max_keys;
     r0 = ok ? o0 : 0;
     tokens = ok ? (o1 - o0) * B : 0;
     nt = ok ? P / kBN : 0;

@@ -45,6 +45,8 @@ struct PrefixParams {
     const int32_t *group_offsets, *prefix_lens;  // [ng + 1], [ng]
     int ng, bs;
     int npt;                    // whole tokens in a 128-row tile
+    int ctas;                   // CTAs of the prefix kernel, a slot each
+    long max_keys;              // that a block-table row can hold
     int32_t *head;              // {CTAs a team, or -1: the group offsets are wrong}
     float *row_lse, *row_o;     // [bs * B * Hq], [.., D]: first pieces
     uint32_t *row_teams;        // [bs * B * Hq]: the teams of a row's first and last piece

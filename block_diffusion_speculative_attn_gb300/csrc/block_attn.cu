@@ -1112,7 +1112,7 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                     pfx_T = __ldcg(prm.pfx.head);
                     pfx_ready = true;
                 }
-                bad = bad || pfx_T < 0;
+                bad = bad || (pfx_T != 1 && pfx_T != 2);
                 if (pfx_row.nt > 0 && valid_row && !bad) {
                     // the first piece's row is where the output row is, with the
                     // numbers of the teams that hold the others
@@ -1120,7 +1120,8 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                     float ls = __ldcg(prm.pfx.row_lse + e.orow);
                     const uint32_t teams = __ldcg(prm.pfx.row_teams + e.orow);
                     load_row(prm.pfx.row_o + e.orow * D + half * OC, po);
-                    const int q1 = (int)(teams & 0xffffu);
+                    // (a prefix kernel that gave up leaves any numbers here)
+                    const int q1 = min((int)(teams & 0xffffu), prm.pfx.ctas / pfx_T - 1);
                     for (int q = (int)(teams >> 16);;) {
                         if (ls == INFINITY) bad = true;  // a page outside the pool
                         else fold(ls, po);
@@ -1932,6 +1933,8 @@ int launch_prefix_attn(const AttnArgs &a, const int32_t *group_offsets,
     x.ng = num_groups;
     x.bs = b.bs;
     x.npt = kPrefixRows / (b.Hq / b.Hkv);
+    x.ctas = prefix_grid(plan.attn.grid);
+    x.max_keys = (long)b.max_pages * b.page_size;
     x.head = reinterpret_cast<int32_t *>(ws + plan.off_head);
     x.row_teams = reinterpret_cast<uint32_t *>(ws + plan.off_row_teams);
     x.row_lse = reinterpret_cast<float *>(ws + plan.off_row_lse);

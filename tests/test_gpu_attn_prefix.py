@@ -200,6 +200,9 @@ def test_bad_requests_get_zeros():
     c.prefix[0] = 731                   # longer than its requests
     expect(c, [0, 1, 2])
     c = make()
+    c.prefix[0] = 2 ** 31 - 1
+    expect(c, [0, 1, 2])
+    c = make()
     c.table[0, 3] = c.num_pages         # a shared page outside the pool
     expect(c, [0, 1, 2])
     c = make()
@@ -212,6 +215,29 @@ def test_bad_requests_get_zeros():
         c = make()
         c.offs = np.asarray(offs, np.int32)
         expect(c, [0, 1, 2, 3, 4])
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each."""
+    a = Case([3, 2], [700, 2560], 30, 8, 8, 2, 128, 64, seed=14)
+    b = Case([9], [1280], np.arange(9) * 9, 16, 32, 8, 128, 16, seed=15)
+    da, db = a.dev(), b.dev()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        for c, d, s in ((a, da, sa), (b, db, sb)):
+            with torch.cuda.stream(s):
+                lse = torch.empty((c.bs * c.B, c.Hq), device=DEV)
+                o = bdsa.block_attn_paged(d["q"], d["k"], d["v"], d["table"], d["seq"], B=c.B,
+                                          page_size=c.ps, scale=c.scale, mode=wl.VERIFY,
+                                          max_ctx_len=4096, num_pages=c.num_pages, lse=lse,
+                                          group_offsets=d["offs"], prefix_lens=d["prefix"])
+                outs.append((c, o, lse))
+    torch.cuda.synchronize()
+    want = {c: c.want(wl.VERIFY) for c in (a, b)}
+    for c, o, lse in outs:
+        assert_attn_close(o, want[c][0], lse, want[c][1])
 
 
 def test_workspace_reuse_graph_and_stream():
