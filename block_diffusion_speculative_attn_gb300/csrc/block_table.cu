@@ -14,7 +14,8 @@
 // scans all requests itself (the three prefix sums live in its shared memory)
 // and then takes its share of the requests, the popped pages, the pushed pages
 // and the tokens, each item finding its request by a binary search of the
-// scanned offsets.
+// scanned offsets.  Measured (launches in a graph): 32 requests of 16 tokens 4.9 us,
+// 4093 decode requests 8.7 us, 1024 prompts of 2.1 million tokens 18.6 us (17.9 MB).
 #include <cuda_runtime.h>
 #include <limits.h>
 
@@ -299,10 +300,12 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableArg
 int launch_block_table(const TableArgs &a, int num_sms, cudaStream_t stream) {
     const size_t smem = (size_t)3 * (a.bs + 1) * sizeof(int);
     // past the default 48 KB of shared memory (static and dynamic together), on
-    // this device
+    // this device; the same limit in every call, so that host threads do not undo
+    // one another's
+    constexpr int kMost = 3 * (BDSA_TABLE_MAX_REQUESTS + 1) * (int)sizeof(int);
     if (smem > 44 * 1024 &&
         cudaFuncSetAttribute(block_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem) != cudaSuccess)
+                             kMost) != cudaSuccess)
         return BDSA_CUDA_ERROR;
     // Every CTA repeats the scan, so no more of them than the items fill: one
     // a 4096 tokens (two rounds of a CTA's threads) or 512 requests.

@@ -31,6 +31,14 @@
 // the tensor cores -- while one tile's PV and next S run (1024 cycles at D =
 // 128), the other's softmax runs on the ALUs -- and share every K and V tile in
 // shared memory.  O is rescaled in TMEM only when a row's max grows by 2^8.
+//
+// Measured, with the block kernel behind it: 8 verify requests of 16 tokens and 64
+// heads over 131072 shared keys 357-368 us for 554 GFLOP, 1.51-1.55 PFLOP/s (0.79 to
+// 0.81 of the measured bf16 rate), a key tile of a pair every 1.65 us: a row tile's
+// chain of S, its maximum, the exponentials and P is longer than the other tile's
+// MMAs.  32 requests of 16 tokens and 32 heads over 4096 keys 70 us (every key
+// attended by every request itself: 86 us), 64 single tokens over 2048 keys 66 us
+// (119): there the start, a piece's end and the block kernel's short units count.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -31,13 +31,23 @@
 //                  (the k-th largest of them is at most the k-th largest logit,
 //                  and their weights bound the weight above a pivot from below);
 //                  the few logits above it are sorted and cut exactly.
-//                  Otherwise (more than kListMax candidates: flat rows, long runs
-//                  of ties; no active filter) radix selection on the logits'
+//                  A flat row's nucleus (top-p alone, more than kListMax
+//                  candidates) is cut the same way in a window around the cut
+//                  that one counting pass finds.  Otherwise (large k, long runs
+//                  of ties, no active filter) radix selection on the logits'
 //                  ordered bit patterns: each level is a histogram (count and
 //                  weight) over the current key range, summed over the cluster
 //                  through distributed shared memory; the bin that holds the cut
 //                  becomes the next range, until it is a single key.  These
 //                  passes read the row again, mostly from L2.
+// Measured: sample_full, 480 bf16 rows of 151936 to probs and tokens, 167 us for
+// 438 MB (2.6 TB/s): the exponentials' packed-fp32 instructions and then the
+// second pass's trip through L2, one after the other in a CTA and only in part
+// under the other CTA of the SM.  sample_cut, 512 fp32 rows of 151936, every filter,
+// 120 us for 622 MB (5.2 TB/s, 0.77 of a plain copy's rate): the stream of the row
+// and the zeros; two waves of CTAs, the second two thirds full.  61 fp16 rows of
+// 100003, top-p over thousands, 63 us: three passes over resident slices and a
+// dozen cluster-wide steps.  16 fp32 rows of 1000, 11 us: those steps alone.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -2008,10 +2018,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
     cluster_wait_reads();
 }
 
+// Slices that stay in shared memory: two of them fit an SM.
+constexpr size_t kMaxResident = 72 * 1024;
+
 template <typename K>
 int launch_cluster(K *kernel, const SampleArgs &a, int threads, size_t smem, cudaStream_t stream) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
+    // (the same limit in every call, so that host threads do not undo one another's)
+    if (smem > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kMaxResident) != cudaSuccess)
         return BDSA_CUDA_ERROR;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long)a.bs * a.B * a.ncta));
@@ -2050,9 +2064,9 @@ int launch_typed(const SampleArgs &in, int num_sms, cudaStream_t stream) {
         return launch_cluster(sample_full_kernel<T>, a, kThreads, 0, stream);
     }
     set_slices(ncta);
-    // slices two of which fit an SM stay there for the later passes
+    // small slices stay in shared memory for the later passes
     const size_t smem = (size_t)a.slice * sizeof(T) + 16;
-    if (smem <= 72 * 1024)
+    if (smem <= kMaxResident)
         return launch_cluster(sample_cut_kernel<T, true>, a, kThreads, smem, stream);
     return launch_cluster(sample_cut_kernel<T, false>, a, kThreads, 0, stream);
 }
