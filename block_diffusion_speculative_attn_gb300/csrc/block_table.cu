@@ -308,7 +308,8 @@ int launch_block_table(const TableArgs &a, int num_sms, cudaStream_t stream) {
                              kMost) != cudaSuccess)
         return BDSA_CUDA_ERROR;
     // Every CTA repeats the scan, so no more of them than the items fill: one
-    // a 4096 tokens (two rounds of a CTA's threads) or 512 requests.
+    // a 4096 tokens (two rounds of a CTA's threads) or 512 requests (a CTA for every
+    // SM is 0.2 us faster on 32 and 4093 decode requests, and takes the whole GPU).
     const long by_tok = (a.max_tokens + 4095) / 4096, by_req = ((long)a.bs + 511) / 512;
     long grid = by_tok > by_req ? by_tok : by_req;
     if (grid > num_sms) grid = num_sms;

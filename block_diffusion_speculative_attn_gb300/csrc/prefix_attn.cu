@@ -37,7 +37,7 @@
 // 0.81 of the measured bf16 rate), a key tile of a pair every 1.65 us: a row tile's
 // chain of S, its maximum, the exponentials and P is longer than the other tile's
 // MMAs.  32 requests of 16 tokens and 32 heads over 4096 keys 70 us (every key
-// attended by every request itself: 86 us), 64 single tokens over 2048 keys 66 us
+// attended by every request itself: 86 us), 64 single tokens over 2048 keys 64 us
 // (119): there the start, a piece's end and the block kernel's short units count.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -326,8 +326,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
             c2s += sch->wsum2[1][w];
         }
         // Teams of two unless the pairs they leave without a partner cost more
-        // than 1/16.
-        const int T = 2 * c2s <= c1s + c1s / 16 ? 2 : 1;
+        // than 1/16 (131072 shared keys: 360 us, teams of one 395; 32 requests
+        // behind 4096: 71 against 75; a tile is 1/8 shorter), or where the pieces
+        // are so few that the partners would be idle (64 tokens behind 2048: 65
+        // against 67).
+        const bool few = c1s / kPrefixMinCost <= gridDim.x / 2;
+        const int T = few || 2 * c2s <= c1s + c1s / 16 ? 2 : 1;
         const long long Wc = T == 2 ? c2s : c1s;
         long long sum = 0;
         for (int g = i0; g < i1; ++g) sum += cost(g, T);
