@@ -404,11 +404,12 @@ __device__ __forceinline__ int warp_of_target(const DrawShared &d, uint64_t targ
 // One step of the draw by the whole CTA: every thread brings the weights q[4] of
 // four successive indices (their sum s4, the first at index idx) in thread
 // order; before grows by the step's weight.  The thread that reaches the target
-// writes its token; until then each step's last positive weight does.
-__device__ __forceinline__ void draw_in_block(DrawShared &d, uint64_t target,
+// writes its token; until then each step's last positive weight does.  True when
+// the step has one, or the target was reached before it (uniform).
+__device__ __forceinline__ bool draw_in_block(DrawShared &d, uint64_t target,
                                               uint64_t &before, const uint64_t (&q)[4],
                                               uint64_t s4, int idx, int32_t *token) {
-    if (before > target) return;  // (uniform)
+    if (before > target) return true;  // (uniform)
     const int tid = threadIdx.x;
     if (tid == 0) d.last = -1;
     const uint64_t inc = block_scan64(s4, d.scan);
@@ -416,6 +417,7 @@ __device__ __forceinline__ void draw_in_block(DrawShared &d, uint64_t target,
     if (tid == kThreads - 1) d.step = inc;
     __syncthreads();
     const uint64_t step = d.step;
+    const bool some = d.last >= 0;
     const bool hit = before + inc > target && before + inc - s4 <= target;
     const bool rest = before + step <= target && tid == d.last;
     if (hit || rest) {
@@ -430,6 +432,7 @@ __device__ __forceinline__ void draw_in_block(DrawShared &d, uint64_t target,
     }
     before += step;
     __syncthreads();
+    return some;
 }
 
 // floor(u * total), below total; u outside [0, 1) is clamped.
@@ -585,6 +588,50 @@ __device__ __noinline__ uint64_t sum_segment(const FullRow<T> &row, const Span &
     for (int x = sg.tail0 + lane; x < sg.tail1; x += 32)
         sum += weight(row.value(__ldg(row.g + x)), rs, tab, wf);
     return sum;
+}
+
+// The first index of the row at or behind x1 whose weight is not zero in units, or
+// else the last such below x0 (the row's largest has one).  By the whole CTA, the
+// row g of V logits.
+template <typename T>
+__device__ __noinline__ int nearest_weight(const typename Logit<T>::Raw *g, int V, int x0, int x1,
+                                           bool inf, const RowScale &rs, const ExpTable &tab,
+                                           int *scratch) {
+    using L = Logit<T>;
+    constexpr int kEach = 8, kStep = kEach * kThreads;
+    const int tid = threadIdx.x;
+    auto has = [&](int x) {
+        float v = clean(L::wide(__ldg(g + x))), wf;
+        if (inf) v = if_inf(v);
+        return weight(v, rs, tab, wf) != 0;
+    };
+    for (int base = x1; base < V; base += kStep) {
+        int at = INT_MAX;
+        for (int k = kEach - 1; k >= 0; --k) {
+            const int x = base + k * kThreads + tid;
+            if (x < V && has(x)) at = x;
+        }
+        if (!__syncthreads_or(at < INT_MAX)) continue;
+        if (tid == 0) *scratch = INT_MAX;
+        __syncthreads();
+        if (at < INT_MAX) atomicMin(scratch, at);
+        __syncthreads();
+        return *scratch;
+    }
+    for (int end = x0; end > 0; end -= kStep) {
+        int at = -1;
+        for (int k = kEach - 1; k >= 0; --k) {
+            const int x = end - 1 - k * kThreads - tid;
+            if (x >= 0 && has(x)) at = x;
+        }
+        if (!__syncthreads_or(at >= 0)) continue;
+        if (tid == 0) *scratch = -1;
+        __syncthreads();
+        if (at >= 0) atomicMax(scratch, at);
+        __syncthreads();
+        return *scratch;
+    }
+    return -1;  // (never)
 }
 
 template <typename T>
@@ -788,11 +835,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_full_kernel(const SampleAr
         const int w = warp_of_target(sm.draw, target, before);
         if (w >= 0) {
             // in warp w's segment of this slice: its weights again, four positions a
-            // thread (single weights round to units, so the last positive one takes
-            // a target past their sum)
+            // thread.  Single weights round to units, the segment's sum as a whole: a
+            // target past the rounded ones goes to the segment's last that is not
+            // zero, and where all of them are zero (a logit leads by 29 nats and more)
+            // to the row's next that is not, or the last.
             const Segment d = segment_of(sp, row.len, w);
             const int x0 = d.head1 > d.head0 ? 0 : sp.head + d.v0 * kVec;
             const int x1 = d.tail1 > d.tail0 ? row.len : sp.head + d.v1 * kVec;
+            bool drawn = false;
             for (int base = x0; base < x1; base += 4 * kThreads) {
                 const int x = base + 4 * tid;
                 uint64_t q[4], s4 = 0;
@@ -802,7 +852,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_full_kernel(const SampleAr
                     q[k] = x + k < x1 ? weight(row.value(__ldg(row.g + x + k)), rs, sm.tab, wf) : 0;
                     s4 += q[k];
                 }
-                draw_in_block(sm.draw, target, before, q, s4, e0 + x, a.tokens + rowi);
+                drawn |= draw_in_block(sm.draw, target, before, q, s4, e0 + x, a.tokens + rowi);
+            }
+            if (!drawn) {  // (uniform)
+                const int x = nearest_weight<T>(row.g - e0, a.V, e0 + x0, e0 + x1, row.inf, rs,
+                                                sm.tab, &sm.draw.last);
+                if (tid == 0) a.tokens[rowi] = x;
             }
         }
     }

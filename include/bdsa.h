@@ -624,9 +624,11 @@ int32_t bdsa_block_table_update(const int32_t *seq_lens, const int32_t *new_lens
  * -1 and zero probs and is reported (BDSA_DEVICE_OUT_OF_RANGE).  u outside
  * [0, 1) is clamped (NaN: 0).
  * Arithmetic: weights to about 2^-30 of themselves, summed as integers in units
- * of 2^-41 of the largest (a weight below half a unit counts as zero in the
- * cuts and the draw); probs carry three fp32 roundings.  A call repeats itself to
- * the bit; another num_sms may round the sums apart by some units.
+ * of 2^-41 of the power of two above the largest (a weight below half a unit is
+ * never drawn, and counts as zero in the cuts); a sum is exact to half a unit a
+ * logit, so a draw that falls between two tokens with weight, into the share of
+ * those below half a unit, takes either.  probs carry three fp32 roundings.  A call
+ * repeats itself to the bit; another num_sms may round the sums apart by some units.
  * tokens ([bs, B]) or probs may be NULL, not both; u is needed for tokens.
  * probs rows must not overlap.  Supported: V <= 2^21, bs * B <= 2^26; rows may
  * start at any element.  One launch, no workspace; the memory from the first to
