@@ -1405,6 +1405,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
         // ---- pivot: nothing below it is kept
         float pivot = -INFINITY;
         bool list = true;
+        bool guess = false;  // the pivot is where top-p's estimate ended
         // (top-p within top-k takes its share of all k, min-p's losers included)
         const bool by_m = use_m && !(use_k && use_p);
         if (by_m) {
@@ -1487,6 +1488,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
                 hi = nhi;
             }
             if (use_k) pivot_k = lo;
+            guess = !use_k && lo > pivot;
             if (lo > -INFINITY) pivot = fmaxf(pivot, lo);
             else list = by_m || a.V <= kListMax;
             // (every maximum at or above the pivot brings a candidate at least)
@@ -1563,8 +1565,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
                 const uint64_t base = use_k ? cum[nk - 1] : all_sum;
                 const uint64_t goal =
                     top_p > 0.f ? max((uint64_t)1, scaled(top_p, base, true)) : 1;
-                // (the list may stop short of the goal only when the pivot of
-                // min-p cut it: min-p then keeps no more than the list)
+                // (the list may stop short of the goal: where the pivot is
+                // min-p's, which then keeps no more than the list, or by the
+                // estimate, which is caught below)
                 int below = 0;
                 for (int x = tid; x < nk; x += kThreads) below += cum[x] < goal;
                 below = __reduce_add_sync(kAll, below);
@@ -1578,7 +1581,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
                 __syncthreads();
                 if (use_p) keep = min(keep, sm.n_below + 1);
                 if (use_m) keep = min(keep, sm.n_min);
-                if (use_p && !use_k && !use_m && sm.n_below == n) list = false;  // short
+                // all of the list is below the goal: it is the answer only if min-p
+                // ends inside it, or set the pivot
+                if (use_p && !use_k && sm.n_below == n &&
+                    (!use_m || (guess && sm.n_min == n)))
+                    list = false;
             }
             keep = max(keep, 1);
             if (list) {
