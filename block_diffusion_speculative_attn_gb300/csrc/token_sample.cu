@@ -1409,9 +1409,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_cut_kernel(const SampleArg
         // (top-p within top-k takes its share of all k, min-p's losers included)
         const bool by_m = use_m && !(use_k && use_p);
         if (by_m) {
-            // w >= m iff l >= lmax + T ln m, less the rounding of both sides
+            // w >= m iff l >= lmax + T ln m, less the rounding of both sides: the
+            // logarithm's, 2^-21 absolute near m = 1, counts T times
             const float t = __logf(fminf(min_p, 1.f)) / (rs.ch * 0.693147181f);
-            pivot = rs.lmax + t * (t < 0.f ? 1.0001f : 1.f) - 1e-4f * fabsf(rs.lmax) - 1e-5f;
+            pivot = rs.lmax + t * (t < 0.f ? 1.0001f : 1.f) - 1e-4f * fabsf(rs.lmax) - 1e-5f -
+                    1e-6f * temp;
         }
         if ((use_k || use_p) && a.V > kListMax / 4) {
             // A histogram of the part maxima over equal bins of [lowest, lmax],
