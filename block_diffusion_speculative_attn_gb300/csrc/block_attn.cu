@@ -1182,7 +1182,8 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
             }
             okg = __all_sync(0xffffffffu, okg);
             bad = __any_sync(0xffffffffu, bad);
-            const bool good = !bad && den > 0.f;
+            // kPre: a NaN score in any piece makes den NaN, which goes to the output
+            const bool good = !bad && (den > 0.f || (kPre && isnan(den)));
             const float inv_den = good ? 1.f / den : 0.f;
             // (a bad piece's partial may hold anything, NaN included)
 #pragma unroll
@@ -1336,11 +1337,13 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                     lacc[1] = f2_mul(lacc[1], a2);
                 }
                 uint32_t pk[NC / 2];
-                if (m_used == -INFINITY) {
+                // (kPre: a row whose only scores so far are NaN keeps them, since the
+                // prefix may hold the rest of its keys)
+                if (!kPre && m_used == -INFINITY) {
 #pragma unroll
                     for (int c = 0; c < NC / 2; ++c) pk[c] = 0u;
                 } else {
-                    const float neg_m = -m_used;
+                    const float neg_m = kPre && m_used == -INFINITY ? 0.f : -m_used;
                     const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(neg_m, neg_m);
 #pragma unroll
                     for (int c = 0; c < NC / 2; ++c) {
@@ -1464,6 +1467,7 @@ __global__ void __launch_bounds__(kAppend ? Cfg<D, M, M == 128>::kThreadsAppend
                 e.ob = ob;
                 e.inv_l = lr > 0.f ? 1.f / lr : 0.f;
                 e.lse2 = l > 0.f ? m_used + log2f(l) : -INFINITY;
+                if (kPre && isnan(l)) e.lse2 = l;  // (for the join)
                 e.complete = pc.a == 0 && pc.e == pc.nt;
                 e.owner = kOwner && prm.owner_merge && pc.a == 0 && pc.e < pc.nt;
                 // every warp checked every page of the piece

@@ -741,10 +741,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::OE + t));
-            // a bad piece is marked by +inf
+            // a bad piece is marked by +inf; a NaN score leaves NaN
             if (real) {
                 (slot0 ? prm.x.slot_lse : prm.x.row_lse)[dst] =
-                    bad ? INFINITY : (l > 0.f ? m_used + log2f(l) : -INFINITY);
+                    bad ? INFINITY : l > 0.f ? m_used + log2f(l) : isnan(l) ? l : -INFINITY;
                 if (!slot0) prm.x.row_teams[dst] = teams;
             }
             if (bad && lane == 0) report_status(prm.dev_status, BDSA_DEVICE_OUT_OF_RANGE);

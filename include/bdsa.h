@@ -519,6 +519,8 @@ int32_t bdsa_tree_accept(const int32_t *block_ids, const int32_t *parent, const 
  * group whose shared pages (up to the 128-key limit) are outside the pool or
  * the row, gets out = 0 and lse = -inf; group_offsets that do not run up from 0
  * to bs give that for every request; all report BDSA_DEVICE_OUT_OF_RANGE.
+ * A row with a NaN score (a NaN in its query or in a key it sees, a score of +inf)
+ * gets out = lse = NaN; it is not reported.
  * Two launches (the prefix of all groups, then the rest, which folds the
  * prefix's share in), chained with programmatic dependent launch.  num_sms
  * above the device's SM count counts as the device's.
