@@ -5,15 +5,14 @@
 // Group g holds requests [off[g], off[g + 1]) and shares its first
 // P' = floor(P_g / 128) * 128 keys.  Its query rows of one KV head, (token, head
 // of the group) in token order, are cut into tiles of npt whole tokens (at most
-// kPrefixRows rows), two tiles to a pair.  CTAs work in teams of T (1 or
-// 2, a cluster): a team takes T pairs of one KV head over the same keys, a pair a
-// member.  A unit is a team's T pairs over all P'
-// keys, numbered (group, KV head, T pairs); each is charged kPrefixUnitCost
-// virtual tiles and its P' / 128 real ones, and team b of S takes the cost range
-// [b Wc / S, (b + 1) Wc / S).  The piece that holds a unit's first tile goes to
-// per-row buffers (a row has one such piece), with the numbers of the teams that
-// hold the unit's first and last tile; any other piece is the first of its CTA and
-// goes to that CTA's slot.
+// kPrefixRows rows), two tiles to a pair.  CTAs work in teams of T (1 or 2): a team
+// takes T pairs of one KV head over the same keys, a pair a member.  A unit is a
+// team's T pairs over all P' keys, numbered (group, KV head, T pairs); each is
+// charged kPrefixUnitCost virtual tiles and its P' / 128 real ones, and team b of S
+// takes the cost range [b Wc / S, (b + 1) Wc / S).  The piece that holds a unit's
+// first tile goes to per-row buffers (a row has one such piece), with the numbers of
+// the teams that hold the unit's first and last tile; any other piece is the first of
+// its CTA and goes to that CTA's slot.
 #pragma once
 
 #include "attn_common.cuh"
@@ -27,11 +26,9 @@ constexpr int kPrefixRows = 128;     // query rows of a tile
 // four the cases below are within 3%).
 constexpr int kPrefixUnitCost = 2;
 // A team takes at least this cost: below it the pieces' partials and their merge
-// cost more than the CTAs gain (64 single tokens of 32 heads behind 2048 keys 69 us;
-// with 4 tiles 72, 3: 73, 2: 76, 10: 76, 20: 91; longer prefixes do not care).
+// cost more than the CTAs gain (64 single tokens of 32 heads behind 2048 keys 63 us a
+// call; with 3 and 4 tiles 66, 8: 67, 12: 69; longer prefixes do not care).
 constexpr int kPrefixMinCost = 6;
-// The prefix kernel's CTAs: whole clusters of two.
-__host__ __device__ constexpr int prefix_grid(int ctas) { return ctas < 2 ? 2 : ctas & ~1; }
 
 // The keys of request r (length L) its group shares, in whole tiles; g its
 // group, or -1 (and 0 keys) when the groups do not place it or its prefix is

@@ -1906,7 +1906,7 @@ PrefixPlan prefix_plan(int bs, int B, int Hq, int Hkv, int D, int num_sms) {
     p.attn = attn_plan(bs, B, Hq, Hkv, D, 0, num_sms);
     size_t off = p.attn.workspace;
     const size_t rows = (size_t)bs * B * Hq;
-    const size_t slots = (size_t)prefix_grid(p.attn.grid) * 2 * kPrefixRows;
+    const size_t slots = (size_t)p.attn.grid * 2 * kPrefixRows;
     auto take = [&](size_t bytes) {
         const size_t at = off;
         off += align256(bytes);
@@ -1937,7 +1937,7 @@ int launch_prefix_attn(const AttnArgs &a, const int32_t *group_offsets,
     x.ng = num_groups;
     x.bs = b.bs;
     x.npt = kPrefixRows / (b.Hq / b.Hkv);
-    x.ctas = prefix_grid(plan.attn.grid);
+    x.ctas = plan.attn.grid;
     x.max_keys = (long)b.max_pages * b.page_size;
     x.head = reinterpret_cast<int32_t *>(ws + plan.off_head);
     x.row_teams = reinterpret_cast<uint32_t *>(ws + plan.off_row_teams);

@@ -17,10 +17,9 @@
 // and persistent CTAs take equal cost ranges.  A piece leaves its rows' o / l
 // and log2-sum-exp in fp32.
 //
-// A team of two CTAs is a thread-block cluster whose members load half of every K
-// and V tile each and multicast it to both: the keys cross from L2 once a team
-// (with a load a CTA, 64 KB a tile, the SMs' 7.1 TB/s together bound the tile
-// loop).
+// A team of two CTAs takes two units' rows over the same keys, each loading every
+// tile for itself: they are at the same keys at about the same time, so that those
+// come from HBM once a team.
 //
 // Inside a CTA (12 warps): warps 0-3 and 4-7 are the softmax of the two row
 // tiles, one thread a row; then a K producer (also Q), a V producer and an MMA
@@ -33,12 +32,13 @@
 // shared memory.  O is rescaled in TMEM only when a row's max grows by 2^8.
 //
 // Measured, with the block kernel behind it: 8 verify requests of 16 tokens and 64
-// heads over 131072 shared keys 357-368 us for 554 GFLOP, 1.51-1.55 PFLOP/s (0.79 to
-// 0.81 of the measured bf16 rate), a key tile of a pair every 1.65 us: a row tile's
-// chain of S, its maximum, the exponentials and P is longer than the other tile's
-// MMAs.  32 requests of 16 tokens and 32 heads over 4096 keys 70 us (every key
-// attended by every request itself: 86 us), 64 single tokens over 2048 keys 64 us
-// (119): there the start, a piece's end and the block kernel's short units count.
+// heads over 131072 shared keys 362 us for 554 GFLOP when the GPU is cool, 368-392 us
+// call after call, 1.41-1.53 PFLOP/s (0.74 to 0.80 of the measured bf16 rate), a key
+// tile of a pair every 1.65 us: a row tile's chain of S, its maximum, the
+// exponentials and P is longer than the other tile's MMAs.  32 requests of 16 tokens
+// and 32 heads over 4096 keys 69 us (every key attended by every request itself: 86
+// us), 64 single tokens over 2048 keys 63 us (119): there the start, a piece's end
+// and the block kernel's short units count.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -151,7 +151,7 @@ struct PWalk {
             pc.r0 = r0;
             pc.tok0 = r0 * p.B + pair * 2 * p.x.npt;
             pc.ntok = tokens - pair * 2 * p.x.npt;
-            // (no tokens left for this member: it still loads its half of the keys)
+            if (pc.ntok <= 0) continue;  // no tokens left for this member
             pc.a = a;
             pc.e = e;
             pc.nt = nt;
@@ -171,30 +171,6 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-// A tile load to the same place in both CTAs of the cluster, completing on the
-// barrier at the same place in each.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap, int32_t x,
-                                                 int32_t y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "h"((uint16_t)3)
-        : "memory");
-}
-// umma_commit to the barrier at the same place in both CTAs of the cluster.
-__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
-}
-__device__ __forceinline__ void pair_sync() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // One lane of the (converged) warp, always the same.
@@ -220,7 +196,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 }
 
 template <int D>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1)
+__global__ void __launch_bounds__(PCfg<D>::kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PParams prm) {
@@ -252,11 +228,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
         }
         for (int k = 0; k < C::NK; ++k) {
             mbar_init(bar(C::KF + k), 1);
-            mbar_init(bar(C::KE + k), 4);
+            mbar_init(bar(C::KE + k), 2);
         }
         for (int k = 0; k < C::NV; ++k) {
             mbar_init(bar(C::VF + k), 1);
-            mbar_init(bar(C::VE + k), 4);
+            mbar_init(bar(C::VE + k), 2);
         }
         mbar_init(bar(C::DR), 1);
         mbar_init(bar(C::DR + 1), 1);
@@ -279,7 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
     }
     fence_proxy_async_smem();
     tc_fence_before();
-    pair_sync();  // (both CTAs' barriers are set up before either is signalled)
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sch->tmem;
 
@@ -326,12 +302,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
             c2s += sch->wsum2[1][w];
         }
         // Teams of two unless the pairs they leave without a partner cost more
-        // than 1/16 (131072 shared keys: 360 us, teams of one 395; 32 requests
-        // behind 4096: 71 against 75; a tile is 1/8 shorter), or where the pieces
-        // are so few that the partners would be idle (64 tokens behind 2048: 65
-        // against 67).
-        const bool few = c1s / kPrefixMinCost <= gridDim.x / 2;
-        const int T = few || 2 * c2s <= c1s + c1s / 16 ? 2 : 1;
+        // than 1/16 (131072 shared keys: 389 us, teams of one 428; 32 requests of 16
+        // tokens behind 4096: 70 against 71.5; with 64 single tokens behind 2048 half
+        // of the CTAs would be without work: 79 against 63).
+        const int T = gridDim.x >= 2 && 2 * c2s <= c1s + c1s / 16 ? 2 : 1;
         const long long Wc = T == 2 ? c2s : c1s;
         long long sum = 0;
         for (int g = i0; g < i1; ++g) sum += cost(g, T);
@@ -398,8 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
                 const uint32_t dst0 = sbase + (is_k ? C::kOffK : C::kOffV);
                 const void *tmap = is_k ? (const void *)&tm_k : (const void *)&tm_v;
                 const int rows_box = prm.box_rows;
-                // a team's members each load half of a tile, to both
-                const int nbox = kBN / walk.T / rows_box, half = walk.member * (kBN / 2);
+                const int nbox = kBN / rows_box;
                 const long ps = 1L << prm.log2_ps;
                 long g = 0;
                 int kq[2] = {0, 0};  // pieces each row tile took part in
@@ -430,7 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
 #pragma unroll
                         for (int bx = 0; bx < kMaxBoxes; ++bx) {
                             if (bx >= nbox) break;
-                            const long t = t0 + half + (long)bx * rows_box;
+                            const long t = t0 + (long)bx * rows_box;
                             const long page = t >> prm.log2_ps;
                             const int32_t id = page < prm.max_pages ? __ldg(bt + page) : -1;
                             slot[bx] = id >= 0 && id < prm.num_pages
@@ -445,16 +418,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
 #pragma unroll
                         for (int bx = 0; bx < kMaxBoxes; ++bx) {
                             if (bx >= nbox) break;
-                            for (int c = 0; c < C::DH; ++c) {
-                                const uint32_t dst = dst0 + st * C::kTile + c * C::kSlab +
-                                                     (half + bx * rows_box) * 128;
-                                if (walk.T == 2)
-                                    tma_load_2d_pair(dst, tmap, pc.h * D + c * 64, slot[bx],
-                                                     bar(FULL + st));
-                                else
-                                    tma_load_2d(dst, tmap, pc.h * D + c * 64, slot[bx],
-                                                bar(FULL + st));
-                            }
+                            for (int c = 0; c < C::DH; ++c)
+                                tma_load_2d(dst0 + st * C::kTile + c * C::kSlab +
+                                                bx * rows_box * 128,
+                                            tmap, pc.h * D + c * 64, slot[bx], bar(FULL + st));
                         }
                     }
                 }
@@ -514,27 +481,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
                 // ring positions and their phases
                 int ks = 0, vs = 0;
                 uint32_t kph = 0, vph = 0;
-                // a ring slot's release: to both members of a team, which each
-                // write the other's half; twice to itself without one (four
-                // arrivals free a slot)
-                auto release = [&](int i) {
-                    if (!leader) return;
-                    if (walk.T == 2) {
-                        umma_commit_pair(bar(i));
-                    } else {
-                        umma_commit(bar(i));
-                        umma_commit(bar(i));
-                    }
-                };
                 auto next_k = [&] {
-                    release(C::KE + ks);
+                    commit(C::KE + ks);
                     if (++ks == C::NK) {
                         ks = 0;
                         kph ^= 1;
                     }
                 };
                 auto next_v = [&] {
-                    release(C::VE + vs);
+                    commit(C::VE + vs);
                     if (++vs == C::NV) {
                         vs = 0;
                         vph ^= 1;
@@ -753,7 +708,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<D>::kThreads, 1
     }
 
     tc_fence_before();
-    pair_sync();  // (neither leaves while the other may still write or signal here)
+    __syncthreads();
     if (warp == C::kMma0) {
         __syncwarp();
         tc_fence_after();
@@ -783,7 +738,7 @@ int launch_partials(const AttnArgs &a, const PrefixParams &x, int grid, cudaStre
             CUDA_SUCCESS)
             return BDSA_CUDA_ERROR;
     }
-    const int box_rows = a.page_size < kBN / 2 ? a.page_size : kBN / 2;
+    const int box_rows = a.page_size < kBN ? a.page_size : kBN;
     for (int which = 0; which < 2; ++which) {
         cuuint64_t dims[2] = {(cuuint64_t)a.Hkv * D, (cuuint64_t)a.num_pages * a.page_size};
         cuuint64_t strides[1] = {(cuuint64_t)a.Hkv * D * 2};
@@ -814,7 +769,7 @@ int launch_partials(const AttnArgs &a, const PrefixParams &x, int grid, cudaStre
     if (cudaFuncSetAttribute(prefix_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmem) != cudaSuccess)
         return BDSA_CUDA_ERROR;
-    return launch_pdl(prefix_attn_kernel<D>, dim3(prefix_grid(grid)), dim3(C::kThreads),
+    return launch_pdl(prefix_attn_kernel<D>, dim3(grid), dim3(C::kThreads),
                       (size_t)C::kSmem, stream, tq, tk, tv, p) == cudaSuccess
                ? BDSA_OK
                : BDSA_CUDA_ERROR;
