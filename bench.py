@@ -45,10 +45,11 @@ METRIC = "draft/verify block-attn query tokens/s + % HBM roofline; accept rows/s
 # written (the 64-row tile merges its cut units inside the launch: no merge
 # kernel).  Valid only for the kernel sources it was taken on: reported as
 # null once they change.
-ATTN_TRAFFIC = {"workload": "qwen3_8b_verify", "bytes_per_call": 313.04e6,
-                "sources_sha256": "52d7a751db9005cea75463ba2c2cf87513cdeffcd4728d33e99fa757d08b8217"}
-ATTN_SOURCES = ("block_diffusion_speculative_attn_gb300/csrc/block_attn.cu",
-                "block_diffusion_speculative_attn_gb300/csrc/bdsa_device.cuh")
+ATTN_TRAFFIC = {"workload": "qwen3_8b_verify", "bytes_per_call": 313.03e6,
+                "sources_sha256": "d95c6adb379afd6381e7998f545b5063c4cd6df261aa3067eefd99392d2e3e7e"}
+ATTN_SOURCES = tuple("block_diffusion_speculative_attn_gb300/csrc/" + f for f in
+                     ("block_attn.cu", "attn_common.cuh", "attn_prefix.cuh", "bdsa_device.cuh",
+                      "bdsa_internal.h"))
 L2_FLUSH_BYTES = 512 << 20  # > 129 MB L2
 L2_CLEAN_BYTES = 256 << 20  # read after the flush: writes its dirty lines back
 
