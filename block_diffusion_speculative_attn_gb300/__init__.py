@@ -567,7 +567,8 @@ def block_table_update(seq_lens, new_lens, owned, block_table, free_pages, free_
     block_table int32 [bs, max_pages] and the ring free_pages int32 [num_pages] are
     updated in place; free_state int32 [2] = (head, count) of the ring.
 
-    total_tokens is the room for the new tokens (at least their number).  Returns
+    total_tokens is the room for the new tokens (at least their number; 0 for no
+    slots and positions, whatever the lengths).  Returns
     a dict of int32 tensors: owned [bs], free_state [2], cu_tokens [bs + 1],
     slot_map and positions [total_tokens]; pass it back as `out` to reuse them
     (owned and free_state must not be the inputs' memory).

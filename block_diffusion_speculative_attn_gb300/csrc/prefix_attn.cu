@@ -34,7 +34,7 @@
 // Measured, with the block kernel behind it: 8 verify requests of 16 tokens and 64
 // heads over 131072 shared keys 362 us for 554 GFLOP when the GPU is cool, 368-392 us
 // call after call, 1.41-1.53 PFLOP/s (0.74 to 0.80 of the measured bf16 rate), a key
-// tile of a pair every 1.65 us: a row tile's chain of S, its maximum, the
+// tile of a pair every 1.6 us: a row tile's chain of S, its maximum, the
 // exponentials and P is longer than the other tile's MMAs.  32 requests of 16 tokens
 // and 32 heads over 4096 keys 69 us (every key attended by every request itself: 86
 // us), 64 single tokens over 2048 keys 63 us (119): there the start, a piece's end

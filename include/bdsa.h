@@ -630,7 +630,8 @@ int32_t bdsa_block_table_update(const int32_t *seq_lens, const int32_t *new_lens
  * never drawn, and counts as zero in the cuts); a sum is exact to half a unit a
  * logit, so a draw that falls between two tokens with weight, into the share of
  * those below half a unit, takes either.  probs carry three fp32 roundings.  A call
- * repeats itself to the bit; another num_sms may round the sums apart by some units.
+ * repeats itself to the bit; another num_sms, or probs left out or wanted, may round
+ * the sums apart by some units.
  * tokens ([bs, B]) or probs may be NULL, not both; u is needed for tokens.
  * probs rows must not overlap.  Supported: V <= 2^21, bs * B <= 2^26; rows may
  * start at any element.  One launch, no workspace; the memory from the first to
