@@ -20,6 +20,11 @@ Calls (all asynchronous on the current stream):
   tree_accept       lossless tree acceptance walk (stochastic or greedy)
   block_table_update  block tables grown / shrunk from request lengths, slots of new tokens
   token_sample      logits -> p (temperature, top-k, top-p, min-p) and tokens from given uniforms
+  chunk_attn_paged  attention of a ragged batch of new tokens (prompt chunks, single tokens)
+  cache_write       the new tokens' keys and values into their cache slots
+  cache_fork        block tables continued from old rows: pages shared, copied, freed
+  cache_copy        pages copied in every layer's caches
+  cache_compact     kept rows moved to the front of their region in every layer's caches
 """
 from __future__ import annotations
 
@@ -44,7 +49,10 @@ EXPORTS = ("bdsa_status_string", "bdsa_version", "bdsa_prepare_block",
            "bdsa_idlm_accept", "bdsa_kv_materialize_workspace_bytes", "bdsa_kv_materialize",
            "bdsa_tree_prepare", "bdsa_block_attn_paged_tree", "bdsa_tree_accept",
            "bdsa_block_table_update", "bdsa_token_sample",
-           "bdsa_block_attn_prefix_workspace_bytes", "bdsa_block_attn_paged_prefix")
+           "bdsa_block_attn_prefix_workspace_bytes", "bdsa_block_attn_paged_prefix",
+           "bdsa_chunk_attn_workspace_bytes", "bdsa_chunk_attn_paged", "bdsa_cache_write",
+           "bdsa_cache_fork_workspace_bytes", "bdsa_cache_fork", "bdsa_cache_copy",
+           "bdsa_cache_compact")
 
 _lib = None
 
@@ -118,6 +126,22 @@ def lib() -> ctypes.CDLL:
     L.bdsa_token_sample.argtypes = [P, i32, i64, i64, P, P, P, P, P, i32, i32, i32, P, P, i64,
                                     i64, i32, P, P]
     L.bdsa_token_sample.restype = i32
+    L.bdsa_chunk_attn_workspace_bytes.argtypes = [i32] * 2
+    L.bdsa_chunk_attn_workspace_bytes.restype = sz
+    L.bdsa_chunk_attn_paged.argtypes = [P, i64, P, P, P, i32, i32, P, P, i32, i32, i32, i32, i32,
+                                        i32, f32, i32, P, P, P, sz, i32, P, P]
+    L.bdsa_chunk_attn_paged.restype = i32
+    L.bdsa_cache_write.argtypes = [P, i64, P, i64, P, i32, P, P, i32, i64, P, P]
+    L.bdsa_cache_write.restype = i32
+    L.bdsa_cache_fork_workspace_bytes.argtypes = [i32] * 3
+    L.bdsa_cache_fork_workspace_bytes.restype = sz
+    L.bdsa_cache_fork.argtypes = [P, P, P, P, i32, i32, i32, i32, i32, P, P, P, P, P, P, P, P, P,
+                                  P, sz, P, P]
+    L.bdsa_cache_fork.restype = i32
+    L.bdsa_cache_copy.argtypes = [P, i32, i64, i32, i32, P, P, P, i32, P, P]
+    L.bdsa_cache_copy.restype = i32
+    L.bdsa_cache_compact.argtypes = [P, i32, i64, i32, i32, P, i32, P, P, i32, i32, P, P]
+    L.bdsa_cache_compact.restype = i32
     _lib = L
     return L
 
@@ -651,3 +675,185 @@ def token_sample(logits, u=None, *, temperature=None, top_k=None, top_p=None, mi
             None if probs is None else probs.data_ptr(), psr, psi, sms,
             _arg(dev_status, "dev_status", i32, (1,), index))
     return tokens, probs
+
+
+# ---------------------------------------------------------------------------
+def _tokens(t, name: str, index: int, dtype=None):
+    """Token stride (elements) of a [T, heads, D] tensor on CUDA device `index`
+    whose heads are dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name} must be a tensor on cuda:{index}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have shape [tokens, heads, D], got {tuple(t.shape)}")
+    T, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name} must have dense heads")
+    return t.stride(0) if T > 1 else H * D
+
+
+def chunk_attn_workspace_bytes(D, sms: int = 0) -> int:
+    return int(lib().bdsa_chunk_attn_workspace_bytes(D, sms))
+
+
+def chunk_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *, page_size: int,
+                     scale: float, mask_block: int = 1, num_pages: int | None = None, out=None,
+                     lse=None, workspace=None, dev_status=None, sms: int = 0):
+    """bdsa_chunk_attn_paged.  q [T, Hq, D] bf16 (heads dense, any token stride);
+    caches [slots, Hkv, D] bf16 that hold the new tokens already; seq_lens int32
+    [bs], the tokens before them; cu_tokens int32 [bs + 1], the rows of q of each
+    request.  mask_block 1: token-causal; b: causal by blocks of b positions.
+
+    Returns out [T, Hq, D] bf16 (lse fp32 [T, Hq] is filled when given).  Rows of q
+    past the last request's leave their rows of out as they are.
+    """
+    _dev(block_table, "block_table", torch.int32)
+    index = block_table.get_device()
+    bs, max_pages = block_table.shape
+    bf16, i32 = torch.bfloat16, torch.int32
+    stride = _tokens(q, "q", index, bf16)
+    T, Hq, D = q.shape
+    if k_cache.dim() != 3 or k_cache.shape[2] != D:
+        raise ValueError(f"k_cache must have shape [slots, Hkv, {D}], got {tuple(k_cache.shape)}")
+    slots, Hkv = k_cache.shape[0], k_cache.shape[1]
+    if num_pages is None:
+        num_pages = slots // page_size
+    elif num_pages * page_size > slots:
+        raise ValueError(f"the caches hold fewer than {num_pages} pages")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=bf16, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(chunk_attn_workspace_bytes(D, sms or num_sms(q.device)),
+                                dtype=torch.uint8, device=q.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    _launch(lib().bdsa_chunk_attn_paged, "bdsa_chunk_attn_paged", index, q.data_ptr(), stride,
+            _arg(k_cache, "k_cache", bf16, (slots, Hkv, D), index),
+            _arg(v_cache, "v_cache", bf16, (slots, Hkv, D), index), block_table.data_ptr(),
+            max_pages, num_pages, _arg(seq_lens, "seq_lens", i32, (bs,), index),
+            _arg(cu_tokens, "cu_tokens", i32, (bs + 1,), index), bs, T, Hq, Hkv, D,
+            int(page_size), float(scale), int(mask_block),
+            _arg(out, "out", bf16, (T, Hq, D), index),
+            _arg(lse, "lse", torch.float32, (T, Hq), index), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), sms,
+            _arg(dev_status, "dev_status", i32, (1,), index))
+    return out
+
+
+def cache_write(k_new, v_new, slot_map, k_cache, v_cache, *, dev_status=None):
+    """bdsa_cache_write: k_cache[slot_map[t]] = k_new[t], and likewise v, for every
+    token; slots of -1 are skipped.  k_new, v_new [T, Hkv, D] (heads dense, any token
+    stride: slices of a fused projection), caches [slots, Hkv, D], one type."""
+    _dev(slot_map, "slot_map", torch.int32)
+    index, dtype = slot_map.get_device(), k_cache.dtype
+    ks, vs = (_tokens(t, n, index, dtype) for t, n in ((k_new, "k_new"), (v_new, "v_new")))
+    T, H, D = k_new.shape
+    if v_new.shape != k_new.shape or slot_map.shape != (T,):
+        raise ValueError(f"v_new must have shape {(T, H, D)} and slot_map {(T,)}, got "
+                         f"{tuple(v_new.shape)} and {tuple(slot_map.shape)}")
+    slots, e = k_cache.shape[0], k_cache.element_size()
+    _launch(lib().bdsa_cache_write, "bdsa_cache_write", index, k_new.data_ptr(), ks * e,
+            v_new.data_ptr(), vs * e, slot_map.data_ptr(), T,
+            _arg(k_cache, "k_cache", dtype, (slots, H, D), index),
+            _arg(v_cache, "v_cache", dtype, (slots, H, D), index), H * D * e, slots,
+            _arg(dev_status, "dev_status", torch.int32, (1,), index))
+
+
+FORK_KEYS = ("block_table", "owned", "shared", "free_state", "copy_src", "copy_dst", "copy_len")
+
+
+def cache_fork_workspace_bytes(bs_in, bs_out, num_pages) -> int:
+    return int(lib().bdsa_cache_fork_workspace_bytes(bs_in, bs_out, num_pages))
+
+
+def cache_fork(parent, keep_lens, block_table, owned, free_pages, free_state, *, page_size: int,
+               out=None, workspace=None, dev_status=None):
+    """bdsa_cache_fork: a new block table whose row r holds the first keep_lens[r]
+    tokens of row parent[r] of the old one (-1: empty).  parent, keep_lens int32 [n];
+    block_table int32 [bs, max_pages], owned int32 [bs]; the ring free_pages int32
+    [num_pages] is updated in place; free_state int32 [2] = (head, count).
+
+    Returns a dict of int32 tensors: block_table [n, max_pages], owned, shared,
+    copy_src, copy_dst, copy_len [n] (what cache_copy takes), free_state [2]; pass it
+    back as `out` to reuse them (none may be an input's memory).
+    """
+    _dev(block_table, "block_table", torch.int32)
+    _dev(parent, "parent", torch.int32)
+    index = block_table.get_device()
+    bs, max_pages = block_table.shape
+    i32, n, num_pages, dev = torch.int32, parent.numel(), free_pages.numel(), block_table.device
+    shapes = ((n, max_pages), (n,), (n,), (2,), (n,), (n,), (n,))
+    if out is None:
+        out = {k: torch.empty(s, dtype=i32, device=dev) for k, s in zip(FORK_KEYS, shapes)}
+        outs = [t.data_ptr() for t in out.values()]
+    else:
+        outs = [_arg(out[k], k, i32, s, index) for k, s in zip(FORK_KEYS, shapes)]
+    if workspace is None:
+        workspace = torch.empty(cache_fork_workspace_bytes(bs, n, num_pages), dtype=torch.uint8,
+                                device=dev)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    _launch(lib().bdsa_cache_fork, "bdsa_cache_fork", index,
+            _arg(parent, "parent", i32, (n,), index),
+            _arg(keep_lens, "keep_lens", i32, (n,), index), block_table.data_ptr(),
+            _arg(owned, "owned", i32, (bs,), index), max_pages, num_pages, bs, n, int(page_size),
+            _arg(free_pages, "free_pages", i32, (num_pages,), index),
+            _arg(free_state, "free_state", i32, (2,), index), *outs, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(),
+            _arg(dev_status, "dev_status", i32, (1,), index))
+    return out
+
+
+def _caches(caches, page_size: int, index: int):
+    """(pointers, number, bytes of a row, pages) of a sequence of [slots, ...]
+    tensors alike, or of one stacked tensor [n, slots, ...]."""
+    one = isinstance(caches, torch.Tensor)
+    if one and (caches.dim() < 3 or not caches.is_contiguous()):
+        raise ValueError("stacked caches must be a contiguous [n, slots, ...] tensor")
+    first = caches if one else caches[0] if len(caches) else None
+    if first is None:
+        return None, 0, 16, 1
+    if not first.is_cuda or first.get_device() != index:
+        raise ValueError(f"caches must be on cuda:{index}")
+    shape = first.shape[1:] if one else first.shape
+    row = first.element_size()
+    for d in shape[1:]:
+        row *= d
+    if one:
+        n, step = first.shape[0], row * shape[0]
+        at = range(first.data_ptr(), first.data_ptr() + n * step, step) if n * step else ()
+    else:
+        n = len(caches)
+        at = [_arg(t, "a cache", first.dtype, shape, index) for t in caches]
+    return (ctypes.c_void_p * n)(*at), n, row, shape[0] // int(page_size)
+
+
+def cache_copy(caches, copy_src, copy_dst, copy_len, *, page_size: int, dev_status=None):
+    """bdsa_cache_copy: the first copy_len[e] slots of page copy_src[e] to page
+    copy_dst[e], in every cache.  caches: a sequence of tensors [slots, ...] alike
+    (the keys and values of every layer), or one stacked tensor [n, slots, ...]."""
+    _dev(copy_src, "copy_src", torch.int32)
+    index, n, i32 = copy_src.get_device(), copy_src.numel(), torch.int32
+    ptrs, nc, row, pages = _caches(caches, page_size, index)
+    _launch(lib().bdsa_cache_copy, "bdsa_cache_copy", index, ptrs, nc, row, int(page_size), pages,
+            _arg(copy_src, "copy_src", i32, (n,), index),
+            _arg(copy_dst, "copy_dst", i32, (n,), index),
+            _arg(copy_len, "copy_len", i32, (n,), index), n,
+            _arg(dev_status, "dev_status", i32, (1,), index))
+
+
+def cache_compact(caches, block_table, seq_lens, path, *, page_size: int, dev_status=None):
+    """bdsa_cache_compact: position seq_lens[r] + path[r, i] moves to seq_lens[r] + i
+    for the entries of path (int32 [bs, width], tree_accept's) before the first -1,
+    in every cache (as in cache_copy)."""
+    _dev(block_table, "block_table", torch.int32)
+    _dev(path, "path", torch.int32)
+    index, i32 = block_table.get_device(), torch.int32
+    bs, max_pages = block_table.shape
+    ptrs, nc, row, pages = _caches(caches, page_size, index)
+    _launch(lib().bdsa_cache_compact, "bdsa_cache_compact", index, ptrs, nc, row, int(page_size),
+            pages, block_table.data_ptr(), max_pages,
+            _arg(seq_lens, "seq_lens", i32, (bs,), index),
+            _arg(path, "path", i32, (bs, path.shape[1]), index), path.shape[1], bs,
+            _arg(dev_status, "dev_status", i32, (1,), index))

@@ -1,0 +1,310 @@
+// cache_fork.cu -- rows of the block table continued from rows of an old one.
+//
+// New row r holds the first t_r = keep[r] tokens of old row parent[r]: its first
+// floor(t_r / ps) pages, whole, are shared with whoever else continues them; its
+// partial last page can have one writer only, so the first row that ends in it keeps
+// it if no row holds it whole, and every other row gets a fresh page and an entry in
+// the list of copies.  Old pages that no new row holds go back to the ring.
+//
+// Who holds a page is counted, not remembered: each call scatters over the pool, for
+// every page, its first entry in the old table (atomic min), the new rows that hold
+// it whole (atomic add) and the first that ends in it (atomic min).  The results of
+// those do not depend on their order, so neither do the tables or the ring.  Four
+// steps, each over all rows with a warp a row:
+//   mark    the three scatters
+//   count   pages that each old row gives back, new rows that need a fresh page
+//   scan    their prefix sums over the rows
+//   write   the new table, the copies, the ring
+#include <cuda_runtime.h>
+#include <limits.h>
+
+#include "bdsa_device.cuh"
+#include "bdsa_internal.h"
+#include "cache_internal.h"
+
+namespace bdsa {
+namespace {
+
+constexpr uint32_t kNone = 0xFFFFFFFFu;
+constexpr int kForkThreads = 256, kScanThreads = 1024;
+
+// The part of the work that a warp takes.
+struct Share {
+    long long warp, warps;  // this warp of how many
+    int lane;
+};
+__device__ __forceinline__ Share share() {
+    const int per = blockDim.x / 32;
+    return {(long long)blockIdx.x * per + threadIdx.x / 32, (long long)gridDim.x * per,
+            (int)threadIdx.x % 32};
+}
+
+// Pages of an old row (0: owned pages that mean nothing).
+__device__ __forceinline__ int owned_pages(const ForkArgs &a, int r, bool &bad) {
+    const int n = __ldg(a.owned + r);
+    bad = n < 0 || n > a.max_pages;
+    return bad ? 0 : n;
+}
+
+// What a new row keeps.
+struct Kept {
+    const int32_t *row;  // the parent's
+    int whole, tail;     // pages it holds whole, tokens in the last one
+    bool bad;            // a parent or a length that means nothing: the row is empty
+};
+__device__ __forceinline__ Kept kept_of(const ForkArgs &a, int r) {
+    Kept k{a.block_table, 0, 0, false};
+    const int p = __ldg(a.parent + r);
+    if (p == -1) return k;
+    k.bad = p < -1 || p >= a.bs_in;
+    if (k.bad) return k;
+    bool wrong;
+    const int own = owned_pages(a, p, wrong), t = __ldg(a.keep + r);
+    k.bad = wrong || t < 0 || (long long)t > (long long)own * a.page_size;
+    if (k.bad) return k;
+    k.row = a.block_table + (long long)p * a.max_pages;
+    k.whole = t / a.page_size;
+    k.tail = t % a.page_size;
+    return k;
+}
+__device__ __forceinline__ bool in_pool(const ForkArgs &a, int id) {
+    return id >= 0 && id < a.num_pages;
+}
+
+__device__ void step_clear(const ForkArgs &a) {
+    const long long n = (long long)gridDim.x * blockDim.x;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < a.num_pages; i += n) {
+        a.first[i] = kNone;
+        a.heir[i] = kNone;
+        a.refs[i] = 0;
+    }
+}
+
+__device__ void step_mark(const ForkArgs &a) {
+    const Share s = share();
+    for (long long x = s.warp; x < (long long)a.bs_in + a.bs_out; x += s.warps) {
+        if (x < a.bs_in) {
+            bool bad;
+            const int r = (int)x, n = owned_pages(a, r, bad);
+            const long long at = (long long)r * a.max_pages;
+            for (int j = s.lane; j < n; j += 32) {
+                const int id = __ldg(a.block_table + at + j);
+                if (in_pool(a, id)) atomicMin(a.first + id, (uint32_t)(at + j));
+            }
+        } else {
+            const int r = (int)(x - a.bs_in);
+            const Kept k = kept_of(a, r);
+            for (int j = s.lane; j < k.whole; j += 32) {
+                const int id = __ldg(k.row + j);
+                if (in_pool(a, id)) atomicAdd(a.refs + id, 1);
+            }
+            if (s.lane == 0 && k.tail > 0) {
+                const int id = __ldg(k.row + k.whole);
+                if (in_pool(a, id)) atomicMin(a.heir + id, (uint32_t)r);
+            }
+        }
+    }
+}
+
+// The new row gets a fresh page for its last tokens (id: the old one).
+__device__ __forceinline__ bool needs_copy(const ForkArgs &a, const Kept &k, int r, int &id) {
+    id = k.tail > 0 ? __ldg(k.row + k.whole) : -1;
+    return in_pool(a, id) && (__ldcg(a.refs + id) > 0 || __ldcg(a.heir + id) != (uint32_t)r);
+}
+// Entry `at` of the old table is the first of a page that nobody holds any more.
+__device__ __forceinline__ bool is_gone(const ForkArgs &a, long long at) {
+    const int id = __ldg(a.block_table + at);
+    return in_pool(a, id) && __ldcg(a.first + id) == (uint32_t)at && __ldcg(a.refs + id) == 0 &&
+           __ldcg(a.heir + id) == kNone;
+}
+
+__device__ void step_count(const ForkArgs &a) {
+    const Share s = share();
+    for (long long x = s.warp; x < (long long)a.bs_in + a.bs_out; x += s.warps) {
+        if (x < a.bs_in) {
+            bool bad;
+            const int r = (int)x, n = owned_pages(a, r, bad);
+            int c = 0;
+            for (int j = s.lane; j < n; j += 32) c += is_gone(a, (long long)r * a.max_pages + j);
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (s.lane == 0) a.gone[r] = c;
+        } else if (s.lane == 0) {
+            const int r = (int)(x - a.bs_in);
+            int id;
+            a.copies[r] = needs_copy(a, kept_of(a, r), r, id);
+        }
+    }
+}
+
+// Exclusive prefix sums of v[0, n) in place, the total in v[n]: one CTA.
+__device__ void scan_rows(int32_t *v, int n) {
+    __shared__ int s_w[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x / 32;
+    const int per = (n + blockDim.x - 1) / blockDim.x;
+    const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
+    int sum = 0;
+    for (int i = i0; i < i1; ++i) sum += __ldcg(v + i);
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += t;
+    }
+    __syncthreads();
+    if (lane == 31) s_w[warp] = inc;
+    __syncthreads();
+    int before = inc - sum, all = 0;
+    for (int w = 0; w < nw; ++w) {
+        if (w < warp) before += s_w[w];
+        all += s_w[w];
+    }
+    for (int i = i0; i < i1; ++i) {
+        const int c = __ldcg(v + i);
+        v[i] = before;
+        before += c;
+    }
+    if (tid == 0) v[n] = all;
+}
+
+__device__ void step_write(const ForkArgs &a) {
+    const Share s = share();
+    const uint32_t np = (uint32_t)a.num_pages;
+    const int head_in = __ldg(a.free_state), count_in = __ldg(a.free_state + 1);
+    const bool state_ok =
+        head_in >= 0 && head_in < a.num_pages && count_in >= 0 && count_in <= a.num_pages;
+    const uint32_t head = state_ok ? (uint32_t)head_in : 0u;
+    const int count = state_ok ? count_in : 0;
+    const int want = __ldcg(a.copies + a.bs_out), gone = __ldcg(a.gone + a.bs_in);
+    const int popped = min(want, count);
+    // more pages in use and free than the pool has: nothing goes back
+    const bool push = state_ok && (long long)count + gone <= a.num_pages;
+    bool report = false;
+    if (s.warp == 0 && s.lane == 0) {
+        a.free_state_out[0] =
+            state_ok ? (int)(((uint64_t)head + (uint64_t)popped) % np) : head_in;
+        a.free_state_out[1] = state_ok ? count - popped + (push ? gone : 0) : count_in;
+        report = !push || popped < want;
+    }
+    for (long long x = s.warp; x < (long long)a.bs_in + a.bs_out; x += s.warps) {
+        if (x < a.bs_in) {
+            // ---- pages that go back, in the order of their entries
+            bool bad;
+            const int r = (int)x, n = owned_pages(a, r, bad);
+            report |= bad;
+            int at = __ldcg(a.gone + r);
+            for (int j0 = 0; j0 < n; j0 += 32) {
+                const int j = j0 + s.lane;
+                const long long e = (long long)r * a.max_pages + j;
+                const bool g = j < n && is_gone(a, e);
+                report |= j < n && !in_pool(a, __ldg(a.block_table + e));
+                const uint32_t m = __ballot_sync(0xffffffffu, g);
+                if (g && push) {
+                    const uint64_t k = (uint64_t)(at + __popc(m & ((1u << s.lane) - 1)));
+                    a.free_pages[((uint64_t)head + (uint64_t)count + k) % np] =
+                        __ldg(a.block_table + e);
+                }
+                at += __popc(m);
+            }
+        } else {
+            // ---- a new row
+            const int r = (int)(x - a.bs_in);
+            const Kept k = kept_of(a, r);
+            int old;
+            const bool copy = needs_copy(a, k, r, old);
+            int end = old, fresh = -1;  // its last page; a fresh one
+            bool have = k.tail > 0;
+            if (copy) {
+                const int at = __ldcg(a.copies + r);
+                have = at < popped;
+                if (have) {
+                    uint64_t cell = (uint64_t)head + (uint64_t)at;
+                    if (cell >= np) cell -= np;
+                    fresh = __ldcg(a.free_pages + cell);
+                    if (!in_pool(a, fresh)) fresh = -1;
+                    report |= fresh < 0;
+                }
+                end = fresh;
+            } else if (have && !in_pool(a, old)) {
+                end = -1;
+                report = true;
+            }
+            report |= k.bad;
+            int shared = 0;
+            int32_t *out = a.block_table_out + (long long)r * a.max_pages;
+            for (int j = s.lane; j < a.max_pages; j += 32) {
+                int id = -1;
+                if (j < k.whole) {
+                    id = __ldg(k.row + j);
+                    if (in_pool(a, id)) {
+                        if (__ldcg(a.refs + id) > 1) shared = j + 1;
+                    } else {
+                        id = -1;
+                        report = true;
+                    }
+                } else if (j == k.whole && have) {
+                    id = end;
+                }
+                out[j] = id;
+            }
+            shared = __reduce_max_sync(0xffffffffu, shared);
+            if (s.lane == 0) {
+                a.owned_out[r] = k.whole + (have ? 1 : 0);
+                a.shared_out[r] = shared;
+                a.copy_src[r] = fresh >= 0 ? old : -1;
+                a.copy_dst[r] = fresh;
+                a.copy_len[r] = fresh >= 0 ? k.tail : 0;
+            }
+        }
+    }
+    if (report) report_status(a.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
+}
+
+__global__ void __launch_bounds__(kForkThreads) fork_clear_kernel(const ForkArgs a) {
+    grid_dependency_wait();
+    step_clear(a);
+}
+__global__ void __launch_bounds__(kForkThreads) fork_mark_kernel(const ForkArgs a) {
+    step_mark(a);
+}
+__global__ void __launch_bounds__(kForkThreads) fork_count_kernel(const ForkArgs a) {
+    step_count(a);
+}
+__global__ void __launch_bounds__(kScanThreads) fork_scan_kernel(const ForkArgs a) {
+    scan_rows(a.copies, a.bs_out);
+    scan_rows(a.gone, a.bs_in);
+}
+__global__ void __launch_bounds__(kForkThreads) fork_write_kernel(const ForkArgs a) {
+    step_write(a);
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t fork_workspace_bytes(int bs_in, int bs_out, int num_pages) {
+    return 3 * up256(4 * (size_t)num_pages) + up256(4 * ((size_t)bs_in + 1)) +
+           up256(4 * ((size_t)bs_out + 1));
+}
+
+int launch_cache_fork(ForkArgs a, void *workspace, cudaStream_t stream) {
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const size_t pages = up256(4 * (size_t)a.num_pages);
+    a.first = reinterpret_cast<uint32_t *>(ws);
+    a.heir = reinterpret_cast<uint32_t *>(ws + pages);
+    a.refs = reinterpret_cast<int32_t *>(ws + 2 * pages);
+    a.gone = reinterpret_cast<int32_t *>(ws + 3 * pages);
+    a.copies = reinterpret_cast<int32_t *>(ws + 3 * pages + up256(4 * ((size_t)a.bs_in + 1)));
+    const long long rows = (long long)a.bs_in + a.bs_out;
+    const unsigned warps = kForkThreads / 32;
+    const unsigned by_row = (unsigned)((rows + warps - 1) / warps);
+    const unsigned by_page =
+        (unsigned)(((long long)a.num_pages + kForkThreads - 1) / kForkThreads);
+    fork_clear_kernel<<<by_page < 1024 ? by_page : 1024, kForkThreads, 0, stream>>>(a);
+    fork_mark_kernel<<<by_row, kForkThreads, 0, stream>>>(a);
+    fork_count_kernel<<<by_row, kForkThreads, 0, stream>>>(a);
+    fork_scan_kernel<<<1, kScanThreads, 0, stream>>>(a);
+    fork_write_kernel<<<by_row, kForkThreads, 0, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? BDSA_OK : BDSA_CUDA_ERROR;
+}
+
+}  // namespace bdsa

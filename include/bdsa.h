@@ -647,6 +647,171 @@ int32_t bdsa_token_sample(const void *logits, int32_t dtype, int64_t l_stride_r,
                           int64_t p_stride_r, int64_t p_stride_i, int32_t num_sms,
                           int32_t *dev_status, void *stream);
 
+/* ------------------------------------------------------------------------ */
+/* bdsa_chunk_attn_paged
+ *
+ * "SGLang dLLM / LLaDA 2.0", section "Attention Mask" (a prompt's chunk sees the
+ * whole cache and, inside itself, a token-causal trapezoid, or rectangles of
+ * block-diffusion blocks); "From DFlash to dLLM Self-Spec (II): SGLang Spec V2",
+ * section 2.2 (the forwards of a serving batch): attention of a ragged batch of
+ * new tokens -- chunks of prompts of any length, single tokens of requests that
+ * decode -- over the paged cache that holds their own keys and values already.
+ *
+ * Request r's new tokens are rows [cu_tokens[r], cu_tokens[r+1]) of q, n_r of them
+ * (0 is allowed), at positions L_r .. L_r + n_r - 1 (L_r = seq_lens[r]);
+ * bdsa_block_table_update's cu_tokens, and its slot_map for bdsa_cache_write.
+ * For token i of request r at position p = L_r + i, query head j (h = j / G):
+ *   out[t, j] = sum_s softmax_s(scale * <q[t, j], k[s, h]>) v[s, h] over s < lim,
+ *   lim = min(L_r + n_r, (p / mask_block + 1) * mask_block)
+ * mask_block 1 is token-causal; with mask_block b the tokens of positions
+ * [k b, (k + 1) b) see their block to its end.
+ *
+ * q        token t at q + t * q_stride elements (q_stride >= Hq * D, below 2^30 and a
+ *          multiple of 8: a slice of a fused projection), heads dense [Hq, D], bf16
+ * k_cache, v_cache, block_table, num_pages: as in bdsa_block_attn_paged
+ * out      [T, Hq, D] bf16; lse [T, Hq] fp32 natural log, or NULL
+ * T        rows of q, out and lse; rows from cu_tokens[bs] on are left as they were
+ * A token that sees a key whose page id is outside the pool, and every token of a
+ * request with L_r < 0 or L_r + n_r beyond its block-table row, gets out = 0 and
+ * lse = -inf, reported (BDSA_DEVICE_OUT_OF_RANGE); other tokens are not touched by
+ * it.  cu_tokens that do not run up from 0 to at most T write nothing, reported.
+ * A row with a NaN score (a NaN in its query or in a key it sees, a score of +inf)
+ * gets NaN; keys it does not see, and cache slots past L_r + n_r, may hold
+ * anything, but a NaN or an infinity in the value of a token of the same request
+ * can reach rows that do not see it (0 * NaN in its 128-key tile).
+ * Arithmetic as in bdsa_block_attn_paged.  softmax_scale finite and > 0; 1 <= mask_block
+ * <= 2^30; D in {64, 128}; G <= 128; page_size a power of two >= 8; q, caches, out
+ * 16-byte aligned.  out, lse and workspace must not overlap the inputs or one
+ * another (BDSA_INVALID_ARG).
+ * num_sms  persistent CTAs (0: the current device's SM count; above 1024: 1024).
+ * Two launches, chained with programmatic dependent launch; the second joins the
+ * row tiles that the equal shares of the first cut.  Workspace: at least
+ * bdsa_chunk_attn_workspace_bytes(D, num_sms) bytes, 256-byte aligned, no
+ * initialisation needed.
+ */
+size_t bdsa_chunk_attn_workspace_bytes(int32_t D, int32_t num_sms);
+
+int32_t bdsa_chunk_attn_paged(const bdsa_bf16 *q, int64_t q_stride, const bdsa_bf16 *k_cache,
+                              const bdsa_bf16 *v_cache, const int32_t *block_table,
+                              int32_t max_pages_per_req, int32_t num_pages,
+                              const int32_t *seq_lens, const int32_t *cu_tokens, int32_t bs,
+                              int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
+                              float softmax_scale, int32_t mask_block, bdsa_bf16 *out, float *lse,
+                              void *workspace, size_t workspace_bytes, int32_t num_sms,
+                              int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* bdsa_cache_write
+ *
+ * "From DFlash to dLLM Self-Spec (II)", section 2.2.2 (K/V go to the cache
+ * locations that the step prepared): for every token t < T with slot
+ * s = slot_map[t] (bdsa_block_table_update's),
+ *   k_cache[s] = k_new[t], v_cache[s] = v_new[t]      (row_bytes each)
+ * k_new, v_new: token t at t * k_stride, t * v_stride bytes (slices of a fused
+ * projection).  A slot of -1 is skipped (padding); one outside [-1, num_slots) is
+ * skipped and reported.  Slots other than -1 must differ from one another.
+ * Any element type: row_bytes (Hkv * D elements), strides and pointers are
+ * multiples of 16 bytes, strides at least row_bytes (and below 2^31), row_bytes <=
+ * 2^20.  The caches
+ * must not overlap the inputs or one another (BDSA_INVALID_ARG).  One launch.
+ */
+int32_t bdsa_cache_write(const void *k_new, int64_t k_stride, const void *v_new,
+                         int64_t v_stride, const int32_t *slot_map, int32_t T, void *k_cache,
+                         void *v_cache, int32_t row_bytes, int64_t num_slots,
+                         int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* bdsa_cache_fork
+ *
+ * The block table of the next step from rows of the present one: prompts forked
+ * into several samples, beams reordered, requests moved, cut short or ended ("From
+ * DFlash to dLLM Self-Spec (II)", section 2.3.5: tables and their reserved pages
+ * are kept between steps; bdsa_block_attn_paged_prefix attends shared pages once).
+ *
+ * New row r (of bs_out) holds the first keep_lens[r] tokens of old row parent[r] (of
+ * bs_in); parent -1 makes it empty.  With whole = keep / page_size and tail = keep %
+ * page_size:
+ *   entries [0, whole) are the parent's: pages held by several rows are shared
+ *   a tail's page is the parent's if no new row holds that page whole and r is the
+ *   first new row that ends in it; else a page popped from the ring, in row order,
+ *   and copy_src[r], copy_dst[r], copy_len[r] = the old page, the new one, tail, for
+ *   bdsa_cache_copy (-1, -1, 0 otherwise)
+ *   entries past the last are -1; owned_out[r] = the row's pages
+ *   shared_out[r] = leading entries up to the last that another row holds too
+ *   (bdsa_block_table_update's shared: it releases none of those)
+ * Pages of the old rows (owned[p] entries of row p, pages reserved past the tokens
+ * among them) that no new row holds are pushed behind the ring's tail, in order of
+ * their first entry in the old table; they can be popped from the next call on.
+ * The ring (free_pages [num_pages], updated in place, and free_state {head, count})
+ * is bdsa_block_table_update's.  The outputs depend on the arguments alone.
+ * The call sees every row of the table: a page that rows outside it hold counts as
+ * held by nobody.  Where the ring runs out, a row gets no last page (owned_out =
+ * whole) and is reported.  A row with a parent outside [-1, bs_in), a keep_lens
+ * outside [0, owned[parent] * page_size], or a parent whose owned is outside [0,
+ * max_pages_per_req] is empty and reported; an entry outside the pool becomes -1
+ * and is reported; a free_state outside the ring pops and pushes nothing and is
+ * passed on, and when pages in use and free exceed num_pages nothing is pushed
+ * (both reported).
+ * Outputs must not overlap inputs or one another (BDSA_INVALID_ARG).  Supported:
+ * bs_in and bs_out <= BDSA_TABLE_MAX_REQUESTS, bs_in * max_pages_per_req < 2^31, any
+ * page_size >= 1, num_pages * page_size < 2^31.  Workspace:
+ * bdsa_cache_fork_workspace_bytes(...) bytes, 256-byte aligned, no initialisation.
+ */
+size_t bdsa_cache_fork_workspace_bytes(int32_t bs_in, int32_t bs_out, int32_t num_pages);
+
+int32_t bdsa_cache_fork(const int32_t *parent, const int32_t *keep_lens,
+                        const int32_t *block_table, const int32_t *owned,
+                        int32_t max_pages_per_req, int32_t num_pages, int32_t bs_in,
+                        int32_t bs_out, int32_t page_size, int32_t *free_pages,
+                        const int32_t *free_state, int32_t *block_table_out, int32_t *owned_out,
+                        int32_t *shared_out, int32_t *free_state_out, int32_t *copy_src,
+                        int32_t *copy_dst, int32_t *copy_len, void *workspace,
+                        size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* bdsa_cache_copy
+ *
+ * Entry e < n copies the first copy_len[e] slots of page copy_src[e] to page
+ * copy_dst[e], in each of n_caches caches (the keys and the values of every layer;
+ * `caches` is a HOST array of device pointers, read before the call returns), each
+ * [num_pages * page_size, row_bytes].  An entry of length 0, or with both pages -1, is
+ * skipped; one with a page outside the pool or a length outside [0, page_size] is
+ * skipped and reported.  No page may be the destination of two entries, nor a
+ * source and a destination.  row_bytes and the caches are multiples of 16 bytes,
+ * row_bytes <= 2^20, n_caches <= BDSA_MAX_CACHES; the caches must not overlap one
+ * another or the lists (BDSA_INVALID_ARG).  One launch for up to 256 caches and
+ * 65535 entries.
+ */
+enum { BDSA_MAX_CACHES = 1024 };
+
+int32_t bdsa_cache_copy(void *const *caches, int32_t n_caches, int64_t row_bytes,
+                        int32_t page_size, int32_t num_pages, const int32_t *copy_src,
+                        const int32_t *copy_dst, const int32_t *copy_len, int32_t n,
+                        int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* bdsa_cache_compact
+ *
+ * The kept rows of each request's region moved to its front, in each of n_caches
+ * caches: "Unlocking Lossless Speedups in LLMs via Discrete Diffusion", the Psi-Spec
+ * Tree sampler (the KV rows of the accepted path stay: bdsa_tree_accept's path), or
+ * a context cut to some of its tokens (seq_lens 0).
+ *
+ * Request r's kept rows are path[r, i] for i < m_r, the entries of its row (path
+ * [bs, width]) before the first -1; they run up strictly from at least 0.  Position
+ * seq_lens[r] + path[r, i] moves to seq_lens[r] + i, through block_table [bs,
+ * max_pages_per_req]; other slots stay as they are.  A request whose path does not run up, or
+ * with a kept position beyond its row or on a page outside the pool, is left alone
+ * and reported.  Rows of different requests must not lie on shared pages.
+ * row_bytes, caches: as in bdsa_cache_copy; any page_size >= 1.  One launch for up to
+ * 256 caches.
+ */
+int32_t bdsa_cache_compact(void *const *caches, int32_t n_caches, int64_t row_bytes,
+                           int32_t page_size, int32_t num_pages, const int32_t *block_table,
+                           int32_t max_pages_per_req, const int32_t *seq_lens,
+                           const int32_t *path, int32_t width, int32_t bs, int32_t *dev_status,
+                           void *stream);
+
 #ifdef __cplusplus
 }
 #endif

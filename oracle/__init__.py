@@ -513,3 +513,156 @@ def block_table_update(seq_lens, new_lens, owned, block_table, free_pages, free_
     return dict(block_table=table, free_pages=ring, owned=own_out,
                 free_state=np.array([h % pool, left] if state_ok else [head, count]),
                 cu_tokens=np.array(cu), slot_map=out[0], positions=out[1], n_bad=int(bad))
+
+
+def chunk_attn(q, k, v, block_table, seq_lens, cu_tokens, page_size, scale, mask_block=1,
+               num_pages=None):
+    """Attention of a ragged batch of new tokens over the paged cache, in fp64, token
+    by token.  q [T, Hq, D]; k, v [slots, Hkv, D].  Returns (out, lse, weight): weight
+    is sum_s p_s |v_s| / sum_s p_s, what a rounding of the p_s can move out by,
+    relative to the rounding.  Rows that are nobody's hold NaN; a row that sees a key
+    without a page, or of a request longer than its row, is 0 with lse -inf."""
+    q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    G = Hq // Hkv
+    max_pages = block_table.shape[1]
+    num_pages = k.shape[0] // page_size if num_pages is None else num_pages
+    out, weight = np.full((T, Hq, D), np.nan), np.full((T, Hq, D), np.nan)
+    lse = np.full((T, Hq), np.nan)
+    cu = [int(x) for x in cu_tokens]
+    if cu[0] != 0 or cu[-1] > T or any(a > b for a, b in zip(cu, cu[1:])):
+        return out, lse, weight
+    for r in range(len(cu) - 1):
+        L, n = int(seq_lens[r]), cu[r + 1] - cu[r]
+        rows = slice(cu[r], cu[r + 1])
+        if L < 0 or L + n > max_pages * page_size:
+            out[rows], weight[rows], lse[rows] = 0.0, 0.0, -np.inf
+            continue
+        if n == 0:
+            continue
+        ids = np.asarray(block_table[r, :-(-(L + n) // page_size)], np.int64)
+        good = (ids >= 0) & (ids < num_pages)
+        first_bad = int(np.argmin(good)) * page_size if not good.all() else L + n
+        t = np.arange(min(first_bad, L + n))
+        slots = ids[t // page_size] * page_size + t % page_size
+        for i in range(n):
+            lim = min(L + n, ((L + i) // mask_block + 1) * mask_block)
+            at = cu[r] + i
+            if lim > first_bad:
+                out[at], weight[at], lse[at] = 0.0, 0.0, -np.inf
+                continue
+            for h in range(Hkv):
+                kk, vv = k[slots[:lim], h], v[slots[:lim], h]
+                heads = slice(h * G, (h + 1) * G)
+                s = q[at, heads] @ kk.T * scale
+                m = s.max(1, keepdims=True)
+                p = np.exp(s - m)
+                z = p.sum(1, keepdims=True)
+                out[at, heads] = p @ vv / z
+                weight[at, heads] = p @ np.abs(vv) / z
+                lse[at, heads] = (m + np.log(z))[:, 0]
+    return out, lse, weight
+
+
+def cache_fork(parent, keep_lens, block_table, owned, free_pages, free_state, page_size):
+    """The fork of a block table, row by row, with a list of holders for every page.
+    Returns a dict: block_table, owned, shared, free_pages, free_state, copy_src,
+    copy_dst, copy_len, n_bad."""
+    table, ring = np.asarray(block_table, np.int64), np.array(free_pages, np.int64)
+    bs, max_pages = table.shape
+    pool, rows, bad = len(ring), len(parent), 0
+    own = [int(x) if 0 <= x <= max_pages else 0 for x in owned]
+    bad += sum(not 0 <= x <= max_pages for x in owned)
+    head, count = (int(x) for x in free_state)
+    state_ok = 0 <= head < pool and 0 <= count <= pool
+    h, left = (head, count) if state_ok else (0, 0)
+    kept = []  # (parent, whole pages, tail) of each new row
+    for r in range(rows):
+        p, t = int(parent[r]), int(keep_lens[r])
+        if p == -1:
+            kept.append((0, 0, 0))
+        elif not 0 <= p < bs or not 0 <= owned[p] <= max_pages or \
+                not 0 <= t <= own[p] * page_size:
+            kept.append((0, 0, 0))
+            bad += 1
+        else:
+            kept.append((p, t // page_size, t % page_size))
+    inside = lambda x: 0 <= x < pool  # noqa: E731
+    whole_rows, tail_rows = {}, {}
+    for r, (p, w, t) in enumerate(kept):
+        for x in table[p, :w] if w else ():
+            whole_rows.setdefault(int(x), []).append(r)
+        if t:
+            tail_rows.setdefault(int(table[p, w]), []).append(r)
+    out = np.full((rows, max_pages), -1, np.int64)
+    owned_out, shared = np.zeros(rows, np.int64), np.zeros(rows, np.int64)
+    src, dst = np.full(rows, -1, np.int64), np.full(rows, -1, np.int64)
+    ln, popped = np.zeros(rows, np.int64), 0
+    old_ring = ring.copy()
+    for r, (p, w, t) in enumerate(kept):
+        for j in range(w):
+            x = int(table[p, j])
+            out[r, j] = x if inside(x) else -1
+            bad += not inside(x)
+            if inside(x) and len(whole_rows[x]) > 1:
+                shared[r] = j + 1
+        owned_out[r] = w
+        if not t:
+            continue
+        x = int(table[p, w])
+        if not inside(x):
+            owned_out[r] = w + 1
+            bad += 1
+        elif x not in whole_rows and tail_rows[x][0] == r:
+            out[r, w], owned_out[r] = x, w + 1
+        elif popped == left:
+            bad += 1
+        else:
+            fresh = int(old_ring[(h + popped) % pool])
+            popped += 1
+            owned_out[r] = w + 1
+            if inside(fresh):
+                out[r, w], src[r], dst[r], ln[r] = fresh, x, fresh, t
+            else:
+                bad += 1
+    gone = []
+    seen = {x for x in list(whole_rows) + list(tail_rows)}
+    for r in range(bs):
+        for x in table[r, :own[r]]:
+            bad += not inside(int(x))
+            if inside(int(x)) and int(x) not in seen:
+                seen.add(int(x))
+                gone.append(int(x))
+    if state_ok and count + len(gone) <= pool:
+        for i, x in enumerate(gone):
+            ring[(h + left + i) % pool] = x
+        state = [(h + popped) % pool, left - popped + len(gone)]
+    else:
+        bad += 1
+        state = [(h + popped) % pool, left - popped] if state_ok else [head, count]
+    return dict(block_table=out, owned=owned_out, shared=shared, free_pages=ring,
+                free_state=np.array(state), copy_src=src, copy_dst=dst, copy_len=ln,
+                n_bad=int(bad))
+
+
+def cache_compact(cache, block_table, seq_lens, path, page_size):
+    """Kept rows of each request moved to the front of its region, all read before
+    any is written.  cache [slots, ...]; returns (the new cache, requests refused)."""
+    cache, old = np.array(cache), np.asarray(cache)
+    num_pages, bad = len(old) // page_size, 0
+    for r in range(len(path)):
+        row = [int(x) for x in path[r]]
+        keep = row[:row.index(-1)] if -1 in row else row
+        L = int(seq_lens[r])
+        ok = L >= 0 and all(a < b for a, b in zip([-1] + keep, keep)) and \
+            (not keep or L + keep[-1] < block_table.shape[1] * page_size)
+        pages = [int(block_table[r, (L + x) // page_size])
+                 for x in keep + list(range(len(keep)))] if ok else []
+        if not ok or any(not 0 <= x < num_pages for x in pages):
+            bad += bool(keep)
+            continue
+        slot = lambda t: int(block_table[r, t // page_size]) * page_size + t % page_size  # noqa: E731, B023
+        for i, x in enumerate(keep):
+            cache[slot(L + i)] = old[slot(L + x)]
+    return cache, bad
