@@ -21,7 +21,8 @@
 // each row tile.  A row tile's S (128 columns of TMEM) is read by its softmax, which
 // writes P as bf16 over it; PV takes P from TMEM.  The two tiles alternate on the
 // tensor cores and share every K and V tile in shared memory.  A row tile whose rows
-// see no key of the unit's last tiles sits those out.  O is rescaled in TMEM only
+// see no key of the unit's last tiles sits those out; where a pair has tokens for one
+// row tile alone, both take its rows, each over every other key tile.  O is rescaled in TMEM only
 // when a row's max grows by 2^8.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -57,6 +58,7 @@ struct ChunkParams {
     int32_t *dev_status;
     int bs, T, max_pages, num_pages, Hq, Hkv, G, npt, mb, log2_ps, box_rows;
     float scale_log2;
+    int wide;                  // out is 32-byte aligned
 };
 
 // A request's lengths and the costs of its units.
@@ -112,38 +114,46 @@ __device__ __forceinline__ int tile_at(long long x, long long span, int nt) {
     return x >= span ? nt : x <= kUnitCost ? 0 : min(nt, (int)((x - kUnitCost) >> 7));
 }
 
-// Walks the pieces of a cost range.
+// Walks the pieces of a cost range: one search for the first unit, then unit by unit.
 struct Walk {
-    int r;
-    long long base;  // cost before request r
-    long long c;     // next cost
+    int r, h, x;      // request, KV head, pair
+    long long cu, c;  // the unit's first cost, the next cost
     Req q;
+    __device__ void start(const ChunkParams &p, int r0, long long base) {
+        r = r0;
+        q = load_req(p, r);
+        const long long rel = c - base;
+        h = (int)(rel / q.head);
+        const long long in = rel - h * q.head;
+        int lo = 0, hi = q.P;  // pairs_before(lo) <= in < pairs_before(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pairs_before(p, q, mid) <= in) lo = mid;
+            else hi = mid;
+        }
+        x = lo;
+        cu = base + h * q.head + pairs_before(p, q, lo);
+    }
     __device__ bool next(const ChunkParams &p, long long c1, Piece &pc) {
         while (c < c1) {
-            const long long cost = q.head * p.Hkv;
-            if (c >= base + cost) {
+            while (x >= q.P) {
+                x = 0;
+                if (++h < p.Hkv && q.P > 0) break;
+                h = 0;
                 if (++r >= p.bs) return false;
-                base += cost;
                 q = load_req(p, r);
-                continue;
-            }
-            const long long rel = c - base;
-            const int h = (int)(rel / q.head);
-            const long long in = rel - h * q.head;
-            int lo = 0, hi = q.P;  // the pair: pairs_before(lo) <= in < pairs_before(hi)
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (pairs_before(p, q, mid) <= in) lo = mid;
-                else hi = mid;
             }
             const int w = 2 * p.npt;
-            pc.cu = base + h * q.head + pairs_before(p, q, lo);
-            pc.span = kUnitCost + q.L +
-                      min((long long)q.n, (lo + 1LL) * w + p.mb - 1);
-            const long long from = c - pc.cu, to = min(c1 - pc.cu, pc.span);
-            c = pc.cu + to;
-            pc.i0 = lo * w;
+            pc.cu = cu;
+            pc.span = kUnitCost + q.L + min((long long)q.n, (x + 1LL) * w + p.mb - 1);
+            const long long from = c - cu, to = min(c1 - cu, pc.span);
+            c = cu + to;
+            pc.i0 = x * w;
             pc.ntok = q.n - pc.i0;
+            if (to == pc.span) {
+                cu += pc.span;
+                ++x;
+            }
             const int last = limit_of(p, q.L, q.n, pc.i0 + min(pc.ntok, w) - 1);
             pc.nt = (last + kBN - 1) / kBN;
             pc.a = tile_at(from, pc.span, pc.nt);
@@ -170,6 +180,66 @@ __device__ __forceinline__ int tiles_of(const ChunkParams &p, const Piece &pc, i
     return max(0, min(pc.e, (lim + kBN - 1) / kBN) - pc.a);
 }
 
+// A piece as the K producer hands it to the other roles (in shared memory).  A pair
+// whose tokens fit one row tile is split: the two row tiles take the same rows over
+// every other key tile each, so that one's MMAs run beside the other's softmax, and
+// join their halves in the end.
+struct Work {
+    int n[2];          // key tiles that each row tile takes
+    int all, a;        // the piece's tiles, the first one (all = 0: no more pieces)
+    int split, nboth;  // a split pair; first tiles that both row tiles take
+    int whole;         // the unit's only piece
+    int r, L, n_new, i0, tok0, ntok, h;
+    int bad;           // (the request's lengths mean nothing)
+    int bad_key;       // the piece's first key without a page, ready with BK
+};
+static_assert(sizeof(Work) == 64, "");
+
+__device__ __forceinline__ void fill_work(const ChunkParams &p, const Piece &pc, Work *w) {
+    const int n0 = tiles_of(p, pc, 0), n1 = tiles_of(p, pc, 1);
+    const bool split = pc.ntok <= p.npt && n0 > 1;
+    w->n[0] = split ? (n0 + 1) / 2 : n0;
+    w->n[1] = split ? n0 / 2 : n1;
+    w->all = pc.e - pc.a;
+    w->a = pc.a;
+    w->split = split;
+    w->nboth = min(n0, n1);
+    w->whole = pc.a == 0 && pc.e == pc.nt;
+    w->r = pc.r;
+    w->L = pc.L;
+    w->n_new = pc.n;
+    w->i0 = pc.i0;
+    w->tok0 = pc.tok0;
+    w->ntok = pc.ntok;
+    w->h = pc.h;
+    w->bad = pc.bad;
+}
+
+// 16 consecutive columns of the thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {  // 1 ulp
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2_approx(float x) {  // 2^-22
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 template <int D>
 struct CCfg {
     static constexpr int DH = D / 64;           // 128-byte slabs of a row
@@ -194,17 +264,18 @@ struct CCfg {
     static constexpr int OE = OF + 2;    // 2: O read by the epilogue
     static constexpr int DR = OE + 2;    // 2: drain
     static constexpr int TK = DR + 2;    // 2: the other row tile's exponentials are done
-    static constexpr int kNumBars = TK + 2;
-    static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-    static constexpr int kMisc = 256;
-    static constexpr int kSmem = kOffMisc + kMisc + 1024;
+    static constexpr int MG = TK + 2;    // row tile 1's half of a split pair is done
+    static constexpr int NW = 4;         // pieces handed on
+    static constexpr int WF = MG + 1;    // NW: a piece is handed on
+    static constexpr int WE = WF + NW;   // NW: every role is done with it
+    static constexpr int BK = WE + NW;   // NW: its bad_key is there
+    static constexpr int kNumBars = BK + NW;
+    static constexpr int kOffHalf = (kOffBar + 8 * kNumBars + 15) / 16 * 16;
+    static constexpr int kOffWork = kOffHalf + 8 * kRows;  // (its rows' m and l)
+    static constexpr int kOffMisc = kOffWork + 64 * NW;
+    static constexpr int kSmem = kOffMisc + 256 + 1024;
     static constexpr int kProdK = 8, kMma0 = 9, kProdV = 10;  // (kMma1 = 11)
     static constexpr int kThreads = 12 * 32;
-    // Registers a thread: 168 at launch (12 warps of 65536 / 384), moved from
-    // the producers' warpgroup to the softmax ones, whose 128 scores a thread
-    // spill otherwise: 256 * 208 + 128 * 80 <= 384 * 168.
-    static constexpr int kSoftmaxRegs = 208, kProducerRegs = 80;
-    static_assert(256 * kSoftmaxRegs + 128 * kProducerRegs <= kThreads * 168, "register split");
 };
 
 struct CSched {
@@ -247,6 +318,12 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
             mbar_init(bar(C::OE + t), 4);
             mbar_init(bar(C::DR + t), 1);
             mbar_init(bar(C::TK + t), 4);
+        }
+        mbar_init(bar(C::MG), 4);
+        for (int k = 0; k < C::NW; ++k) {
+            mbar_init(bar(C::WF + k), 1);
+            mbar_init(bar(C::WE + k), 11);  // V producer, 2 MMA issuers, 8 softmax warps
+            mbar_init(bar(C::BK + k), 1);
         }
         for (int k = 0; k < C::NK; ++k) {
             mbar_init(bar(C::KF + k), 1);
@@ -333,99 +410,135 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
         }
         __syncthreads();
     }
-    const long long c1 = sch->c1;
-    Walk walk;
-    walk.c = sch->c0;
-    if (walk.c < c1) {
-        walk.r = sch->r0;
-        walk.base = sch->base;
-        walk.q = load_req(prm, walk.r);
-    }
-    Piece pc;
+    Work *works = reinterpret_cast<Work *>(smem + C::kOffWork);
 
-    // (each warpgroup's split inside its own branch: code they share is compiled
-    // for the smaller count)
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kProducerRegs));
         if (warp == C::kProdK || warp == C::kProdV) {
-            // ------------------------------------------------ TMA producers
-            if (lane == 0) {
-                const bool is_k = warp == C::kProdK;
-                const int NR = is_k ? C::NK : C::NV, FULL = is_k ? C::KF : C::VF;
-                const int EMPTY = is_k ? C::KE : C::VE;
-                const uint32_t dst0 = sbase + (is_k ? C::kOffK : C::kOffV);
-                const void *tmap = is_k ? (const void *)&tm_k : (const void *)&tm_v;
-                const int rows_box = prm.box_rows;
-                const int nbox = kBN / rows_box;
-                const int ps = 1 << prm.log2_ps;
-                // keys without a page of the pool read as zeros: a row past the
-                // cache's last is filled by the load
-                const int outside = prm.num_pages << prm.log2_ps;
-                int st = 0;
-                uint32_t ph = 1;
-                long g = 0;
-                int kq[2] = {0, 0};  // pieces each row tile took part in
-                bool ok = true;
-                while (ok && walk.next(prm, c1, pc)) {
-                    if (is_k) {
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (!ok || tiles_of(prm, pc, t) == 0) continue;
-                            if (kq[t] > 0)
-                                ok = mbar_wait(bar(C::QE + t), (kq[t] - 1) & 1, abort_flag,
-                                               prm.dev_status);
-                            if (!ok) break;
-                            mbar_arrive_expect_tx(bar(C::QF + t), (uint32_t)(rows * D * 2));
-                            for (int c = 0; c < C::DH; ++c)
-                                tma_load_4d(sbase + C::kOffQ + t * C::kTile + c * C::kSlab, &tm_q,
-                                            c * 64, 0, pc.h, pc.tok0 + t * prm.npt,
-                                            bar(C::QF + t));
-                            ++kq[t];
+            // ------------------------------------------------ TMA producers; K's walks
+            // (lane b loads box b of a tile)
+            const bool is_k = warp == C::kProdK;
+            const int NR = is_k ? C::NK : C::NV, FULL = is_k ? C::KF : C::VF;
+            const int EMPTY = is_k ? C::KE : C::VE;
+            const uint32_t dst0 = sbase + (is_k ? C::kOffK : C::kOffV) +
+                                  (uint32_t)(lane * prm.box_rows * 128);
+            const void *tmap = is_k ? (const void *)&tm_k : (const void *)&tm_v;
+            const bool loads = lane * prm.box_rows < kBN;
+            const int ps = 1 << prm.log2_ps;
+            // keys without a page of the pool read as zeros: a row past the
+            // cache's last is filled by the load
+            const int outside = prm.num_pages << prm.log2_ps;
+            const long long c1 = sch->c1;
+            Walk walk;
+            walk.c = sch->c0;
+            if (is_k && walk.c < c1) walk.start(prm, sch->r0, sch->base);
+            int st = 0;
+            uint32_t ph = 1;
+            long g = 0;
+            int kq[2] = {0, 0};  // pieces each row tile took part in
+            bool ok = true;
+            auto wait = [&](int i, uint32_t parity) {
+                ok = ok && mbar_wait(bar(i), parity & 1, abort_flag, prm.dev_status);
+                ok = __all_sync(0xffffffffu, ok);
+                return ok;
+            };
+            for (uint32_t k = 0;; ++k) {
+                const int ws = k % C::NW;
+                volatile Work *w = works + ws;
+                if (is_k) {
+                    if (k >= C::NW && !wait(C::WE + ws, k / C::NW - 1)) break;
+                    Piece pc;
+                    const bool more = walk.next(prm, c1, pc);
+                    if (lane == 0) {
+                        if (more) fill_work(prm, pc, works + ws);
+                        else w->all = 0;
+                        if (more && pc.a == 0 && pc.e < pc.nt) {  // the unit goes on elsewhere
+                            Cut d;
+                            d.valid = 1;
+                            d.tok0 = pc.tok0;
+                            d.ntok = pc.ntok;
+                            d.h = pc.h;
+                            d.nt = pc.nt;
+                            d.S = sch->S;
+                            d.cu = pc.cu;
+                            d.span = pc.span;
+                            d.Wc = sch->Wc;
+                            prm.cut[blockIdx.x] = d;
                         }
-                        if (!ok) break;
+                        mbar_arrive(bar(C::WF + ws));
                     }
-                    const int32_t *bt = prm.block_table + (long)pc.r * prm.max_pages;
-                    const int n_keys = pc.L + pc.n;
-                    for (int j = pc.a; j < pc.e; ++j, ++g) {
-                        const int t0 = j * kBN;
-                        int32_t slot[kMaxBoxes];
+                    __syncwarp();
+                } else if (!wait(C::WF + ws, k / C::NW)) {
+                    break;
+                }
+                const int all = w->all, a0 = w->a;
+                if (all == 0) break;
+                const int32_t *bt = prm.block_table + (long)w->r * prm.max_pages;
+                const int n_keys = w->bad ? 0 : w->L + w->n_new;
+                const int col = w->h * D;
+                int bad_key = w->bad ? 0 : INT_MAX;
+                for (int j = 0; j < all; ++j) {
+                    const int t = (a0 + j) * kBN + lane * prm.box_rows;
+                    const bool mine = loads && t < n_keys;
+                    const int id = mine ? __ldg(bt + (t >> prm.log2_ps)) : -1;
+                    const bool in = id >= 0 && id < prm.num_pages;
+                    const int slot = in ? id * ps + (t & (ps - 1)) : outside;
+                    if (mine && !in) bad_key = min(bad_key, t);
+                    if (!wait(EMPTY + st, ph)) break;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(FULL + st), (uint32_t)C::kTile);
+                    __syncwarp();
+                    if (loads) {
 #pragma unroll
-                        for (int bx = 0; bx < kMaxBoxes; ++bx) {
-                            if (bx >= nbox) break;
-                            const int t = t0 + bx * rows_box;
-                            const int page = t >> prm.log2_ps;
-                            const int32_t id = t < n_keys && !pc.bad ? __ldg(bt + page) : -1;
-                            slot[bx] = id >= 0 && id < prm.num_pages ? id * ps + (t & (ps - 1))
-                                                                     : outside;
+                        for (int c = 0; c < C::DH; ++c)
+                            tma_load_2d(dst0 + st * C::kTile + c * C::kSlab, tmap, col + c * 64,
+                                        slot, bar(FULL + st));
+                    }
+                    ++g;
+                    if (++st == NR) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                    if (is_k && j == 0) {  // (the first K tile needs no wait for Q)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            if (!ok || w->n[x] == 0) continue;
+                            if (kq[x] > 0 && !wait(C::QE + x, kq[x] - 1)) continue;
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(bar(C::QF + x), (uint32_t)(rows * D * 2));
+                                for (int c = 0; c < C::DH; ++c)
+                                    tma_load_4d(sbase + C::kOffQ + x * C::kTile + c * C::kSlab,
+                                                &tm_q, c * 64, 0, w->h,
+                                                w->tok0 + (w->split ? 0 : x * prm.npt),
+                                                bar(C::QF + x));
+                            }
+                            ++kq[x];
                         }
-                        ok = mbar_wait(bar(EMPTY + st), ph, abort_flag, prm.dev_status);
                         if (!ok) break;
-                        mbar_arrive_expect_tx(bar(FULL + st), (uint32_t)C::kTile);
-#pragma unroll
-                        for (int bx = 0; bx < kMaxBoxes; ++bx) {
-                            if (bx >= nbox) break;
-                            for (int c = 0; c < C::DH; ++c)
-                                tma_load_2d(dst0 + st * C::kTile + c * C::kSlab +
-                                                bx * rows_box * 128,
-                                            tmap, pc.h * D + c * 64, slot[bx], bar(FULL + st));
-                        }
-                        if (++st == NR) {
-                            st = 0;
-                            ph ^= 1;
-                        }
                     }
                 }
-                // Drain: the last load issued into each buffer has landed.
-                if (is_k)
+                if (!ok) break;
+                if (is_k) {
+                    bad_key = __reduce_min_sync(0xffffffffu, bad_key);
+                    if (lane == 0) {
+                        w->bad_key = bad_key;
+                        mbar_arrive(bar(C::BK + ws));
+                    }
+                } else if (lane == 0) {
+                    mbar_arrive(bar(C::WE + ws));
+                }
+                __syncwarp();
+            }
+            // Drain: the last load issued into each buffer has landed.
+            if (lane == 0) {
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        if (kq[t] > 0) mbar_wait_drain(bar(C::QF + t), (kq[t] - 1) & 1);
+                for (int x = 0; x < 2; ++x)
+                    if (is_k && kq[x] > 0) mbar_wait_drain(bar(C::QF + x), (kq[x] - 1) & 1);
                 for (long i = max(0L, g - NR); i < g; ++i)
                     mbar_wait_drain(bar(FULL + (int)(i % NR)), (uint32_t)((i / NR) & 1));
             }
+            __syncwarp();
         } else {
             // ------------------------------------------------ MMA issuers, one a row tile
-            // The whole warp walks the schedule and one elected lane issues: an
+            // The whole warp takes each piece and one elected lane issues: an
             // MMA takes its descriptors from uniform registers, which only code
             // that the warp runs together keeps them in.
             const int t = warp == C::kMma0 ? 0 : 1;
@@ -464,7 +577,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                 for (int k4 = 0; k4 < 4; ++k4) {
                     const int kk = part * 4 + k4;
                     umma_bf16_ts(tm + kO, tm + kS + kk * 8, v + (uint32_t)(kk * 128), idesc_pv,
-                                 (first && k4 == 0) ? 0u : 1u);
+                                 (first && part == 0 && k4 == 0) ? 0u : 1u);
                 }
             };
             // ring positions and their phases
@@ -484,119 +597,159 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                     vph ^= 1;
                 }
             };
-            while (ok && walk.next(prm, c1, pc)) {
-                const int n = tiles_of(prm, pc, t), all = pc.e - pc.a;
+            // a tile that this row tile does not take: only its release
+            auto pass_k = [&] {
+                wait(C::KF + ks, kph);
+                if (!ok) return;
+                if (leader) mbar_arrive(bar(C::KE + ks));
+                if (++ks == C::NK) {
+                    ks = 0;
+                    kph ^= 1;
+                }
+            };
+            auto pass_v = [&] {
+                wait(C::VF + vs, vph);
+                if (!ok) return;
+                if (leader) mbar_arrive(bar(C::VE + vs));
+                if (++vs == C::NV) {
+                    vs = 0;
+                    vph ^= 1;
+                }
+            };
+            for (uint32_t k = 0;; ++k) {
+                const int ws = k % C::NW;
+                wait(C::WF + ws, k / C::NW);
+                if (!ok) break;
+                const int n = works[ws].n[t], all = works[ws].all;
+                const bool split = works[ws].split != 0;
+                if (all == 0) break;
+                __syncwarp();
+                if (leader) mbar_arrive(bar(C::WE + ws));
+                const int first = split ? t : 0;
                 if (n > 0) {
-                    // the first S
-                    wait(C::KF + ks, kph);
-                    wait(C::QF + t, kt);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_s(ks);
-                    if (n == 1) commit(C::QE + t);
-                    next_k();
-                    for (int j = 0; j < n; ++j) {
+                    if (first) pass_k();
+                    // step j: PV of tile j (none at -1), then S of tile j + 1
+#pragma unroll 1
+                    for (int j = -1; j < n; ++j) {
                         const bool more = j + 1 < n;
-                        wait(C::VF + vs, vph);
-                        if (j == 0 && kt > 0) wait(C::OE + t, kt - 1);
-                        wait(C::PF + 2 * t, gt);
+                        if (j >= 0) {
+                            wait(C::VF + vs, vph);
+                            if (j == 0 && kt > 0) wait(C::OE + t, kt - 1);
+                        }
+#pragma unroll 1
+                        for (int part = 0; part < 2; ++part) {
+                            if (j >= 0) {
+                                wait(C::PF + 2 * t + part, gt);
+                                if (!ok) break;
+                                tc_fence_after();
+                                issue_pv(vs, part, j == 0);
+                            }
+                            if (part == 0 && more) {
+                                if (split && j >= 0) pass_k();
+                                wait(C::KF + ks, kph);
+                                if (j < 0) wait(C::QF + t, kt);
+                            }
+                        }
                         if (!ok) break;
-                        tc_fence_after();
-                        issue_pv(vs, 0, j == 0);
-                        if (more) wait(C::KF + ks, kph);
-                        wait(C::PF + 2 * t + 1, gt);
-                        if (!ok) break;
-                        ++gt;
-                        tc_fence_after();
-                        issue_pv(vs, 1, false);
                         if (more) {
+                            tc_fence_after();
                             issue_s(ks);
                             if (j + 2 == n) commit(C::QE + t);
-                            next_v();
-                            next_k();
                         } else {
                             commit(C::OF + t);
+                        }
+                        if (j >= 0) {
                             next_v();
+                            ++gt;
+                        }
+                        if (more) {
+                            next_k();
+                            if (split && (t == 1 || j >= 0)) pass_v();
                         }
                     }
                     ++kt;
                 }
-                // its share of the releases of tiles that its rows do not see
-                for (int j = n; ok && j < all; ++j) {
-                    wait(C::KF + ks, kph);
-                    if (ok) next_k();
-                    wait(C::VF + vs, vph);
-                    if (ok) next_v();
+                // (K before V, tile by tile: the rings move together)
+                const int past = n > 0 ? first + (n - 1) * (split ? 2 : 1) + 1 : 0;
+                for (int j = past; ok && j < all; ++j) {
+                    pass_k();
+                    pass_v();
                 }
+                if (!ok) break;
             }
             commit(C::DR + t);
             mbar_wait_drain(bar(C::DR + t), 0);
         }
     } else {
         // ------------------------------------------------ softmax + epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         const int t = warp >> 2;                       // row tile
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lane_base + kS + t * 128;
         const uint32_t o_addr = tmem + lane_base + kO + t * 128;
         const float sl2 = prm.scale_log2;
-        const int node = row / prm.G;                  // token within the tile
         uint32_t gs = 0, k = 0;
         uint32_t turn = 0;  // tiles that both row tiles took
+        uint32_t halves = 0;  // split pairs
         int vs0 = 0;        // V ring position and phase of the piece's first tile
         uint32_t vph0 = 0;
+        float2 *half = reinterpret_cast<float2 *>(smem + C::kOffHalf);
         bool ok = true;
-        while (ok && walk.next(prm, c1, pc)) {
-            const int n = tiles_of(prm, pc, t);
-            const int nboth = t == 0 ? (prm.npt < pc.ntok ? n : 0)
-                                     : (n > 0 ? tiles_of(prm, pc, 0) : 0);
-            const int all = pc.e - pc.a, n_keys = pc.L + pc.n;
-            const bool whole = pc.a == 0 && pc.e == pc.nt;
-            const int token = t * prm.npt + node;
-            const bool real = row < rows && token < pc.ntok;
+        for (uint32_t piece = 0;; ++piece) {
+            const int ws = piece % C::NW;
+            ok = mbar_wait(bar(C::WF + ws), (piece / C::NW) & 1, abort_flag, prm.dev_status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || works[ws].all == 0) break;
+            // (read where it is used: kept in registers across the tiles it costs spills)
+            const volatile Work &w = works[ws];
+            const int n = w.n[t], n_keys = w.L + w.n_new, nboth = w.nboth;
+            const bool split = w.split != 0;
             // keys this row sees (rows that are nobody's: all, nothing to mask)
-            const int lim = real ? limit_of(prm, pc.L, pc.n, pc.i0 + token) : INT_MAX;
-            // the piece's first key without a page of the pool
-            int bad_key = pc.bad ? 0 : INT_MAX;
-            if (n > 0 && !pc.bad) {
-                const int p0 = (pc.a * kBN) >> prm.log2_ps;
-                const int p1 = (min((pc.a + n) * kBN, n_keys) - 1) >> prm.log2_ps;
-                const int32_t *bt = prm.block_table + (long)pc.r * prm.max_pages;
-#pragma unroll 4
-                for (int pg = p0 + lane; pg <= p1; pg += 32) {
-                    const int32_t id = __ldg(bt + pg);
-                    if (id < 0 || id >= prm.num_pages) bad_key = min(bad_key, pg << prm.log2_ps);
-                }
-                bad_key = __reduce_min_sync(0xffffffffu, bad_key);
+            int lim = INT_MAX;
+            if (row < rows) {
+                const int token = (split ? 0 : t * prm.npt) + row / prm.G;
+                if (token < w.ntok) lim = limit_of(prm, w.L, w.n_new, w.i0 + token);
             }
+            int vi = vs0 + (split ? t : 0);                      // the tile's place in the ring
+            int t0 = (w.a + (split ? t : 0)) * kBN;              // its first key
+            const int step = split ? 2 : 1;
             float m_used = -INFINITY;
             uint64_t lacc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-            for (int j = 0; j < n; ++j, ++gs) {
-                const int t0 = (pc.a + j) * kBN;
+            for (int j = 0; j < n; ++j, ++gs, vi += step, t0 += step * kBN) {
                 ok = mbar_wait(bar(C::SF + t), gs & 1, abort_flag, prm.dev_status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                float sv[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tmem_ld32(s_addr + c * 32, *reinterpret_cast<float(*)[32]>(&sv[c * 32]));
-                tmem_wait_ld();
+                // ---- scores of keys that a row does not see become -inf
                 const int nvis = lim - t0;
                 if (__any_sync(0xffffffffu, nvis < kBN)) {
+#pragma unroll 1
+                    for (int b = 0; b < kBN; b += 32) {
+                        if (!__any_sync(0xffffffffu, nvis < b + 32)) continue;
+                        float sv[32];
+                        tmem_ld32(s_addr + b, sv);
+                        tmem_wait_ld();
+                        const int left = nvis - b;
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) sv[c] = c < nvis ? sv[c] : -INFINITY;
+                        for (int c = 0; c < 32; ++c) sv[c] = c < left ? sv[c] : -INFINITY;
+                        tmem_st32(s_addr + b, sv);
+                    }
+                    tmem_wait_st();
                 }
-                float mx[8];
+                // ---- the maximum (S is read twice: 128 scores a thread held over both
+                // passes are half of its registers, and code of four times the size)
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                for (int b = 0; b < kBN; b += 64) {
+                    float sv[64];
+                    tmem_ld32(s_addr + b, *reinterpret_cast<float(*)[32]>(&sv[0]));
+                    tmem_ld32(s_addr + b + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
+                    tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 8; ++c) mx[c] = sv[c];
-#pragma unroll
-                for (int c = 8; c < 128; c += 2)
-                    mx[(c >> 1) & 7] = max3f(mx[(c >> 1) & 7], sv[c], sv[c + 1]);
-                const float m_new = fmaxf(max3f(max3f(mx[0], mx[1], mx[2]), mx[3], mx[4]),
-                                          max3f(mx[5], mx[6], mx[7])) *
-                                    sl2;
+                    for (int c = 0; c < 64; c += 2)
+                        mx[(c >> 1) & 3] = max3f(mx[(c >> 1) & 3], sv[c], sv[c + 1]);
+                }
+                const float m_new = fmaxf(max3f(mx[0], mx[1], mx[2]), mx[3]) * sl2;
                 float alpha = 1.f;
                 bool resc = false;
                 if (m_new > m_used + kRescaleLog2) {
@@ -611,7 +764,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                     // (S of this tile was issued after PV of the last one, and
                     // its barrier covers both: O is complete)
                     if (j > 0) {
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             float ov[32];
                             tmem_ld32(o_addr + c * 32, ov);
@@ -626,17 +779,16 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                 // and 0 * NaN is NaN: they become zeros before PV reads them
                 // (each row tile before its own PV; both write the same zeros)
                 if (t0 + kBN > n_keys) {
-                    const int vi = vs0 + j;  // (tiles of this piece: at most ..)
                     const int vs = vi % C::NV;
                     ok = mbar_wait(bar(C::VF + vs), (vph0 + (uint32_t)(vi / C::NV)) & 1,
                                    abort_flag, prm.dev_status);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    const int first = n_keys - t0;
-                    for (int idx = row; idx < C::DH * 8 * (kBN - first); idx += kRows) {
+                    const int valid = n_keys - t0;
+                    for (int idx = row; idx < C::DH * 8 * (kBN - valid); idx += kRows) {
                         const int u = idx & 7, rr = idx >> 3;
-                        const int slab = rr >= kBN - first ? 1 : 0;
-                        const int m = first + rr - slab * (kBN - first);
+                        const int slab = rr >= kBN - valid ? 1 : 0;
+                        const int m = valid + rr - slab * (kBN - valid);
                         st_shared_v4(sbase + C::kOffV + vs * C::kTile + slab * C::kSlab + m * 128 +
                                          u * 16,
                                      0, 0, 0, 0);
@@ -655,24 +807,31 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                 }
                 const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
                 const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(neg_m, neg_m);
+                // (the next 32 scores are on their way while these become P)
+                float sv[2][32];
+                tmem_ld32(s_addr, sv[0]);
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t pk[16];
+                        tmem_wait_ld();
+                        if (h + c < 2) tmem_ld32(s_addr + h * 64 + c * 32 + 32, sv[1 - c]);
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const float2 xv = f2_unpack(
-                            f2_fma(f2_pack(sv[c * 32 + 2 * q], sv[c * 32 + 2 * q + 1]), sc2, nm2));
-                        const float p0 = ex2_approx(xv.x), p1 = ex2_approx(xv.y);
-                        pk[q] = pack_bf16x2(p0, p1);
-                        lacc[q & 1] = f2_add(lacc[q & 1], f2_pack(p0, p1));
+                        for (int q = 0; q < 16; ++q) {
+                            const float2 xv = f2_unpack(
+                                f2_fma(f2_pack(sv[c][2 * q], sv[c][2 * q + 1]), sc2, nm2));
+                            const float p0 = ex2_approx(xv.x), p1 = ex2_approx(xv.y);
+                            pk[q] = pack_bf16x2(p0, p1);
+                            lacc[q & 1] = f2_add(lacc[q & 1], f2_pack(p0, p1));
+                        }
+                        tmem_st16(s_addr + h * 32 + c * 16, pk);
                     }
-                    tmem_st16(s_addr + c * 16, pk);
-                    if (c & 1) {  // half of P: its PV may start
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(C::PF + 2 * t + (c >> 1)));
-                    }
+                    // half of P: its PV may start
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::PF + 2 * t + h));
                 }
                 if (both) {
                     if (lane == 0) mbar_arrive(bar(C::TK + 1 - t));
@@ -680,7 +839,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                 }
             }
             if (!ok) break;
-            vs0 += all;
+            vs0 += w.all;
             vph0 += (uint32_t)(vs0 / C::NV);
             vs0 %= C::NV;
             // ---- end of the piece: o / l and the log2-sum-exp
@@ -692,74 +851,98 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                 ++k;
             }
             const float2 la = f2_unpack(lacc[0]), lb = f2_unpack(lacc[1]);
-            const float l = (la.x + la.y) + (lb.x + lb.y);
-            const bool hit = bad_key < lim;
-            const float inv = l > 0.f ? 1.f / l : isnan(l) ? l : 0.f;
-            const float l2 = l > 0.f ? m_used + log2f(l) : isnan(l) ? l : -INFINITY;
-            if (whole) {
-                const long at = (long)(pc.tok0 + token) * prm.Hq + (long)pc.h * prm.G +
-                                row % prm.G;
-                uint16_t *po = prm.out + at * D;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    float ov[32];
-                    tmem_ld32(o_addr + c * 32, ov);
-                    tmem_wait_ld();
-                    if (!real) continue;
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int q = 0; q < 16; ++q)
-                        pk[q] = hit ? 0u : pack_bf16x2(ov[2 * q] * inv, ov[2 * q + 1] * inv);
-                    // (out rows are 16-byte aligned)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        *reinterpret_cast<uint4 *>(po + c * 32 + 8 * v) =
-                            make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
-                }
-                if (real && prm.lse != nullptr) prm.lse[at] = hit ? -INFINITY : l2 * kLn2;
-            } else {
-                const long dst =
-                    ((long)blockIdx.x * 2 + (pc.a == 0 ? 1 : 0)) * 2 * kRows + t * kRows + row;
-                float *po = prm.slot_o + dst * D;
-                if (n > 0) {
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        float ov[32];
-                        tmem_ld32(o_addr + c * 32, ov);
-                        tmem_wait_ld();
-                        if (!real) continue;
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            st_global_v8(po + c * 32 + 8 * v, __float_as_uint(ov[8 * v] * inv),
-                                         __float_as_uint(ov[8 * v + 1] * inv),
-                                         __float_as_uint(ov[8 * v + 2] * inv),
-                                         __float_as_uint(ov[8 * v + 3] * inv),
-                                         __float_as_uint(ov[8 * v + 4] * inv),
-                                         __float_as_uint(ov[8 * v + 5] * inv),
-                                         __float_as_uint(ov[8 * v + 6] * inv),
-                                         __float_as_uint(ov[8 * v + 7] * inv));
+            float l = (la.x + la.y) + (lb.x + lb.y);
+            float w0 = 1.f, w1 = 0.f;  // weights of the halves of a split pair
+            if (split) {
+                if (t == 1) {  // its half stays in TMEM for row tile 0
+                    half[row] = make_float2(m_used, l);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(C::MG));
+                        mbar_arrive(bar(C::WE + ws));
                     }
+                    continue;
                 }
-                // +inf marks a row that sees a key without a page; a NaN score leaves NaN
-                if (real) prm.slot_lse[dst] = hit ? INFINITY : l2;
-                if (tid == 0 && pc.a == 0) {
-                    Cut d;
-                    d.valid = 1;
-                    d.tok0 = pc.tok0;
-                    d.ntok = pc.ntok;
-                    d.h = pc.h;
-                    d.nt = pc.nt;
-                    d.S = sch->S;
-                    d.cu = pc.cu;
-                    d.span = pc.span;
-                    d.Wc = sch->Wc;
-                    prm.cut[blockIdx.x] = d;
+                ok = mbar_wait(bar(C::MG), halves & 1, abort_flag, prm.dev_status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                ++halves;
+                const float2 o = half[row];
+                const float mm = fmaxf(m_used, o.x);
+                w0 = m_used == -INFINITY ? 0.f : ex2_approx(m_used - mm);
+                w1 = o.x == -INFINITY ? 0.f : ex2_approx(o.x - mm);
+                l = l * w0 + o.y * w1;
+                m_used = mm;
+            }
+            ok = mbar_wait(bar(C::BK + ws), (piece / C::NW) & 1, abort_flag, prm.dev_status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const bool hit = w.bad_key < lim;
+            const float inv = l > 0.f ? rcp_approx(l) : isnan(l) ? l : 0.f;
+            const float l2 = l > 0.f ? m_used + lg2_approx(l) : isnan(l) ? l : -INFINITY;
+            w0 = hit ? 0.f : w0 * inv;
+            w1 = hit ? 0.f : w1 * inv;
+            const int token = (split ? 0 : t * prm.npt) + row / prm.G;
+            const bool real = lim != INT_MAX, whole = w.whole != 0;
+            const long at = (long)(w.tok0 + token) * prm.Hq + (long)w.h * prm.G + row % prm.G;
+            const long dst =
+                ((long)blockIdx.x * 2 + (w.a == 0 ? 1 : 0)) * 2 * kRows + t * kRows + row;
+            float *ps = prm.slot_o + dst * D;
+            uint16_t *po = prm.out + at * D;
+#pragma unroll 1
+            for (int c = 0; n > 0 && c < D; c += 16) {
+                float ov[16];
+                tmem_ld16(o_addr + c, ov);
+                if (split) {
+                    float o1[16];
+                    tmem_ld16(o_addr + 128 + c, o1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) ov[q] = ov[q] * w0 + o1[q] * w1;
+                } else {
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) ov[q] *= w0;
+                }
+                if (!real) continue;
+                if (whole) {
+                    uint32_t pk[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        pk[q] = hit ? 0u : pack_bf16x2(ov[2 * q], ov[2 * q + 1]);
+                    if (prm.wide) {  // a whole sector
+                        st_global_v8(po + c, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6],
+                                     pk[7]);
+                    } else {
+                        *reinterpret_cast<uint4 *>(po + c) =
+                            make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        *reinterpret_cast<uint4 *>(po + c + 8) =
+                            make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                    }
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 16; v += 8)
+                        st_global_v8(ps + c + v, __float_as_uint(ov[v]),
+                                     __float_as_uint(ov[v + 1]), __float_as_uint(ov[v + 2]),
+                                     __float_as_uint(ov[v + 3]), __float_as_uint(ov[v + 4]),
+                                     __float_as_uint(ov[v + 5]), __float_as_uint(ov[v + 6]),
+                                     __float_as_uint(ov[v + 7]));
                 }
             }
-            if (n > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::OE + t));
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (n > 0) mbar_arrive(bar(C::OE + t));
+                if (split) mbar_arrive(bar(C::OE + 1));
+                mbar_arrive(bar(C::WE + ws));
+            }
+            if (real) {
+                // +inf marks a row of a partial that sees a key without a page; a NaN
+                // score leaves NaN
+                if (!whole) prm.slot_lse[dst] = hit ? INFINITY : l2;
+                else if (prm.lse != nullptr) prm.lse[at] = hit ? -INFINITY : l2 * kLn2;
             }
             if (hit && real) report_status(prm.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
         }
@@ -910,6 +1093,7 @@ int launch_chunk(const ChunkArgs &a, cudaStream_t stream) {
     p.log2_ps = lg;
     p.box_rows = box_rows;
     p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
     if (cudaFuncSetAttribute(chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmem) != cudaSuccess)
         return BDSA_CUDA_ERROR;
