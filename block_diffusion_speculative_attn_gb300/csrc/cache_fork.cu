@@ -10,11 +10,11 @@
 // every page, its first entry in the old table (atomic min), the new rows that hold
 // it whole (atomic add) and the first that ends in it (atomic min).  The results of
 // those do not depend on their order, so neither do the tables or the ring.  Four
-// steps, each over all rows with a warp a row:
+// steps, with a warp a row:
+//   clear   the scattered arrays
 //   mark    the three scatters
 //   count   pages that each old row gives back, new rows that need a fresh page
-//   scan    their prefix sums over the rows
-//   write   the new table, the copies, the ring
+//   write   the new table, the copies, the ring (every CTA sums the counts itself)
 #include <cuda_runtime.h>
 #include <limits.h>
 
@@ -26,7 +26,9 @@ namespace bdsa {
 namespace {
 
 constexpr uint32_t kNone = 0xFFFFFFFFu;
-constexpr int kForkThreads = 256, kScanThreads = 1024;
+constexpr int kForkThreads = 512, kForkCtas = 16;
+// Table entries and pages up to which one cluster takes the call.
+constexpr long long kClusterWork = 1 << 18;
 
 // The part of the work that a warp takes.
 struct Share {
@@ -136,21 +138,23 @@ __device__ void step_count(const ForkArgs &a) {
     }
 }
 
-// Exclusive prefix sums of v[0, n) in place, the total in v[n]: one CTA.
-__device__ void scan_rows(int32_t *v, int n) {
+// Exclusive prefix sums of v[0, n) into the CTA's out[0, n], the total in out[n].
+__device__ void scan_rows(const int32_t *v, int n, int *out) {
     __shared__ int s_w[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x / 32;
-    const int per = (n + blockDim.x - 1) / blockDim.x;
+    for (int i = tid; i < n; i += blockDim.x) out[i] = __ldcg(v + i);
+    // (an odd number of rows in a row a thread: no bank conflicts)
+    const int per = ((n + (int)blockDim.x - 1) / (int)blockDim.x) | 1;
     const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
+    __syncthreads();
     int sum = 0;
-    for (int i = i0; i < i1; ++i) sum += __ldcg(v + i);
+    for (int i = i0; i < i1; ++i) sum += out[i];
     int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int t = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += t;
     }
-    __syncthreads();
     if (lane == 31) s_w[warp] = inc;
     __syncthreads();
     int before = inc - sum, all = 0;
@@ -159,14 +163,19 @@ __device__ void scan_rows(int32_t *v, int n) {
         all += s_w[w];
     }
     for (int i = i0; i < i1; ++i) {
-        const int c = __ldcg(v + i);
-        v[i] = before;
+        const int c = out[i];
+        out[i] = before;
         before += c;
     }
-    if (tid == 0) v[n] = all;
+    if (tid == 0) out[n] = all;
+    __syncthreads();
 }
 
 __device__ void step_write(const ForkArgs &a) {
+    extern __shared__ int s_rows[];
+    int *s_copies = s_rows, *s_gone = s_rows + a.bs_out + 1;
+    scan_rows(a.copies, a.bs_out, s_copies);
+    scan_rows(a.gone, a.bs_in, s_gone);
     const Share s = share();
     const uint32_t np = (uint32_t)a.num_pages;
     const int head_in = __ldg(a.free_state), count_in = __ldg(a.free_state + 1);
@@ -174,7 +183,7 @@ __device__ void step_write(const ForkArgs &a) {
         head_in >= 0 && head_in < a.num_pages && count_in >= 0 && count_in <= a.num_pages;
     const uint32_t head = state_ok ? (uint32_t)head_in : 0u;
     const int count = state_ok ? count_in : 0;
-    const int want = __ldcg(a.copies + a.bs_out), gone = __ldcg(a.gone + a.bs_in);
+    const int want = s_copies[a.bs_out], gone = s_gone[a.bs_in];
     const int popped = min(want, count);
     // more pages in use and free than the pool has: nothing goes back
     const bool push = state_ok && (long long)count + gone <= a.num_pages;
@@ -191,7 +200,7 @@ __device__ void step_write(const ForkArgs &a) {
             bool bad;
             const int r = (int)x, n = owned_pages(a, r, bad);
             report |= bad;
-            int at = __ldcg(a.gone + r);
+            int at = s_gone[r];
             for (int j0 = 0; j0 < n; j0 += 32) {
                 const int j = j0 + s.lane;
                 const long long e = (long long)r * a.max_pages + j;
@@ -214,7 +223,7 @@ __device__ void step_write(const ForkArgs &a) {
             int end = old, fresh = -1;  // its last page; a fresh one
             bool have = k.tail > 0;
             if (copy) {
-                const int at = __ldcg(a.copies + r);
+                const int at = s_copies[r];
                 have = at < popped;
                 if (have) {
                     uint64_t cell = (uint64_t)head + (uint64_t)at;
@@ -259,8 +268,27 @@ __device__ void step_write(const ForkArgs &a) {
     if (report) report_status(a.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
 }
 
-__global__ void __launch_bounds__(kForkThreads) fork_clear_kernel(const ForkArgs a) {
+// Everything before is done and seen by every CTA of the cluster.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One cluster does all steps: a launch instead of four.
+__global__ void __launch_bounds__(kForkThreads) fork_cluster_kernel(const ForkArgs a) {
     grid_dependency_wait();
+    grid_launch_dependents();
+    step_clear(a);
+    cluster_sync();
+    step_mark(a);
+    cluster_sync();
+    step_count(a);
+    cluster_sync();
+    step_write(a);
+}
+
+// The steps as grids, for tables that one cluster would be long about.
+__global__ void __launch_bounds__(kForkThreads) fork_clear_kernel(const ForkArgs a) {
     step_clear(a);
 }
 __global__ void __launch_bounds__(kForkThreads) fork_mark_kernel(const ForkArgs a) {
@@ -268,10 +296,6 @@ __global__ void __launch_bounds__(kForkThreads) fork_mark_kernel(const ForkArgs 
 }
 __global__ void __launch_bounds__(kForkThreads) fork_count_kernel(const ForkArgs a) {
     step_count(a);
-}
-__global__ void __launch_bounds__(kScanThreads) fork_scan_kernel(const ForkArgs a) {
-    scan_rows(a.copies, a.bs_out);
-    scan_rows(a.gone, a.bs_in);
 }
 __global__ void __launch_bounds__(kForkThreads) fork_write_kernel(const ForkArgs a) {
     step_write(a);
@@ -295,15 +319,49 @@ int launch_cache_fork(ForkArgs a, void *workspace, cudaStream_t stream) {
     a.gone = reinterpret_cast<int32_t *>(ws + 3 * pages);
     a.copies = reinterpret_cast<int32_t *>(ws + 3 * pages + up256(4 * ((size_t)a.bs_in + 1)));
     const long long rows = (long long)a.bs_in + a.bs_out;
+    const size_t smem = 4 * ((size_t)rows + 2);
+    // past the default 48 KB, on this device; the same limit in every call, so that
+    // host threads do not undo one another's
+    constexpr int kMost = 4 * (2 * BDSA_TABLE_MAX_REQUESTS + 2);
+    auto more = [&](const void *k) {
+        return smem <= 44 * 1024 ||
+               cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) ==
+                   cudaSuccess;
+    };
+    if (rows * a.max_pages + a.num_pages <= kClusterWork) {
+        if (!more((const void *)fork_cluster_kernel) ||
+            cudaFuncSetAttribute((const void *)fork_cluster_kernel,
+                                 cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                 1) != cudaSuccess)
+            return BDSA_CUDA_ERROR;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kForkCtas);
+        cfg.blockDim = dim3(kForkThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kForkCtas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, fork_cluster_kernel, (const ForkArgs)a) == cudaSuccess
+                   ? BDSA_OK
+                   : BDSA_CUDA_ERROR;
+    }
+    if (!more((const void *)fork_write_kernel)) return BDSA_CUDA_ERROR;
     const unsigned warps = kForkThreads / 32;
     const unsigned by_row = (unsigned)((rows + warps - 1) / warps);
     const unsigned by_page =
         (unsigned)(((long long)a.num_pages + kForkThreads - 1) / kForkThreads);
+    // (every CTA of the last step sums all rows: not many more than fill the GPU)
+    const unsigned few = by_row < 608 ? by_row : 608;
     fork_clear_kernel<<<by_page < 1024 ? by_page : 1024, kForkThreads, 0, stream>>>(a);
     fork_mark_kernel<<<by_row, kForkThreads, 0, stream>>>(a);
     fork_count_kernel<<<by_row, kForkThreads, 0, stream>>>(a);
-    fork_scan_kernel<<<1, kScanThreads, 0, stream>>>(a);
-    fork_write_kernel<<<by_row, kForkThreads, 0, stream>>>(a);
+    fork_write_kernel<<<few, kForkThreads, smem, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? BDSA_OK : BDSA_CUDA_ERROR;
 }
 

@@ -46,7 +46,9 @@ constexpr int kMinCost = 768;   // a CTA takes at least this cost
 // The unit that a CTA left cut after its first piece.
 struct Cut {
     int valid, tok0, ntok, h, nt, S;
-    long long cu, span, Wc;  // the unit's first cost and its cost, the whole call's
+    long long cu, span;  // the unit's first cost and its cost
+    long long each;      // the CTAs' shares
+    int rem;
 };
 
 struct ChunkParams {
@@ -110,9 +112,22 @@ struct Piece {
     long long cu, span;   // the unit's first cost and its cost
 };
 
+// The unit's first tile that is not before cost x: whole tiles, to the nearest.
 __device__ __forceinline__ int tile_at(long long x, long long span, int nt) {
-    return x >= span ? nt : x <= kUnitCost ? 0 : min(nt, (int)((x - kUnitCost) >> 7));
+    return x >= span ? nt : x <= kUnitCost ? 0 : min(nt, (int)((x - kUnitCost + 64) >> 7));
 }
+
+// a / b for 0 <= a, 0 < b: a 64-bit division is a long subroutine here.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    return ((uint64_t)(a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// Where CTA b's share of the cost starts: equal shares, the first rem one longer.
+struct Shares {
+    long long each;
+    int rem;
+    __device__ long long start(int b) const { return b * each + min(b, rem); }
+};
 
 // Walks the pieces of a cost range: one search for the first unit, then unit by unit.
 struct Walk {
@@ -123,7 +138,7 @@ struct Walk {
         r = r0;
         q = load_req(p, r);
         const long long rel = c - base;
-        h = (int)(rel / q.head);
+        h = (int)divide(rel, q.head);
         const long long in = rel - h * q.head;
         int lo = 0, hi = q.P;  // pairs_before(lo) <= in < pairs_before(hi)
         while (hi - lo > 1) {
@@ -282,7 +297,8 @@ struct CSched {
     uint32_t tmem;
     int abort, r0, S;
     long long wsum[12];
-    long long c0, c1, base, Wc;
+    long long c0, c1, base;
+    Shares sh;
 };
 static_assert(sizeof(CSched) <= 256, "the schedule state has 256 bytes");
 
@@ -365,14 +381,13 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
         const int i0 = min(bs, tid * per), i1 = min(bs, i0 + per);
         // offsets that do not run up from 0 to at most T: no row is anybody's
         bool wrong = false;
+        long long sum = 0;
         for (int r = i0; r < i1; ++r) {
             const int o0 = __ldg(prm.cu + r), o1 = __ldg(prm.cu + r + 1);
-            wrong |= o1 < o0 || (r == 0 && o0 != 0) || (r == bs - 1 && o1 > prm.T);
+            const bool off = o1 < o0 || o0 < 0 || (r == 0 && o0 != 0) || o1 > prm.T;
+            wrong |= off;
+            if (!off) sum += load_req(prm, r).head * prm.Hkv;
         }
-        wrong = __syncthreads_or(wrong);
-        long long sum = 0;
-        if (!wrong)
-            for (int r = i0; r < i1; ++r) sum += load_req(prm, r).head * prm.Hkv;
         long long inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -380,17 +395,21 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
             if (lane >= o) inc += t;
         }
         if (lane == 31) sch->wsum[warp] = inc;
-        __syncthreads();
+        wrong = __syncthreads_or(wrong);
         long long wex = 0, Wc = 0;
         for (int w = 0; w < C::kThreads / 32; ++w) {
             if (w < warp) wex += sch->wsum[w];
             Wc += sch->wsum[w];
         }
-        const long long S = max(1LL, min((long long)gridDim.x, Wc / kMinCost));
-        const long long b = blockIdx.x;
-        const long long c0 = b < S ? b * Wc / S : Wc, c1 = b < S ? (b + 1) * Wc / S : Wc;
+        if (wrong) Wc = 0;
+        const int S = (int)max(1LL, min((long long)gridDim.x, Wc / kMinCost));
+        Shares sh;
+        sh.each = divide(Wc, S);
+        sh.rem = (int)(Wc - sh.each * S);
+        const int b = blockIdx.x;
+        const long long c0 = b < S ? sh.start(b) : Wc, c1 = b < S ? sh.start(b + 1) : Wc;
         long long at = wex + inc - sum;
-        if (at <= c0 && c0 < at + sum) {
+        if (c0 < c1 && at <= c0 && c0 < at + sum) {
             for (int r = i0; r < i1; ++r) {
                 const long long cost = load_req(prm, r).head * prm.Hkv;
                 if (at <= c0 && c0 < at + cost) {
@@ -403,8 +422,8 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
         if (tid == 0) {
             sch->c0 = c0;
             sch->c1 = c1;
-            sch->S = (int)S;
-            sch->Wc = Wc;
+            sch->S = S;
+            sch->sh = sh;
             prm.cut[blockIdx.x].valid = 0;
             if (wrong && blockIdx.x == 0) report_status(prm.dev_status, BDSA_DEVICE_OUT_OF_RANGE);
         }
@@ -461,7 +480,8 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                             d.S = sch->S;
                             d.cu = pc.cu;
                             d.span = pc.span;
-                            d.Wc = sch->Wc;
+                            d.each = sch->sh.each;
+                            d.rem = sch->sh.rem;
                             prm.cut[blockIdx.x] = d;
                         }
                         mbar_arrive(bar(C::WF + ws));
@@ -977,7 +997,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
     int np = 0;
     for (int k0 = 1; np == 0 && b + k0 < d.S; k0 += 32) {
         const int k = k0 + lane;
-        const long long end = (long long)(b + k + 1) * d.Wc / d.S;
+        const long long end = Shares{d.each, d.rem}.start(b + k + 1);
         const bool done = b + k >= d.S - 1 || tile_at(end - d.cu, d.span, d.nt) >= d.nt;
         const uint32_t m = __ballot_sync(0xffffffffu, done);
         if (m != 0) np = k0 + __ffs(m);  // pieces: this CTA's and those up to that one

@@ -397,11 +397,14 @@ def test_accepted_path_compacted_after_a_tree():
     parent = np.full((bs, nodes), -1)
     for i in range(1, nodes):
         parent[:, i] = rng.integers(max(0, i - 6), i, bs)
-    ids = rng.integers(0, 4, (bs, nodes))
-    p = torch.softmax(torch.randn(bs, nodes, V) + 9 * (torch.arange(V) < 4), -1).to(DEV)
+    ids = np.tile(np.arange(nodes), (bs, 1))
+    p = np.zeros((bs, nodes, V), np.float32)  # every node draws the token of its last child
+    for r in range(bs):
+        for i in range(nodes):
+            kids = np.flatnonzero(parent[r] == i)
+            p[r, i, kids[-1] if len(kids) else V - 1] = 1.0
     ctx = rng.integers(0, 40, bs)
-    acc = bdsa.tree_accept(i32(ids), i32(parent), p.contiguous(),
-                           torch.rand(bs, nodes).to(DEV), i32(ctx))
+    acc = bdsa.tree_accept(i32(ids), i32(parent), torch.from_numpy(p).to(DEV), None, i32(ctx))
     table = rng.permutation(bs * 6).reshape(bs, 6)
     caches = rand((4, bs * 6 * ps, 2, 64), 3, torch.bfloat16)
     before, st = bits(caches), status()
