@@ -29,6 +29,7 @@ Calls (all asynchronous on the current stream):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -697,6 +698,11 @@ def chunk_attn_workspace_bytes(D, sms: int = 0) -> int:
     return int(lib().bdsa_chunk_attn_workspace_bytes(D, sms))
 
 
+@functools.lru_cache(maxsize=None)
+def _chunk_workspace(D, sms, index) -> int:
+    return chunk_attn_workspace_bytes(D, sms or num_sms(index))
+
+
 def chunk_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *, page_size: int,
                      scale: float, mask_block: int = 1, num_pages: int | None = None, out=None,
                      lse=None, workspace=None, dev_status=None, sms: int = 0):
@@ -724,8 +730,8 @@ def chunk_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *, p
     if out is None:
         out = torch.empty((T, Hq, D), dtype=bf16, device=q.device)
     if workspace is None:
-        workspace = torch.empty(chunk_attn_workspace_bytes(D, sms or num_sms(q.device)),
-                                dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(_chunk_workspace(D, sms, index), dtype=torch.uint8,
+                                device=q.device)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     _launch(lib().bdsa_chunk_attn_paged, "bdsa_chunk_attn_paged", index, q.data_ptr(), stride,

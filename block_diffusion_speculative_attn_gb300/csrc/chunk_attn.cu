@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                 // ---- the maximum (S is read twice: 128 scores a thread held over both
                 // passes are half of its registers, and code of four times the size)
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
+#pragma unroll
                 for (int b = 0; b < kBN; b += 64) {
                     float sv[64];
                     tmem_ld32(s_addr + b, *reinterpret_cast<float(*)[32]>(&sv[0]));
@@ -815,6 +815,9 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                     }
                     fence_proxy_async_smem();
                 }
+                // (the next 32 scores are on their way while these become P)
+                float sv[2][32];
+                tmem_ld32(s_addr, sv[0]);
                 // The row tiles' exponentials in turn: at the same time each takes
                 // twice as long (the special function unit is shared), and then
                 // both row tiles' MMAs come at once and nothing overlaps.
@@ -827,9 +830,6 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                 }
                 const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
                 const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(neg_m, neg_m);
-                // (the next 32 scores are on their way while these become P)
-                float sv[2][32];
-                tmem_ld32(s_addr, sv[0]);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
 #pragma unroll
