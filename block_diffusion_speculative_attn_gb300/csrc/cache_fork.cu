@@ -10,7 +10,8 @@
 // every page, its first entry in the old table (atomic min), the new rows that hold
 // it whole (atomic add) and the first that ends in it (atomic min).  The results of
 // those do not depend on their order, so neither do the tables or the ring.  Four
-// steps, with a warp a row:
+// steps, with a warp for each part of a row (kPart entries at least, a whole row where
+// there are many; 16 rows of 8192 pages by whole rows 506 us, in parts 22):
 //   clear   the scattered arrays
 //   mark    the three scatters
 //   count   pages that each old row gives back, new rows that need a fresh page
@@ -18,6 +19,7 @@
 #include <cuda_runtime.h>
 #include <limits.h>
 
+#include "attn_common.cuh"
 #include "bdsa_device.cuh"
 #include "bdsa_internal.h"
 #include "cache_internal.h"
@@ -27,8 +29,12 @@ namespace {
 
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr int kForkThreads = 512, kForkCtas = 16;
-// Table entries and pages up to which one cluster takes the call.
-constexpr long long kClusterWork = 1 << 18;
+// Table entries and pages up to which one cluster takes the call: 64 rows of 64 pages
+// 11.4 us in one cluster, 11.8 in four grids (and three launches more for the host);
+// 256 rows 16 and 12, 512 rows 26 and 13, 2048 rows of 128 pages 114 and 27.
+constexpr long long kClusterWork = 1 << 15;
+// Entries of a warp's part of a row at least, and parts of a table at most.
+constexpr int kPart = 128, kMaxParts = BDSA_TABLE_MAX_REQUESTS;
 
 // The part of the work that a warp takes.
 struct Share {
@@ -82,27 +88,48 @@ __device__ void step_clear(const ForkArgs &a) {
     }
 }
 
+// A warp's part of a row: the row and its entries [lo, hi).
+struct Part {
+    int r, lo, hi;
+    bool old, first;  // a row of the old table; the row's first part
+};
+__device__ __forceinline__ long long parts_of(const ForkArgs &a) {
+    return (long long)a.bs_in * a.parts_in + (long long)a.bs_out * a.parts_out;
+}
+__device__ __forceinline__ Part part_at(const ForkArgs &a, long long x) {
+    const long long in = (long long)a.bs_in * a.parts_in;
+    Part p;
+    p.old = x < in;
+    const int y = (int)(p.old ? x : x - in), n = p.old ? a.parts_in : a.parts_out;
+    const int len = p.old ? a.len_in : a.len_out;
+    p.r = y / n;
+    p.lo = (y - p.r * n) * len;
+    p.hi = min(a.max_pages, p.lo + len);
+    p.first = p.lo == 0;
+    return p;
+}
+
 __device__ void step_mark(const ForkArgs &a) {
     const Share s = share();
-    for (long long x = s.warp; x < (long long)a.bs_in + a.bs_out; x += s.warps) {
-        if (x < a.bs_in) {
+    for (long long x = s.warp, n = parts_of(a); x < n; x += s.warps) {
+        const Part p = part_at(a, x);
+        if (p.old) {
             bool bad;
-            const int r = (int)x, n = owned_pages(a, r, bad);
-            const long long at = (long long)r * a.max_pages;
-            for (int j = s.lane; j < n; j += 32) {
+            const int hi = min(p.hi, owned_pages(a, p.r, bad));
+            const long long at = (long long)p.r * a.max_pages;
+            for (int j = p.lo + s.lane; j < hi; j += 32) {
                 const int id = __ldg(a.block_table + at + j);
                 if (in_pool(a, id)) atomicMin(a.first + id, (uint32_t)(at + j));
             }
         } else {
-            const int r = (int)(x - a.bs_in);
-            const Kept k = kept_of(a, r);
-            for (int j = s.lane; j < k.whole; j += 32) {
+            const Kept k = kept_of(a, p.r);
+            for (int j = p.lo + s.lane; j < min(p.hi, k.whole); j += 32) {
                 const int id = __ldg(k.row + j);
                 if (in_pool(a, id)) atomicAdd(a.refs + id, 1);
             }
-            if (s.lane == 0 && k.tail > 0) {
+            if (p.first && s.lane == 0 && k.tail > 0) {
                 const int id = __ldg(k.row + k.whole);
-                if (in_pool(a, id)) atomicMin(a.heir + id, (uint32_t)r);
+                if (in_pool(a, id)) atomicMin(a.heir + id, (uint32_t)p.r);
             }
         }
     }
@@ -122,18 +149,20 @@ __device__ __forceinline__ bool is_gone(const ForkArgs &a, long long at) {
 
 __device__ void step_count(const ForkArgs &a) {
     const Share s = share();
-    for (long long x = s.warp; x < (long long)a.bs_in + a.bs_out; x += s.warps) {
-        if (x < a.bs_in) {
+    for (long long x = s.warp, n = parts_of(a); x < n; x += s.warps) {
+        const Part p = part_at(a, x);
+        if (p.old) {
             bool bad;
-            const int r = (int)x, n = owned_pages(a, r, bad);
+            const int hi = min(p.hi, owned_pages(a, p.r, bad));
             int c = 0;
-            for (int j = s.lane; j < n; j += 32) c += is_gone(a, (long long)r * a.max_pages + j);
+            for (int j = p.lo + s.lane; j < hi; j += 32)
+                c += is_gone(a, (long long)p.r * a.max_pages + j);
             c = __reduce_add_sync(0xffffffffu, c);
-            if (s.lane == 0) a.gone[r] = c;
-        } else if (s.lane == 0) {
-            const int r = (int)(x - a.bs_in);
+            if (s.lane == 0) a.gone[x] = c;
+        } else if (p.first && s.lane == 0) {
             int id;
-            a.copies[r] = needs_copy(a, kept_of(a, r), r, id);
+            a.copies[p.r] = needs_copy(a, kept_of(a, p.r), p.r, id);
+            a.shared_out[p.r] = 0;
         }
     }
 }
@@ -175,7 +204,7 @@ __device__ void step_write(const ForkArgs &a) {
     extern __shared__ int s_rows[];
     int *s_copies = s_rows, *s_gone = s_rows + a.bs_out + 1;
     scan_rows(a.copies, a.bs_out, s_copies);
-    scan_rows(a.gone, a.bs_in, s_gone);
+    scan_rows(a.gone, a.bs_in * a.parts_in, s_gone);
     const Share s = share();
     const uint32_t np = (uint32_t)a.num_pages;
     const int head_in = __ldg(a.free_state), count_in = __ldg(a.free_state + 1);
@@ -183,7 +212,7 @@ __device__ void step_write(const ForkArgs &a) {
         head_in >= 0 && head_in < a.num_pages && count_in >= 0 && count_in <= a.num_pages;
     const uint32_t head = state_ok ? (uint32_t)head_in : 0u;
     const int count = state_ok ? count_in : 0;
-    const int want = s_copies[a.bs_out], gone = s_gone[a.bs_in];
+    const int want = s_copies[a.bs_out], gone = s_gone[a.bs_in * a.parts_in];
     const int popped = min(want, count);
     // more pages in use and free than the pool has: nothing goes back
     const bool push = state_ok && (long long)count + gone <= a.num_pages;
@@ -194,18 +223,20 @@ __device__ void step_write(const ForkArgs &a) {
         a.free_state_out[1] = state_ok ? count - popped + (push ? gone : 0) : count_in;
         report = !push || popped < want;
     }
-    for (long long x = s.warp; x < (long long)a.bs_in + a.bs_out; x += s.warps) {
-        if (x < a.bs_in) {
+    for (long long x = s.warp, all = parts_of(a); x < all; x += s.warps) {
+        const Part p = part_at(a, x);
+        const int r = p.r;
+        if (p.old) {
             // ---- pages that go back, in the order of their entries
             bool bad;
-            const int r = (int)x, n = owned_pages(a, r, bad);
+            const int hi = min(p.hi, owned_pages(a, r, bad));
             report |= bad;
-            int at = s_gone[r];
-            for (int j0 = 0; j0 < n; j0 += 32) {
+            int at = s_gone[x];
+            for (int j0 = p.lo; j0 < hi; j0 += 32) {
                 const int j = j0 + s.lane;
                 const long long e = (long long)r * a.max_pages + j;
-                const bool g = j < n && is_gone(a, e);
-                report |= j < n && !in_pool(a, __ldg(a.block_table + e));
+                const bool g = j < hi && is_gone(a, e);
+                report |= j < hi && !in_pool(a, __ldg(a.block_table + e));
                 const uint32_t m = __ballot_sync(0xffffffffu, g);
                 if (g && push) {
                     const uint64_t k = (uint64_t)(at + __popc(m & ((1u << s.lane) - 1)));
@@ -214,51 +245,52 @@ __device__ void step_write(const ForkArgs &a) {
                 }
                 at += __popc(m);
             }
-        } else {
-            // ---- a new row
-            const int r = (int)(x - a.bs_in);
-            const Kept k = kept_of(a, r);
-            int old;
-            const bool copy = needs_copy(a, k, r, old);
-            int end = old, fresh = -1;  // its last page; a fresh one
-            bool have = k.tail > 0;
-            if (copy) {
-                const int at = s_copies[r];
-                have = at < popped;
-                if (have) {
-                    uint64_t cell = (uint64_t)head + (uint64_t)at;
-                    if (cell >= np) cell -= np;
-                    fresh = __ldcg(a.free_pages + cell);
-                    if (!in_pool(a, fresh)) fresh = -1;
-                    report |= fresh < 0;
-                }
-                end = fresh;
-            } else if (have && !in_pool(a, old)) {
-                end = -1;
-                report = true;
+            continue;
+        }
+        // ---- a new row
+        const Kept k = kept_of(a, r);
+        int old;
+        const bool copy = needs_copy(a, k, r, old);
+        int end = old, fresh = -1;  // its last page; a fresh one
+        bool have = k.tail > 0;
+        if (copy) {
+            const int at = s_copies[r];
+            have = at < popped;
+            if (have) {
+                uint64_t cell = (uint64_t)head + (uint64_t)at;
+                if (cell >= np) cell -= np;
+                fresh = __ldcg(a.free_pages + cell);
+                if (!in_pool(a, fresh)) fresh = -1;
+                report |= fresh < 0;
             }
-            report |= k.bad;
-            int shared = 0;
-            int32_t *out = a.block_table_out + (long long)r * a.max_pages;
-            for (int j = s.lane; j < a.max_pages; j += 32) {
-                int id = -1;
-                if (j < k.whole) {
-                    id = __ldg(k.row + j);
-                    if (in_pool(a, id)) {
-                        if (__ldcg(a.refs + id) > 1) shared = j + 1;
-                    } else {
-                        id = -1;
-                        report = true;
-                    }
-                } else if (j == k.whole && have) {
-                    id = end;
+            end = fresh;
+        } else if (have && !in_pool(a, old)) {
+            end = -1;
+            report = true;
+        }
+        report |= k.bad;
+        int shared = 0;
+        int32_t *out = a.block_table_out + (long long)r * a.max_pages;
+        for (int j = p.lo + s.lane; j < p.hi; j += 32) {
+            int id = -1;
+            if (j < k.whole) {
+                id = __ldg(k.row + j);
+                if (in_pool(a, id)) {
+                    if (__ldcg(a.refs + id) > 1) shared = j + 1;
+                } else {
+                    id = -1;
+                    report = true;
                 }
-                out[j] = id;
+            } else if (j == k.whole && have) {
+                id = end;
             }
-            shared = __reduce_max_sync(0xffffffffu, shared);
-            if (s.lane == 0) {
+            out[j] = id;
+        }
+        shared = __reduce_max_sync(0xffffffffu, shared);
+        if (s.lane == 0) {
+            if (shared > 0) atomicMax(a.shared_out + r, shared);
+            if (p.first) {
                 a.owned_out[r] = k.whole + (have ? 1 : 0);
-                a.shared_out[r] = shared;
                 a.copy_src[r] = fresh >= 0 ? old : -1;
                 a.copy_dst[r] = fresh;
                 a.copy_len[r] = fresh >= 0 ? k.tail : 0;
@@ -289,16 +321,30 @@ __global__ void __launch_bounds__(kForkThreads) fork_cluster_kernel(const ForkAr
 
 // The steps as grids, for tables that one cluster would be long about.
 __global__ void __launch_bounds__(kForkThreads) fork_clear_kernel(const ForkArgs a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
     step_clear(a);
 }
 __global__ void __launch_bounds__(kForkThreads) fork_mark_kernel(const ForkArgs a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
     step_mark(a);
 }
 __global__ void __launch_bounds__(kForkThreads) fork_count_kernel(const ForkArgs a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
     step_count(a);
 }
 __global__ void __launch_bounds__(kForkThreads) fork_write_kernel(const ForkArgs a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
     step_write(a);
+}
+
+// The rows' parts: as many as give a table kMaxParts at most.
+int parts_of_row(int bs, int max_pages) {
+    const int by_len = (max_pages + kPart - 1) / kPart, most = kMaxParts / (bs > 0 ? bs : 1);
+    return by_len < most ? by_len : most < 1 ? 1 : most;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -306,8 +352,8 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 }  // namespace
 
 size_t fork_workspace_bytes(int bs_in, int bs_out, int num_pages) {
-    return 3 * up256(4 * (size_t)num_pages) + up256(4 * ((size_t)bs_in + 1)) +
-           up256(4 * ((size_t)bs_out + 1));
+    return 3 * up256(4 * (size_t)num_pages) + up256(4 * (size_t)kMaxParts) +
+           up256(4 * (size_t)bs_out);
 }
 
 int launch_cache_fork(ForkArgs a, void *workspace, cudaStream_t stream) {
@@ -317,9 +363,14 @@ int launch_cache_fork(ForkArgs a, void *workspace, cudaStream_t stream) {
     a.heir = reinterpret_cast<uint32_t *>(ws + pages);
     a.refs = reinterpret_cast<int32_t *>(ws + 2 * pages);
     a.gone = reinterpret_cast<int32_t *>(ws + 3 * pages);
-    a.copies = reinterpret_cast<int32_t *>(ws + 3 * pages + up256(4 * ((size_t)a.bs_in + 1)));
+    a.copies = reinterpret_cast<int32_t *>(ws + 3 * pages + up256(4 * (size_t)kMaxParts));
+    a.parts_in = parts_of_row(a.bs_in, a.max_pages);
+    a.parts_out = parts_of_row(a.bs_out, a.max_pages);
+    a.len_in = (a.max_pages + a.parts_in - 1) / a.parts_in;
+    a.len_out = (a.max_pages + a.parts_out - 1) / a.parts_out;
     const long long rows = (long long)a.bs_in + a.bs_out;
-    const size_t smem = 4 * ((size_t)rows + 2);
+    const long long parts = (long long)a.bs_in * a.parts_in + (long long)a.bs_out * a.parts_out;
+    const size_t smem = 4 * ((size_t)a.bs_in * a.parts_in + (size_t)a.bs_out + 2);
     // past the default 48 KB, on this device; the same limit in every call, so that
     // host threads do not undo one another's
     constexpr int kMost = 4 * (2 * BDSA_TABLE_MAX_REQUESTS + 2);
@@ -353,16 +404,18 @@ int launch_cache_fork(ForkArgs a, void *workspace, cudaStream_t stream) {
     }
     if (!more((const void *)fork_write_kernel)) return BDSA_CUDA_ERROR;
     const unsigned warps = kForkThreads / 32;
-    const unsigned by_row = (unsigned)((rows + warps - 1) / warps);
+    const unsigned by_part = (unsigned)(parts > 0 ? (parts + warps - 1) / warps : 1);
     const unsigned by_page =
         (unsigned)(((long long)a.num_pages + kForkThreads - 1) / kForkThreads);
-    // (every CTA of the last step sums all rows: not many more than fill the GPU)
-    const unsigned few = by_row < 608 ? by_row : 608;
-    fork_clear_kernel<<<by_page < 1024 ? by_page : 1024, kForkThreads, 0, stream>>>(a);
-    fork_mark_kernel<<<by_row, kForkThreads, 0, stream>>>(a);
-    fork_count_kernel<<<by_row, kForkThreads, 0, stream>>>(a);
-    fork_write_kernel<<<few, kForkThreads, smem, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? BDSA_OK : BDSA_CUDA_ERROR;
+    // (every CTA of the last step sums all counts: not many more than fill the GPU)
+    const unsigned few = by_part < 608 ? by_part : 608;
+    auto step = [&](void (*k)(const ForkArgs), unsigned grid, size_t bytes) {
+        return launch_pdl(k, dim3(grid), dim3(kForkThreads), bytes, stream, a) == cudaSuccess;
+    };
+    const bool ok = step(fork_clear_kernel, by_page < 1024 ? by_page : 1024, 0) &&
+                    step(fork_mark_kernel, by_part, 0) && step(fork_count_kernel, by_part, 0) &&
+                    step(fork_write_kernel, few, smem);
+    return ok ? BDSA_OK : BDSA_CUDA_ERROR;
 }
 
 }  // namespace bdsa

@@ -78,10 +78,11 @@ struct ForkArgs {
     int32_t *owned_out, *shared_out, *free_state_out;
     int32_t *copy_src, *copy_dst, *copy_len; // [bs_out]
     int max_pages, num_pages, bs_in, bs_out, page_size;
+    int parts_in, len_in, parts_out, len_out;  // parts of a row, entries of a part
     // workspace
     uint32_t *first, *heir;  // [num_pages]: first old entry, first row that it ends
     int32_t *refs;           // [num_pages]: new rows that hold it whole
-    int32_t *copies, *gone;  // [bs_out + 1], [bs_in + 1]: pages popped / pushed before a row
+    int32_t *copies, *gone;  // [bs_out], [bs_in * parts_in]: pages popped, pushed
     int32_t *dev_status;
 };
 size_t fork_workspace_bytes(int bs_in, int bs_out, int num_pages);

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <limits.h>
 
+#include "attn_common.cuh"
 #include "bdsa_device.cuh"
 #include "bdsa_internal.h"
 #include "cache_internal.h"
@@ -205,20 +206,6 @@ __global__ void __launch_bounds__(kMoveThreads)
     }
 }
 
-template <typename K, typename... A>
-cudaError_t launch(K kernel, dim3 grid, int threads, cudaStream_t stream, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace
 
 int launch_cache_write(const WriteArgs &a, int num_sms, cudaStream_t stream) {
@@ -226,7 +213,7 @@ int launch_cache_write(const WriteArgs &a, int num_sms, cudaStream_t stream) {
     const int per = kThreads / lanes * kWriteRows;  // tokens a CTA takes at once
     const long long want = ((long long)a.T + per - 1) / per, most = 8LL * num_sms;
     const unsigned grid = (unsigned)(want < most ? want : most);
-    return launch(cache_write_kernel, dim3(grid), kThreads, stream, a, lanes) == cudaSuccess
+    return launch_pdl(cache_write_kernel, dim3(grid), dim3(kThreads), 0, stream, a, lanes) == cudaSuccess
                ? BDSA_OK
                : BDSA_CUDA_ERROR;
 }
@@ -241,8 +228,8 @@ int launch_cache_copy(const CopyArgs &a, void *const *caches, int n_caches, cuda
         for (int i = 0; i < nc; ++i) list.p[i] = static_cast<uint8_t *>(caches[c0 + i]);
         for (int e0 = 0; e0 < a.n; e0 += 65535) {
             const unsigned ne = (unsigned)(a.n - e0 < 65535 ? a.n - e0 : 65535);
-            if (launch(cache_copy_kernel, dim3(chunks, ne, nc), kThreads, stream, a, list,
-                       e0) != cudaSuccess)
+            if (launch_pdl(cache_copy_kernel, dim3(chunks, ne, nc), dim3(kThreads), 0, stream, a,
+                           list, e0) != cudaSuccess)
                 return BDSA_CUDA_ERROR;
         }
     }
@@ -263,8 +250,8 @@ int launch_cache_compact(const CompactArgs &a, void *const *caches, int n_caches
         parts = parts < 1 ? 1 : parts < rows32 ? parts : rows32;
         for (int r0 = 0; r0 < a.bs; r0 += 65535) {
             const unsigned nr = (unsigned)(a.bs - r0 < 65535 ? a.bs - r0 : 65535);
-            if (launch(cache_compact_kernel, dim3(grid, nr, (unsigned)parts), kMoveThreads,
-                       stream, a, list, nc, r0) != cudaSuccess)
+            if (launch_pdl(cache_compact_kernel, dim3(grid, nr, (unsigned)parts),
+                           dim3(kMoveThreads), 0, stream, a, list, nc, r0) != cudaSuccess)
                 return BDSA_CUDA_ERROR;
         }
     }

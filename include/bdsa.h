@@ -756,6 +756,8 @@ int32_t bdsa_cache_write(const void *k_new, int64_t k_stride, const void *v_new,
  * bs_in and bs_out <= BDSA_TABLE_MAX_REQUESTS, bs_in * max_pages_per_req < 2^31, any
  * page_size >= 1, num_pages * page_size < 2^31.  Workspace:
  * bdsa_cache_fork_workspace_bytes(...) bytes, 256-byte aligned, no initialisation.
+ * One launch for small tables, four chained with programmatic dependent launch for
+ * others.
  */
 size_t bdsa_cache_fork_workspace_bytes(int32_t bs_in, int32_t bs_out, int32_t num_pages);
 

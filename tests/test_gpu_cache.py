@@ -142,6 +142,20 @@ def test_fork_large():
     f.check()
 
 
+def test_fork_long_rows():
+    """Rows in several parts."""
+    Fork(9, 13, 1000, 16, 1, share=0.7).check()
+    Fork(3, 40, 8192, 16, 2, share=0.9).check()
+
+
+@pytest.mark.parametrize("pool", [1, 40000])
+def test_fork_of_no_rows_at_all(pool):
+    f = Fork(0, 0, 3, 16, 1)
+    f.pool, f.ring, f.state = pool, np.arange(pool), [0, 1]
+    out = f.check()
+    assert out["free_state"].tolist() == [0, 1]
+
+
 def test_fork_is_the_identity_for_rows_of_their_own():
     f = Fork(40, 40, 6, 16, 2, share=0.0)
     f.parent, f.keep = np.arange(40), f.owned * 16 - (f.owned > 0)
