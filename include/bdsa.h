@@ -687,7 +687,8 @@ int32_t bdsa_token_sample(const void *logits, int32_t dtype, int64_t l_stride_r,
  * Two launches, chained with programmatic dependent launch; the second joins the
  * row tiles that the equal shares of the first cut.  Workspace: at least
  * bdsa_chunk_attn_workspace_bytes(D, num_sms) bytes, 256-byte aligned, no
- * initialisation needed.
+ * initialisation needed; calls that share one workspace must be ordered on the same
+ * stream.
  */
 size_t bdsa_chunk_attn_workspace_bytes(int32_t D, int32_t num_sms);
 
