@@ -17,13 +17,28 @@
 // the log2-sum-exp of each row), which a second kernel joins.
 //
 // Inside a CTA (12 warps): warps 0-3 and 4-7 are the softmax of the two row tiles,
-// one thread a row; then a K producer (also Q), a V producer and an MMA issuer for
-// each row tile.  A row tile's S (128 columns of TMEM) is read by its softmax, which
+// one thread a row; then a K producer (also Q), which alone walks the CTA's range and
+// hands each piece on in shared memory, a V producer and an MMA issuer for each row
+// tile.  A row tile's S (128 columns of TMEM) is read by its softmax, which
 // writes P as bf16 over it; PV takes P from TMEM.  The two tiles alternate on the
 // tensor cores and share every K and V tile in shared memory.  A row tile whose rows
 // see no key of the unit's last tiles sits those out; where a pair has tokens for one
-// row tile alone, both take its rows, each over every other key tile.  O is rescaled in TMEM only
-// when a row's max grows by 2^8.
+// row tile alone, both take its rows, each over every other key tile.  O is rescaled in
+// TMEM only when a row's max grows by 2^8.
+//
+// What bounds it (us a call, launches in a graph):
+//   64 single tokens over 512-8192 keys of 8 KV heads, pages of 16    196  HBM: 1.23 GB
+//     at 0.93 of the copy rate (one row tile over all key tiles: 283 then)
+//   24 prompts of 17-2048 tokens, 32 heads                            353  1.0 PFLOP/s;
+//     161 key tiles a CTA of 1.55 us and 26 pieces of about 3 us
+//   8 x 512-1024 tokens in blocks of 32 behind 1024-8192, 16 heads    256  1.29 PFLOP/s
+//   4096 tokens behind 28672, 32 heads           1410 cool, 1440-1500 call after call at
+//     the power limit: 1.37-1.46 PFLOP/s (0.71-0.76 of the measured rate)
+// A pair's key tile costs about 1.6 us against 1.3 of MMAs: the exponentials of the two
+// row tiles follow one another (in turns, below), and with the trip from P over PV and
+// the next S they are longer than the other tile's MMAs.  A unit costs about 3 us
+// besides: instructions that run once a unit come from far (code of 127 KB instead of
+// 79: 565 us for the prompts), and O has to leave TMEM before the next unit's PV.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,8 +55,12 @@ namespace bdsa {
 namespace {
 
 constexpr int kRows = 128;      // query rows of a tile
-constexpr int kUnitCost = 256;  // keys a unit switch is charged (a Q load, an epilogue)
-constexpr int kMinCost = 768;   // a CTA takes at least this cost
+// Keys a unit switch is charged (a Q load, an epilogue): the prompts above take 389 us
+// with 128, 355 with 256, 360 with 384, 370 with 512.
+constexpr int kUnitCost = 256;
+// A CTA takes at least this cost: two units of one tile (with 384, 512 and 1536 nothing
+// above or smaller moves).
+constexpr int kMinCost = 768;
 
 // The unit that a CTA left cut after its first piece.
 struct Cut {
@@ -818,9 +837,10 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                 // (the next 32 scores are on their way while these become P)
                 float sv[2][32];
                 tmem_ld32(s_addr, sv[0]);
-                // The row tiles' exponentials in turn: at the same time each takes
-                // twice as long (the special function unit is shared), and then
-                // both row tiles' MMAs come at once and nothing overlaps.
+                // The row tiles' exponentials in turn: at the same time each takes about
+                // twice as long, and then both row tiles' MMAs come at once and nothing
+                // overlaps (the prompts 418 us instead of 353; with the turn handed on
+                // after a quarter, a half, three quarters of them 393, 382, 375).
                 const bool both = j < nboth;
                 if (both && (t == 1 || turn > 0)) {
                     ok = mbar_wait(bar(C::TK + t), (t == 1 ? turn : turn - 1) & 1, abort_flag,
