@@ -318,6 +318,62 @@ def test_compact_refuses_whole_requests():
     assert (want != before).any()
 
 
+def test_compact_rows_that_lie_behind_the_kept_ones():
+    """First tokens and a window of the last ones: several CTAs share a request."""
+    bs, ps, n = 3, 16, 900
+    keep = [4 + 200, 3, 4 + 440]
+    path = np.full((bs, max(keep)), -1)
+    for r, m in enumerate(keep):
+        path[r, :m] = np.concatenate([np.arange(min(4, m)), n - max(m - 4, 0) +
+                                      np.arange(max(m - 4, 0))])[:m]
+    table = np.random.default_rng(3).permutation(bs * 57).reshape(bs, 57)
+    caches = rand((3, bs * 57 * ps, 2, 64), 4, torch.bfloat16)
+    before, st = bits(caches), status()
+    for _ in range(2):  # (the rows that move stay where they were: the same again)
+        bdsa.cache_compact(caches, i32(table), i32(np.zeros(bs)), i32(path), page_size=ps,
+                           dev_status=st)
+        for c in range(3):
+            want, bad = oracle.cache_compact(before[c], table, np.zeros(bs), path, ps)
+            assert bad == 0 and (bits(caches)[c] == want).all()
+    assert int(st) == 0
+
+
+def test_lists_longer_than_a_grid():
+    n = 70001
+    cache = rand((1, 2 * n, 1, 8), 5)
+    want = cache.clone()
+    want[0, n:] = want[0, :n]
+    ids = torch.arange(n, dtype=torch.int32, device=DEV)
+    bdsa.cache_copy(cache, ids, ids + n, torch.ones_like(ids), page_size=1)
+    assert (bits(cache) == bits(want)).all()
+    # a request each: row 1 of its two moves to row 0
+    path = torch.ones((n, 1), dtype=torch.int32, device=DEV)
+    table = torch.stack([ids, ids + n], 1).contiguous()
+    want[0, :n] = want[0, n:]
+    cache[0, n:] += 1
+    want[0, :n], want[0, n:] = cache[0, n:], cache[0, n:]
+    bdsa.cache_compact(cache, table, torch.zeros_like(ids), path, page_size=1)
+    assert (bits(cache) == bits(want)).all()
+
+
+@pytest.mark.parametrize("rows", [20, 700])
+def test_fork_captured(rows):
+    """As one cluster and as four grids."""
+    f = Fork(rows, rows, 60, 16, 30, share=0.8)
+    want = f.check()
+    ring, parts = i32(f.ring), [i32(x) for x in (f.parent, f.keep, f.table, f.owned, f.state)]
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        out = bdsa.cache_fork(parts[0], parts[1], parts[2], parts[3], ring, parts[4],
+                              page_size=16)
+    for _ in range(3):
+        ring.copy_(i32(f.ring))
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(out[k], want[k]) for k in out) and torch.equal(ring, f.ring_dev)
+
+
 # ------------------------------------------------------------------ together
 def serving_step(caches, s, ps, x):
     """Prompts written and attended, forked into samples, extended by one token: the

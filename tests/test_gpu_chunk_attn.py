@@ -277,3 +277,57 @@ def test_matches_block_attention():
         tol = 2 * 2.0 ** -8 * (np.abs(out) + weight) + 2.0 ** -10 * weight
         assert (np.abs(out - out2.double().cpu().numpy()) <= tol).all()
         assert np.abs(lse - lse2.double().cpu().numpy()).max() < 1e-3
+
+
+@pytest.mark.parametrize("ps", [256, 1024])
+@pytest.mark.parametrize("bad", [False, True])
+def test_pages_of_several_tiles(ps, bad):
+    c = Case([300, 1, 40], [900, 2100, 0], Hq=4, Hkv=2, D=64, ps=ps, seed=21)
+    if bad:  # keys [ps, 2 ps) of request 0: its first tokens do not reach them at ps 1024
+        c.table[0, 1] = -3
+    c.check(status=16 if bad else 0)
+    c.status.zero_()
+    c.check(status=16 if bad else 0, sms=40)
+
+
+def test_many_requests():
+    rng = np.random.default_rng(22)
+    new = rng.integers(0, 3, 1100)
+    Case(new, rng.integers(0, 90, 1100), Hq=2, Hkv=1, D=64, ps=8, seed=22).check()
+
+
+@pytest.mark.parametrize("heads", [(64, 64), (40, 8), (128, 1)])
+def test_many_heads(heads):
+    Case([40, 1], [200, 65], *heads, D=128, ps=32, seed=23).check()
+
+
+@pytest.mark.parametrize("sms", [0, 30])
+def test_output_at_any_16_bytes(sms):
+    c = Case([70, 1, 3], [400, 900, 0], Hq=4, Hkv=2, D=128, ps=16, seed=24)
+    d = c.dev()
+    first = c.run(d, sms=sms)
+    flat = torch.full((c.T * 4 * 128 + 16,), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = flat[8:8 + c.T * 4 * 128].view(c.T, 4, 128)
+    assert out.data_ptr() % 32 == 16
+    bdsa.chunk_attn_paged(d["q"], d["k"], d["v"], d["table"], d["ctx"], d["cu"], page_size=16,
+                          scale=c.scale, out=out, sms=sms)
+    assert (out.double().cpu().numpy() == first[0]).all()
+    assert (flat[:8] == 7.0).all() and (flat[8 + c.T * 4 * 128:] == 7.0).all()
+
+
+def test_two_streams_at_once():
+    cases = [Case([200, 1, 1], [900, 3000, 70], Hq=8, Hkv=2, D=128, ps=16, seed=s)
+             for s in (25, 26)]
+    devs = [c.dev() for c in cases]
+    alone = [c.run(d) for c, d in zip(cases, devs)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = []
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, d, s in zip(cases, devs, streams):
+            with torch.cuda.stream(s):
+                outs.append(bdsa.chunk_attn_paged(d["q"], d["k"], d["v"], d["table"], d["ctx"],
+                                                  d["cu"], page_size=16, scale=c.scale))
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert (o.double().cpu().numpy() == alone[i % 2][0]).all()
