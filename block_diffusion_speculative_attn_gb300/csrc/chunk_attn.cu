@@ -9,7 +9,7 @@
 // Shape of the work: the (token, head of the group) rows of one (request, KV head)
 // are cut into tiles of npt whole tokens (at most 128 rows), two tiles to a pair.  A
 // unit is a pair over its keys, in 128-key tiles.  Units are ordered (request, KV
-// head, pair) and charged kUnitCost keys and those that they see; persistent CTAs
+// head, pair) and charged for a switch and the keys that they see; persistent CTAs
 // take equal ranges of that cost, so single tokens, prompts of any lengths and one
 // long document split alike over the GPU without a list of units.  All sums over a
 // request's pairs are closed forms, so a CTA finds its range by one scan of the
@@ -55,16 +55,18 @@ namespace bdsa {
 namespace {
 
 constexpr int kRows = 128;      // query rows of a tile
-// Keys a unit switch is charged (a Q load, an epilogue): the prompts above take 389 us
-// with 128, 355 with 256, 360 with 384, 370 with 512.
-constexpr int kUnitCost = 256;
-// A CTA takes at least this cost: two units of one tile (with 384, 512 and 1536 nothing
-// above or smaller moves).
-constexpr int kMinCost = 768;
+// The cost of a unit: a key counts kPairKey where both row tiles have tokens, kOneKey
+// where one has (a tile of those is 1.5 and 1.0-1.1 us), a switch kUnitCost (a Q load,
+// an epilogue: 2 tiles of a pair).  With one weight the mixed batch above took 70 us:
+// its CTAs ended between 45 and 68.
+constexpr int kPairKey = 3, kOneKey = 2;
+constexpr int kUnitCost = 768;
+// A CTA takes at least this cost: two units of one tile.
+constexpr int kMinCost = 2304;
 
 // The unit that a CTA left cut after its first piece.
 struct Cut {
-    int valid, tok0, ntok, h, nt, S;
+    int valid, tok0, ntok, h, nt, S, key;
     long long cu, span;  // the unit's first cost and its cost
     long long each;      // the CTAs' shares
     int rem;
@@ -87,8 +89,17 @@ struct Req {
     int L, n, tok, P;  // context, new tokens, the first one's row, pairs
     bool bad;          // lengths that the table row cannot hold: its rows become zero
     int pstar;         // pairs whose keys are not clipped at L + n
+    int last;          // cost of a key in the last pair
     long long head;    // cost of a KV head's pairs
 };
+
+// Cost of the pairs before pair x < P of a KV head: pair y sees L + min(n, (y + 1) w +
+// mb - 1) keys at most.
+__device__ __forceinline__ long long pairs_before(const ChunkParams &p, const Req &q, int x) {
+    const long long w = 2 * p.npt, a = min(x, q.pstar);
+    return x * (kUnitCost + (long long)kPairKey * q.L) +
+           kPairKey * (w * (a * (a + 1) / 2) + a * (p.mb - 1) + (x - a) * q.n);
+}
 
 __device__ __forceinline__ Req load_req(const ChunkParams &p, int r) {
     Req q;
@@ -102,18 +113,10 @@ __device__ __forceinline__ Req load_req(const ChunkParams &p, int r) {
     const int w = 2 * p.npt;
     q.P = (q.n + w - 1) / w;
     q.pstar = q.n >= p.mb ? (q.n - p.mb) / w : 0;
-    const long long ps = q.pstar;
-    q.head = (long long)q.P * (kUnitCost + q.L) + w * (ps * (ps + 1) / 2) + ps * (p.mb - 1) +
-             (q.P - ps) * q.n;
+    q.last = q.n - (q.P - 1) * w <= p.npt ? kOneKey : kPairKey;
+    q.head = q.P > 0 ? pairs_before(p, q, q.P - 1) + kUnitCost + q.last * ((long long)q.L + q.n)
+                     : 0;
     return q;
-}
-
-// Cost of the pairs before pair x of a KV head: pair y costs kUnitCost + L +
-// min(n, (y + 1) w + mb - 1).
-__device__ __forceinline__ long long pairs_before(const ChunkParams &p, const Req &q, int x) {
-    const long long w = 2 * p.npt, a = min(x, q.pstar);
-    return (long long)x * (kUnitCost + q.L) + w * (a * (a + 1) / 2) + a * (p.mb - 1) +
-           (x - a) * q.n;
 }
 
 // Keys that token i of the request sees.
@@ -129,11 +132,16 @@ struct Piece {
     int h, a, e, nt;      // KV head, tiles [a, e) of nt
     bool bad;
     long long cu, span;   // the unit's first cost and its cost
+    int key;              // the cost of one of its keys
 };
 
 // The unit's first tile that is not before cost x: whole tiles, to the nearest.
-__device__ __forceinline__ int tile_at(long long x, long long span, int nt) {
-    return x >= span ? nt : x <= kUnitCost ? 0 : min(nt, (int)((x - kUnitCost + 64) >> 7));
+__device__ __forceinline__ int tile_at(long long x, long long span, int nt, int key) {
+    if (x >= span) return nt;
+    if (x <= kUnitCost) return 0;
+    const uint64_t k = (uint64_t)(x - kUnitCost);
+    return min(nt, (int)(key == kPairKey ? (k + 64 * kPairKey) / (128 * kPairKey)
+                                         : (k + 64 * kOneKey) / (128 * kOneKey)));
 }
 
 // a / b for 0 <= a, 0 < b: a 64-bit division is a long subroutine here.
@@ -179,7 +187,8 @@ struct Walk {
             }
             const int w = 2 * p.npt;
             pc.cu = cu;
-            pc.span = kUnitCost + q.L + min((long long)q.n, (x + 1LL) * w + p.mb - 1);
+            pc.key = x == q.P - 1 ? q.last : kPairKey;
+            pc.span = kUnitCost + pc.key * (q.L + min((long long)q.n, (x + 1LL) * w + p.mb - 1));
             const long long from = c - cu, to = min(c1 - cu, pc.span);
             c = cu + to;
             pc.i0 = x * w;
@@ -190,8 +199,8 @@ struct Walk {
             }
             const int last = limit_of(p, q.L, q.n, pc.i0 + min(pc.ntok, w) - 1);
             pc.nt = (last + kBN - 1) / kBN;
-            pc.a = tile_at(from, pc.span, pc.nt);
-            pc.e = tile_at(to, pc.span, pc.nt);
+            pc.a = tile_at(from, pc.span, pc.nt, pc.key);
+            pc.e = tile_at(to, pc.span, pc.nt, pc.key);
             if (pc.a >= pc.e) continue;
             pc.r = r;
             pc.L = q.L;
@@ -497,6 +506,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                             d.h = pc.h;
                             d.nt = pc.nt;
                             d.S = sch->S;
+                            d.key = pc.key;
                             d.cu = pc.cu;
                             d.span = pc.span;
                             d.each = sch->sh.each;
@@ -761,7 +771,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                 tc_fence_after();
                 // ---- scores of keys that a row does not see become -inf
                 const int nvis = lim - t0;
-                if (__any_sync(0xffffffffu, nvis < kBN)) {
+                if (__builtin_expect(__any_sync(0xffffffffu, nvis < kBN), 0)) {
 #pragma unroll 1
                     for (int b = 0; b < kBN; b += 32) {
                         if (!__any_sync(0xffffffffu, nvis < b + 32)) continue;
@@ -796,7 +806,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                     m_used = m_new;
                     resc = true;
                 }
-                if (__any_sync(0xffffffffu, resc)) {
+                if (__builtin_expect(__any_sync(0xffffffffu, resc), 0)) {
                     const uint64_t a2 = f2_pack(alpha, alpha);
                     lacc[0] = f2_mul(lacc[0], a2);
                     lacc[1] = f2_mul(lacc[1], a2);
@@ -817,7 +827,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                 // V rows past the request's last key are whatever the page holds,
                 // and 0 * NaN is NaN: they become zeros before PV reads them
                 // (each row tile before its own PV; both write the same zeros)
-                if (t0 + kBN > n_keys) {
+                if (__builtin_expect(t0 + kBN > n_keys, 0)) {
                     const int vs = vi % C::NV;
                     ok = mbar_wait(bar(C::VF + vs), (vph0 + (uint32_t)(vi / C::NV)) & 1,
                                    abort_flag, prm.dev_status);
@@ -1018,7 +1028,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
     for (int k0 = 1; np == 0 && b + k0 < d.S; k0 += 32) {
         const int k = k0 + lane;
         const long long end = Shares{d.each, d.rem}.start(b + k + 1);
-        const bool done = b + k >= d.S - 1 || tile_at(end - d.cu, d.span, d.nt) >= d.nt;
+        const bool done = b + k >= d.S - 1 || tile_at(end - d.cu, d.span, d.nt, d.key) >= d.nt;
         const uint32_t m = __ballot_sync(0xffffffffu, done);
         if (m != 0) np = k0 + __ffs(m);  // pieces: this CTA's and those up to that one
     }
