@@ -88,6 +88,7 @@ struct ChunkParams {
 struct Req {
     int L, n, tok, P;  // context, new tokens, the first one's row, pairs
     bool bad;          // lengths that the table row cannot hold: its rows become zero
+    bool off;          // its offsets are not within q
     int pstar;         // pairs whose keys are not clipped at L + n
     int last;          // cost of a key in the last pair
     long long head;    // cost of a KV head's pairs
@@ -104,9 +105,11 @@ __device__ __forceinline__ long long pairs_before(const ChunkParams &p, const Re
 __device__ __forceinline__ Req load_req(const ChunkParams &p, int r) {
     Req q;
     const int c0 = __ldg(p.cu + r), c1 = __ldg(p.cu + r + 1);
-    q.tok = c0;
-    q.n = c1 - c0;
     q.L = __ldg(p.seq_lens + r);
+    q.tok = c0;
+    // (offsets that no row can have: the whole call does nothing then)
+    q.off = c0 < 0 || c1 < c0 || c1 > p.T || (r == 0 && c0 != 0);
+    q.n = q.off ? 0 : c1 - c0;
     const long long room = (long long)p.max_pages << p.log2_ps;
     q.bad = q.L < 0 || (long long)q.L + q.n > min(room, (long long)INT_MAX - 2 * kBN);
     if (q.bad) q.L = 0;
@@ -161,9 +164,9 @@ struct Walk {
     int r, h, x;      // request, KV head, pair
     long long cu, c;  // the unit's first cost, the next cost
     Req q;
-    __device__ void start(const ChunkParams &p, int r0, long long base) {
+    __device__ void start(const ChunkParams &p, int r0, const Req &req, long long base) {
         r = r0;
-        q = load_req(p, r);
+        q = req;
         const long long rel = c - base;
         h = (int)divide(rel, q.head);
         const long long in = rel - h * q.head;
@@ -327,6 +330,7 @@ struct CSched {
     long long wsum[12];
     long long c0, c1, base;
     Shares sh;
+    Req req;               // request r0's
 };
 static_assert(sizeof(CSched) <= 256, "the schedule state has 256 bytes");
 
@@ -410,11 +414,11 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
         // offsets that do not run up from 0 to at most T: no row is anybody's
         bool wrong = false;
         long long sum = 0;
+        Req mine;  // the thread's last request
         for (int r = i0; r < i1; ++r) {
-            const int o0 = __ldg(prm.cu + r), o1 = __ldg(prm.cu + r + 1);
-            const bool off = o1 < o0 || o0 < 0 || (r == 0 && o0 != 0) || o1 > prm.T;
-            wrong |= off;
-            if (!off) sum += load_req(prm, r).head * prm.Hkv;
+            mine = load_req(prm, r);
+            wrong |= mine.off;
+            sum += mine.head * prm.Hkv;
         }
         long long inc = sum;
 #pragma unroll
@@ -439,10 +443,12 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
         long long at = wex + inc - sum;
         if (c0 < c1 && at <= c0 && c0 < at + sum) {
             for (int r = i0; r < i1; ++r) {
-                const long long cost = load_req(prm, r).head * prm.Hkv;
+                if (per > 1) mine = load_req(prm, r);
+                const long long cost = mine.head * prm.Hkv;
                 if (at <= c0 && c0 < at + cost) {
                     sch->r0 = r;
                     sch->base = at;
+                    sch->req = mine;
                 }
                 at += cost;
             }
@@ -477,7 +483,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
             const long long c1 = sch->c1;
             Walk walk;
             walk.c = sch->c0;
-            if (is_k && walk.c < c1) walk.start(prm, sch->r0, sch->base);
+            if (is_k && walk.c < c1) walk.start(prm, sch->r0, sch->req, sch->base);
             int st = 0;
             uint32_t ph = 1;
             long g = 0;
@@ -1033,10 +1039,15 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
         if (m != 0) np = k0 + __ffs(m);  // pieces: this CTA's and those up to that one
     }
     auto slot = [&](int i) { return ((long)(b + i) * 2 + (i == 0 ? 1 : 0)) * 2 * kRows + row; };
+    // lane `sub` of a row reads the log2-sum-exps of pieces sub, sub + 8, ..
+    auto lse_of = [&](int i) {
+        return real && i < np ? __ldcg(prm.slot_lse + slot(i)) : -INFINITY;
+    };
+    const float first = lse_of(sub);
     float mx = -INFINITY;
     bool hit = false, nan = false;
     for (int i = sub; i < np; i += 8) {
-        const float v = real ? __ldcg(prm.slot_lse + slot(i)) : -INFINITY;
+        const float v = i == sub ? first : lse_of(i);
         hit |= v == INFINITY;
         nan |= isnan(v);
         mx = fmaxf(mx, v);
@@ -1047,18 +1058,19 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
         hit |= __shfl_xor_sync(0xffffffffu, (int)hit, o) != 0;
         nan |= __shfl_xor_sync(0xffffffffu, (int)nan, o) != 0;
     }
-    if (!real) return;
     constexpr int W = D / 8;  // values a thread
     float acc[W], sum = 0.f;
 #pragma unroll
     for (int c = 0; c < W; ++c) acc[c] = 0.f;
-    if (!hit && !nan && mx > -INFINITY) {
-#pragma unroll 2
-        for (int i = 0; i < np; ++i) {
-            const float v = __ldcg(prm.slot_lse + slot(i));
-            if (v == -INFINITY) continue;  // (its o may not have been written)
-            const float w = ex2_approx(v - mx);
-            const float *po = prm.slot_o + slot(i) * D + sub * W;
+    const bool some = real && !hit && !nan && mx > -INFINITY;
+    for (int i0 = 0; i0 < np; i0 += 8) {
+        const float v = i0 == 0 ? first : lse_of(i0 + sub);
+        const float wv = some && v > -INFINITY ? ex2_approx(v - mx) : 0.f;
+#pragma unroll 4
+        for (int j = 0; j < min(8, np - i0); ++j) {
+            const float w = __shfl_sync(0xffffffffu, wv, (lane & ~7) + j);
+            if (w == 0.f) continue;  // (its o may not have been written)
+            const float *po = prm.slot_o + slot(i0 + j) * D + sub * W;
             float ov[W];
 #pragma unroll
             for (int c = 0; c < W; c += 8) ld_cg_v8(po + c, ov + c);
@@ -1067,6 +1079,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
             for (int c = 0; c < W; ++c) acc[c] = fmaf(w, ov[c], acc[c]);
         }
     }
+    if (!real) return;
     const float inv = nan ? NAN : sum > 0.f ? 1.f / sum : 0.f;
     const long at = (long)(d.tok0 + token) * prm.Hq + (long)d.h * prm.G + rr % prm.G;
     uint16_t *po = prm.out + at * D + sub * W;
