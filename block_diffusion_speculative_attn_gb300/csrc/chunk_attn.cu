@@ -261,6 +261,17 @@ __device__ __forceinline__ void fill_work(const ChunkParams &p, const Piece &pc,
     w->bad = pc.bad;
 }
 
+// mbar_wait with the part behind the first try in one place (the instruction caches hold
+// the code of all roles); where many registers are live, mbar_wait itself.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort,
+                                     int32_t *dev_status) {
+    return mbar_wait(bar, parity, abort, dev_status);
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort,
+                                         int32_t *dev_status) {
+    return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort, dev_status);
+}
+
 // 16 consecutive columns of the thread's lane.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];
@@ -490,7 +501,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
             int kq[2] = {0, 0};  // pieces each row tile took part in
             bool ok = true;
             auto wait = [&](int i, uint32_t parity) {
-                ok = ok && mbar_wait(bar(i), parity & 1, abort_flag, prm.dev_status);
+                ok = ok && wait_bar(bar(i), parity & 1, abort_flag, prm.dev_status);
                 ok = __all_sync(0xffffffffu, ok);
                 return ok;
             };
@@ -604,7 +615,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
             uint32_t gt = 0, kt = 0;  // S tiles and pieces of this row tile
             bool ok = true;
             auto wait = [&](int i, uint32_t parity) {
-                ok = ok && mbar_wait(bar(i), parity & 1, abort_flag, prm.dev_status);
+                ok = ok && wait_bar(bar(i), parity & 1, abort_flag, prm.dev_status);
                 ok = __all_sync(0xffffffffu, ok);
             };
             auto commit = [&](int i) {
@@ -752,7 +763,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
         bool ok = true;
         for (uint32_t piece = 0;; ++piece) {
             const int ws = piece % C::NW;
-            ok = mbar_wait(bar(C::WF + ws), (piece / C::NW) & 1, abort_flag, prm.dev_status);
+            ok = wait_bar(bar(C::WF + ws), (piece / C::NW) & 1, abort_flag, prm.dev_status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || works[ws].all == 0) break;
             // (read where it is used: kept in registers across the tiles it costs spills)
@@ -900,7 +911,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
             vs0 %= C::NV;
             // ---- end of the piece: o / l and the log2-sum-exp
             if (n > 0) {
-                ok = mbar_wait(bar(C::OF + t), k & 1, abort_flag, prm.dev_status);
+                ok = wait_bar(bar(C::OF + t), k & 1, abort_flag, prm.dev_status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -920,7 +931,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                     }
                     continue;
                 }
-                ok = mbar_wait(bar(C::MG), halves & 1, abort_flag, prm.dev_status);
+                ok = wait_bar(bar(C::MG), halves & 1, abort_flag, prm.dev_status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -932,7 +943,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, 1)
                 l = l * w0 + o.y * w1;
                 m_used = mm;
             }
-            ok = mbar_wait(bar(C::BK + ws), (piece / C::NW) & 1, abort_flag, prm.dev_status);
+            ok = wait_bar(bar(C::BK + ws), (piece / C::NW) & 1, abort_flag, prm.dev_status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const bool hit = w.bad_key < lim;
