@@ -679,19 +679,20 @@ def token_sample(logits, u=None, *, temperature=None, top_k=None, top_p=None, mi
 
 
 # ---------------------------------------------------------------------------
-def _tokens(t, name: str, index: int, dtype=None):
-    """Token stride (elements) of a [T, heads, D] tensor on CUDA device `index`
-    whose heads are dense."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
+def _tokens(t, name: str, index: int, dtype):
+    """(tokens, heads, D) and token stride (elements) of a [T, heads, D] tensor on
+    CUDA device `index` whose heads are dense."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
         raise ValueError(f"{name} must be a tensor on cuda:{index}")
-    if dtype is not None and t.dtype is not dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have shape [tokens, heads, D], got {tuple(t.shape)}")
-    T, H, D = t.shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have shape [tokens, heads, D], got {tuple(shape)}")
+    T, H, D = shape
+    if (D > 1 and stride[2] != 1) or (H > 1 and stride[1] != D):
         raise ValueError(f"{name} must have dense heads")
-    return t.stride(0) if T > 1 else H * D
+    return shape, stride[0] if T > 1 else H * D
 
 
 def chunk_attn_workspace_bytes(D, sms: int = 0) -> int:
@@ -718,11 +719,11 @@ def chunk_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *, p
     index = block_table.get_device()
     bs, max_pages = block_table.shape
     bf16, i32 = torch.bfloat16, torch.int32
-    stride = _tokens(q, "q", index, bf16)
-    T, Hq, D = q.shape
-    if k_cache.dim() != 3 or k_cache.shape[2] != D:
-        raise ValueError(f"k_cache must have shape [slots, Hkv, {D}], got {tuple(k_cache.shape)}")
-    slots, Hkv = k_cache.shape[0], k_cache.shape[1]
+    (T, Hq, D), stride = _tokens(q, "q", index, bf16)
+    cache = k_cache.shape
+    if len(cache) != 3 or cache[2] != D:
+        raise ValueError(f"k_cache must have shape [slots, Hkv, {D}], got {tuple(cache)}")
+    slots, Hkv = cache[0], cache[1]
     if num_pages is None:
         num_pages = slots // page_size
     elif num_pages * page_size > slots:
@@ -735,8 +736,8 @@ def chunk_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *, p
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     _launch(lib().bdsa_chunk_attn_paged, "bdsa_chunk_attn_paged", index, q.data_ptr(), stride,
-            _arg(k_cache, "k_cache", bf16, (slots, Hkv, D), index),
-            _arg(v_cache, "v_cache", bf16, (slots, Hkv, D), index), block_table.data_ptr(),
+            _arg(k_cache, "k_cache", bf16, cache, index),
+            _arg(v_cache, "v_cache", bf16, cache, index), block_table.data_ptr(),
             max_pages, num_pages, _arg(seq_lens, "seq_lens", i32, (bs,), index),
             _arg(cu_tokens, "cu_tokens", i32, (bs + 1,), index), bs, T, Hq, Hkv, D,
             int(page_size), float(scale), int(mask_block),
@@ -753,16 +754,18 @@ def cache_write(k_new, v_new, slot_map, k_cache, v_cache, *, dev_status=None):
     stride: slices of a fused projection), caches [slots, Hkv, D], one type."""
     _dev(slot_map, "slot_map", torch.int32)
     index, dtype = slot_map.get_device(), k_cache.dtype
-    ks, vs = (_tokens(t, n, index, dtype) for t, n in ((k_new, "k_new"), (v_new, "v_new")))
-    T, H, D = k_new.shape
-    if v_new.shape != k_new.shape or slot_map.shape != (T,):
+    shape, ks = _tokens(k_new, "k_new", index, dtype)
+    shape_v, vs = _tokens(v_new, "v_new", index, dtype)
+    T, H, D = shape
+    if shape_v != shape or slot_map.shape != (T,):
         raise ValueError(f"v_new must have shape {(T, H, D)} and slot_map {(T,)}, got "
-                         f"{tuple(v_new.shape)} and {tuple(slot_map.shape)}")
+                         f"{tuple(shape_v)} and {tuple(slot_map.shape)}")
     slots, e = k_cache.shape[0], k_cache.element_size()
+    cache = (slots, H, D)
     _launch(lib().bdsa_cache_write, "bdsa_cache_write", index, k_new.data_ptr(), ks * e,
             v_new.data_ptr(), vs * e, slot_map.data_ptr(), T,
-            _arg(k_cache, "k_cache", dtype, (slots, H, D), index),
-            _arg(v_cache, "v_cache", dtype, (slots, H, D), index), H * D * e, slots,
+            _arg(k_cache, "k_cache", dtype, cache, index),
+            _arg(v_cache, "v_cache", dtype, cache, index), H * D * e, slots,
             _arg(dev_status, "dev_status", torch.int32, (1,), index))
 
 

@@ -27,13 +27,14 @@
 // TMEM only when a row's max grows by 2^8.
 //
 // What bounds it (us a call, launches in a graph):
-//   64 single tokens over 512-8192 keys of 8 KV heads, pages of 16    196  HBM: 1.23 GB
-//     at 0.93 of the copy rate (one row tile over all key tiles: 283 then)
-//   24 prompts of 17-2048 tokens, 32 heads                            353  1.0 PFLOP/s;
+//   64 single tokens over 512-8192 keys of 8 KV heads, pages of 16    191-195  HBM: 1.23 GB
+//     at 0.93-0.95 of the copy rate (one row tile over all key tiles: 283)
+//   24 prompts of 17-2048 tokens, 32 heads                            340-355  1.0 PFLOP/s;
 //     161 key tiles a CTA of 1.55 us and 26 pieces of about 3 us
-//   8 x 512-1024 tokens in blocks of 32 behind 1024-8192, 16 heads    256  1.29 PFLOP/s
+//   8 x 512-1024 tokens in blocks of 32 behind 1024-8192, 16 heads    250  1.32 PFLOP/s
 //   4096 tokens behind 28672, 32 heads           1410 cool, 1440-1500 call after call at
 //     the power limit: 1.37-1.46 PFLOP/s (0.71-0.76 of the measured rate)
+//   44 single tokens and 4 chunks of 128-512 tokens, 16 heads          59
 // A pair's key tile costs about 1.6 us against 1.3 of MMAs: the exponentials of the two
 // row tiles follow one another (in turns, below), and with the trip from P over PV and
 // the next S they are longer than the other tile's MMAs.  A unit costs about 3 us
