@@ -35,11 +35,13 @@
 //   4096 tokens behind 28672, 32 heads           1410 cool, 1440-1500 call after call at
 //     the power limit: 1.37-1.46 PFLOP/s (0.71-0.76 of the measured rate)
 //   44 single tokens and 4 chunks of 128-512 tokens, 16 heads          59
-// A pair's key tile costs about 1.6 us against 1.3 of MMAs: the exponentials of the two
-// row tiles follow one another (in turns, below), and with the trip from P over PV and
-// the next S they are longer than the other tile's MMAs.  A unit costs about 3 us
-// besides: instructions that run once a unit come from far (code of 127 KB instead of
-// 79: 565 us for the prompts), and O has to leave TMEM before the next unit's PV.
+// A pair's key tile costs 2970 cycles against 2048 of MMAs: a row tile's chain of S, its
+// maximum, the exponentials, P, PV and the next S is longer than the other tile's MMAs.
+// Call after call the GPU is at its power limit (1.37 kW; the long chunk at 1650 MHz,
+// the blocks at 1810, the prompts at 1950), so what saves instructions saves time twice.
+// A unit costs about 3 us besides: instructions that run once a unit come from far
+// (with code of 127 KB instead of 72 the prompts take 565 us), and O has to leave TMEM
+// before the next unit's PV.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
