@@ -9,6 +9,7 @@
 
 #include "../../include/bdsa.h"
 #include "bdsa_internal.h"
+#include "host_checks.h"
 
 namespace bdsa {
 
@@ -29,30 +30,7 @@ int device_num_sms(int requested) {
 
 namespace {
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
-
-// A range of memory a call reads or writes (null: none).
-struct Range {
-    const void *p;
-    int64_t bytes;
-};
-// Whether each of outs is apart from every one of ins and from the other outs.
-bool apart(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
-    auto meet = [](const Range &a, const Range &b) {
-        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-        return a.p && b.p && a.bytes > 0 && b.bytes > 0 &&
-               (x < y ? y - x < (uintptr_t)a.bytes : x - y < (uintptr_t)b.bytes);
-    };
-    for (const Range *o = outs.begin(); o != outs.end(); ++o) {
-        for (const Range &i : ins)
-            if (meet(*o, i)) return false;
-        for (const Range *p = o + 1; p != outs.end(); ++p)
-            if (meet(*o, *p)) return false;
-    }
-    return true;
-}
 
 }  // namespace
 
