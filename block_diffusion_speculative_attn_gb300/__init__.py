@@ -733,8 +733,8 @@ def chunk_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *, p
     if workspace is None:
         workspace = torch.empty(_chunk_workspace(D, sms, index), dtype=torch.uint8,
                                 device=q.device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous memory on cuda:{index}")
     _launch(lib().bdsa_chunk_attn_paged, "bdsa_chunk_attn_paged", index, q.data_ptr(), stride,
             _arg(k_cache, "k_cache", bf16, cache, index),
             _arg(v_cache, "v_cache", bf16, cache, index), block_table.data_ptr(),
@@ -801,8 +801,8 @@ def cache_fork(parent, keep_lens, block_table, owned, free_pages, free_state, *,
     if workspace is None:
         workspace = torch.empty(cache_fork_workspace_bytes(bs, n, num_pages), dtype=torch.uint8,
                                 device=dev)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous memory on cuda:{index}")
     _launch(lib().bdsa_cache_fork, "bdsa_cache_fork", index,
             _arg(parent, "parent", i32, (n,), index),
             _arg(keep_lens, "keep_lens", i32, (n,), index), block_table.data_ptr(),
