@@ -582,6 +582,14 @@ def _arg(t, name: str, dtype, shape, index: int):
     return t.data_ptr()
 
 
+def _int32(x, name: str) -> int:
+    """x as the int32 that the library takes (ctypes would pass on its lower bits)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 TABLE_KEYS = ("owned", "free_state", "cu_tokens", "slot_map", "positions")
 
 
@@ -724,10 +732,12 @@ def chunk_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *, p
     if len(cache) != 3 or cache[2] != D:
         raise ValueError(f"k_cache must have shape [slots, Hkv, {D}], got {tuple(cache)}")
     slots, Hkv = cache[0], cache[1]
+    page_size, sms = _int32(page_size, "page_size"), _int32(sms, "sms")
     if num_pages is None:
         num_pages = slots // page_size
     elif num_pages * page_size > slots:
         raise ValueError(f"the caches hold fewer than {num_pages} pages")
+    num_pages = _int32(num_pages, "num_pages")
     if out is None:
         out = torch.empty((T, Hq, D), dtype=bf16, device=q.device)
     if workspace is None:
@@ -740,7 +750,7 @@ def chunk_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, *, p
             _arg(v_cache, "v_cache", bf16, cache, index), block_table.data_ptr(),
             max_pages, num_pages, _arg(seq_lens, "seq_lens", i32, (bs,), index),
             _arg(cu_tokens, "cu_tokens", i32, (bs + 1,), index), bs, T, Hq, Hkv, D,
-            int(page_size), float(scale), int(mask_block),
+            page_size, float(scale), _int32(mask_block, "mask_block"),
             _arg(out, "out", bf16, (T, Hq, D), index),
             _arg(lse, "lse", torch.float32, (T, Hq), index), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), sms,
@@ -765,8 +775,8 @@ def cache_write(k_new, v_new, slot_map, k_cache, v_cache, *, dev_status=None):
     _launch(lib().bdsa_cache_write, "bdsa_cache_write", index, k_new.data_ptr(), ks * e,
             v_new.data_ptr(), vs * e, slot_map.data_ptr(), T,
             _arg(k_cache, "k_cache", dtype, cache, index),
-            _arg(v_cache, "v_cache", dtype, cache, index), H * D * e, slots,
-            _arg(dev_status, "dev_status", torch.int32, (1,), index))
+            _arg(v_cache, "v_cache", dtype, cache, index), _int32(H * D * e, "a row's bytes"),
+            slots, _arg(dev_status, "dev_status", torch.int32, (1,), index))
 
 
 FORK_KEYS = ("block_table", "owned", "shared", "free_state", "copy_src", "copy_dst", "copy_len")
@@ -806,7 +816,8 @@ def cache_fork(parent, keep_lens, block_table, owned, free_pages, free_state, *,
     _launch(lib().bdsa_cache_fork, "bdsa_cache_fork", index,
             _arg(parent, "parent", i32, (n,), index),
             _arg(keep_lens, "keep_lens", i32, (n,), index), block_table.data_ptr(),
-            _arg(owned, "owned", i32, (bs,), index), max_pages, num_pages, bs, n, int(page_size),
+            _arg(owned, "owned", i32, (bs,), index), max_pages, num_pages, bs, n,
+            _int32(page_size, "page_size"),
             _arg(free_pages, "free_pages", i32, (num_pages,), index),
             _arg(free_state, "free_state", i32, (2,), index), *outs, workspace.data_ptr(),
             workspace.numel() * workspace.element_size(),
@@ -818,6 +829,7 @@ def _caches(caches, page_size: int, index: int):
     """(pointers, number, bytes of a row, pages) of a sequence of [slots, ...]
     tensors alike, or of one stacked tensor [n, slots, ...]."""
     one = isinstance(caches, torch.Tensor)
+    page_size = _int32(page_size, "page_size")
     if one and (caches.dim() < 3 or not caches.is_contiguous()):
         raise ValueError("stacked caches must be a contiguous [n, slots, ...] tensor")
     first = caches if one else caches[0] if len(caches) else None
@@ -835,7 +847,7 @@ def _caches(caches, page_size: int, index: int):
     else:
         n = len(caches)
         at = [_arg(t, "a cache", first.dtype, shape, index) for t in caches]
-    return (ctypes.c_void_p * n)(*at), n, row, shape[0] // int(page_size)
+    return (ctypes.c_void_p * n)(*at), n, row, shape[0] // page_size
 
 
 def cache_copy(caches, copy_src, copy_dst, copy_len, *, page_size: int, dev_status=None):
