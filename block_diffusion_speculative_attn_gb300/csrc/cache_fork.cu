@@ -10,8 +10,8 @@
 // every page, its first entry in the old table (atomic min), the new rows that hold
 // it whole (atomic add) and the first that ends in it (atomic min).  The results of
 // those do not depend on their order, so neither do the tables or the ring.  Four
-// steps, with a warp for each part of a row (kPart entries at least, a whole row where
-// there are many; 16 rows of 8192 pages by whole rows 506 us, in parts 22):
+// steps, with a warp for each part of a row (kPart entries at most, a whole row where
+// there are many rows; 16 rows of 8192 pages by whole rows 506 us, in parts 22):
 //   clear   the scattered arrays
 //   mark    the three scatters
 //   count   pages that each old row gives back, new rows that need a fresh page
@@ -29,11 +29,16 @@ namespace {
 
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr int kForkThreads = 512, kForkCtas = 16;
-// Table entries and pages up to which one cluster takes the call: 64 rows of 64 pages
-// 11.4 us in one cluster, 11.8 in four grids (and three launches more for the host);
-// 256 rows 16 and 12, 512 rows 26 and 13, 2048 rows of 128 pages 114 and 27.
+// Table entries and pages, and parts of rows, up to which one cluster takes the call (a
+// launch instead of four, about 10 us of the host's time): 64 rows of 64 pages 11.4 us
+// in one cluster, 11.8 in four grids; 256 rows 16 and 12, 512 rows 26 and 13, 2048 rows
+// of 128 pages 114 and 27.  Its 256 warps take the parts in turns, however short: 256
+// rows of 4 pages (512 parts) 12.6 and 10.4, 1024 rows of 1 page 30 and 14, 10000 rows
+// 263 and 44.
 constexpr long long kClusterWork = 1 << 15;
-// Entries of a warp's part of a row at least, and parts of a table at most.
+constexpr long long kClusterParts = 1024;
+// Entries of a warp's part of a row at most; more where a table's parts would be more
+// than kMaxParts.
 constexpr int kPart = 128, kMaxParts = BDSA_TABLE_MAX_REQUESTS;
 
 // The part of the work that a warp takes.
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_write_kernel(const ForkArgs
     step_write(a);
 }
 
-// The rows' parts: as many as give a table kMaxParts at most.
+// The rows' parts: as many as kPart asks for, if a table has no more than kMaxParts then.
 int parts_of_row(int bs, int max_pages) {
     const int by_len = (max_pages + kPart - 1) / kPart, most = kMaxParts / (bs > 0 ? bs : 1);
     return by_len < most ? by_len : most < 1 ? 1 : most;
@@ -371,17 +376,8 @@ int launch_cache_fork(ForkArgs a, void *workspace, cudaStream_t stream) {
     const long long rows = (long long)a.bs_in + a.bs_out;
     const long long parts = (long long)a.bs_in * a.parts_in + (long long)a.bs_out * a.parts_out;
     const size_t smem = 4 * ((size_t)a.bs_in * a.parts_in + (size_t)a.bs_out + 2);
-    // past the default 48 KB, on this device; the same limit in every call, so that
-    // host threads do not undo one another's
-    constexpr int kMost = 4 * (2 * BDSA_TABLE_MAX_REQUESTS + 2);
-    auto more = [&](const void *k) {
-        return smem <= 44 * 1024 ||
-               cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) ==
-                   cudaSuccess;
-    };
-    if (rows * a.max_pages + a.num_pages <= kClusterWork) {
-        if (!more((const void *)fork_cluster_kernel) ||
-            cudaFuncSetAttribute((const void *)fork_cluster_kernel,
+    if (parts <= kClusterParts && rows * a.max_pages + a.num_pages <= kClusterWork) {
+        if (cudaFuncSetAttribute((const void *)fork_cluster_kernel,
                                  cudaFuncAttributeNonPortableClusterSizeAllowed,
                                  1) != cudaSuccess)
             return BDSA_CUDA_ERROR;
@@ -402,7 +398,13 @@ int launch_cache_fork(ForkArgs a, void *workspace, cudaStream_t stream) {
                    ? BDSA_OK
                    : BDSA_CUDA_ERROR;
     }
-    if (!more((const void *)fork_write_kernel)) return BDSA_CUDA_ERROR;
+    // past the default 48 KB, on this device; the same limit in every call, so that
+    // host threads do not undo one another's
+    constexpr int kMost = 4 * (2 * BDSA_TABLE_MAX_REQUESTS + 2);
+    if (smem > 44 * 1024 &&
+        cudaFuncSetAttribute((const void *)fork_write_kernel,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess)
+        return BDSA_CUDA_ERROR;
     const unsigned warps = kForkThreads / 32;
     const unsigned by_part = (unsigned)(parts > 0 ? (parts + warps - 1) / warps : 1);
     const unsigned by_page =
