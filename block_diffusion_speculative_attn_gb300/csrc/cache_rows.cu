@@ -116,7 +116,9 @@ __global__ void __launch_bounds__(kThreads)
 // 16 bytes of the row of one cache and reads kMoveRows rows before it writes them, so
 // no two threads meet and none waits for another; where no row lies on another's
 // place (all that move lie past the kept rows' region), several CTAs share a
-// request's rows.  The slots of 32 rows are looked up by the lanes of a warp, one each,
+// request's rows.  Where some do, one CTA a request and column of bytes is left: 4000
+// rows of 16 caches without 100 of them take 557 us for one request (the bytes 38), 916
+// for 16 (604).  The slots of 32 rows are looked up by the lanes of a warp, one each,
 // and passed round.
 constexpr int kMoveThreads = 128;
 // Rows a thread has in flight and CTAs an SM that a call is cut into: 16 chats of 16

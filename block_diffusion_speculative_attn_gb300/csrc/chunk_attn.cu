@@ -31,17 +31,19 @@
 //     at 0.93-0.95 of the copy rate (one row tile over all key tiles: 283)
 //   24 prompts of 17-2048 tokens, 32 heads                            340-355  1.0 PFLOP/s;
 //     161 key tiles a CTA of 1.55 us and 26 pieces of about 3 us
-//   8 x 512-1024 tokens in blocks of 32 behind 1024-8192, 16 heads    250  1.32 PFLOP/s
-//   4096 tokens behind 28672, 32 heads           1410 cool, 1440-1500 call after call at
-//     the power limit: 1.37-1.46 PFLOP/s (0.71-0.76 of the measured rate)
+//   8 x 512-1024 tokens in blocks of 32 behind 1024-8192, 16 heads    241-252  1.31-1.37
+//     PFLOP/s
+//   4096 tokens behind 28672, 32 heads           1410 cool, 1440-1515 call after call at
+//     the power limit: 1.36-1.46 PFLOP/s (0.71-0.76 of the measured rate)
 //   44 single tokens and 4 chunks of 128-512 tokens, 16 heads          59
 // A pair's key tile costs 2970 cycles against 2048 of MMAs: a row tile's chain of S, its
 // maximum, the exponentials, P, PV and the next S is longer than the other tile's MMAs.
-// Call after call the GPU is at its power limit (1.37 kW; the long chunk at 1650 MHz,
-// the blocks at 1810, the prompts at 1950), so what saves instructions saves time twice.
+// Call after call the GPU is at its power limit besides (1.37 kW; the long chunk at 1650
+// MHz, the blocks at 1810, the prompts at 1950); the chain is the larger part: a clock of
+// the long chunk does 0.73 of what one of the library's product does at the same limit.
 // A unit costs about 3 us besides: instructions that run once a unit come from far
-// (with code of 127 KB instead of 72 the prompts take 565 us), and O has to leave TMEM
-// before the next unit's PV.
+// (with code of 127 KB instead of 79 the prompts took 574 us, not 349), and O has to leave
+// TMEM before the next unit's PV.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -64,7 +66,11 @@ constexpr int kRows = 128;      // query rows of a tile
 // its CTAs ended between 45 and 68.
 constexpr int kPairKey = 3, kOneKey = 2;
 constexpr int kUnitCost = 768;
-// A CTA takes at least this cost: two units of one tile.
+// A CTA takes at least this cost, two units of one tile: then a CTA whose whole share lies
+// in one unit has tiles of it (4 at least), as the join takes for granted.  Calls of few
+// short units run on fewer CTAs than they have units, one behind the other (2 requests
+// of 8 tokens and one KV head: both on one CTA, 3-4 us each); other values were not
+// measured.
 constexpr int kMinCost = 2304;
 
 // The unit that a CTA left cut after its first piece.

@@ -678,7 +678,9 @@ int32_t bdsa_token_sample(const void *logits, int32_t dtype, int64_t l_stride_r,
  * A row with a NaN score (a NaN in its query or in a key it sees, a score of +inf)
  * gets NaN; keys it does not see, and cache slots past L_r + n_r, may hold
  * anything, but a NaN or an infinity in the value of a token of the same request
- * can reach rows that do not see it (0 * NaN in its 128-key tile).
+ * can reach rows that do not see it (0 * NaN): those of a row tile (128 / G tokens of
+ * the request, from a multiple of that on) whose last token sees the value's 128-key
+ * tile; it reaches no lse, no other KV head and no other request.
  * Arithmetic as in bdsa_block_attn_paged.  softmax_scale finite and > 0; 1 <= mask_block
  * <= 2^30; D in {64, 128}; G <= 128; page_size a power of two >= 8; q, caches, out
  * 16-byte aligned.  out, lse and workspace must not overlap the inputs or one
